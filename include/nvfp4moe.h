@@ -371,6 +371,181 @@ NVFP4MOE_API int nvfp4moe_router_topk(const uint16_t* x, int32_t T, int32_t H, c
                                       int32_t K, int32_t renormalize, float* logits, int32_t* ids, float* probs,
                                       void* stream);
 
+/* Element types of logits and gradients. */
+enum { NVFP4MOE_F32 = 0, NVFP4MOE_BF16 = 1 };
+
+/* The router's scoring GEMM by itself: logits [T, E] as nvfp4moe_router_topk
+ * computes them (same bits, arguments and requirements), for callers whose
+ * selection is nvfp4moe_router_select. */
+NVFP4MOE_API int nvfp4moe_router_logits(const uint16_t* x, int32_t T, int32_t H, const uint16_t* w_router, int32_t E,
+                                        float* logits, void* stream);
+
+/* Expert selection from router logits: scores, a bias that balances the
+ * experts' load, groups of experts, top-k and weights (host struct). */
+enum { NVFP4MOE_SCORE_SOFTMAX = 0, NVFP4MOE_SCORE_SIGMOID = 1 };
+enum { NVFP4MOE_GROUP_MAX = 0, NVFP4MOE_GROUP_TOP2 = 1 };
+typedef struct {
+    int32_t n_experts;   /* E: 1..1024 */
+    int32_t top_k;       /* K: 1..32, at most top_groups * E / n_groups */
+    int32_t score;       /* NVFP4MOE_SCORE_* */
+    int32_t renormalize; /* 1: weights are divided by their sum over the selection */
+    float scale;         /* finite factor of the weights */
+    int32_t n_groups;    /* groups of E / n_groups consecutive experts: 1..64, a divisor of E */
+    int32_t top_groups;  /* groups that stay: 1..n_groups */
+    int32_t group_score; /* NVFP4MOE_GROUP_* */
+    int32_t logits_type; /* NVFP4MOE_F32 or NVFP4MOE_BF16 */
+} nvfp4moe_select_config;
+
+/* For each token, with its logits l (E of them, the row ld elements after the
+ * previous token's):
+ *   - a logit that is NaN or -inf is unusable and its score is 0; +inf counts
+ *     as the largest finite FP32 value;
+ *   - scores s: softmax over the usable logits, or sigmoid(l);
+ *   - bias (FP32 [E], may be NULL) takes part in the selection only.  An
+ *     expert is available if its logit is usable and its bias neither NaN nor
+ *     -inf (+inf counts as the largest finite value).  It is selected by
+ *     v = s + bias, or without a bias by v = l (the same order);
+ *   - a group's value is the largest v of its available experts (MAX), or the
+ *     sum of its two largest s + bias (TOP2; the one if it has only one).  The
+ *     top_groups groups of largest value stay, ties to the lower group, groups
+ *     without an available expert last;
+ *   - ids: the K experts of largest v in these groups, largest first, ties to
+ *     the lower id.  Where fewer than K are available the others follow by id
+ *     with weight 0, so the ids of a token are always K distinct experts (a
+ *     row that is masked whole gets probabilities of 0);
+ *   - probs: scale * s (renormalize 0), or scale * s / (sum of s over the
+ *     token's available selected experts), computed so that the sum does not
+ *     vanish however negative the logits are.
+ * s and v are formed in FP64, so the choice does not depend on FP32 rounding;
+ * with a bias (or TOP2) values closer than 2^-42 relative count as equal.
+ *   ids [T, K] int32, probs [T, K] FP32: caller-owned outputs
+ * Requirements: ld >= E; logits aligned to their element, ids, probs and bias
+ * to 4 bytes (rows are read four elements at a time where ld and the pointer
+ * allow it).  T == 0 is a no-op.  No workspace, no synchronisation; each
+ * token's result depends on its own row only. */
+NVFP4MOE_API int nvfp4moe_router_select(const nvfp4moe_select_config* cfg, const void* logits, int64_t ld, int64_t T,
+                                        const float* bias, int32_t* ids, float* probs, void* stream);
+
+/* The gradient of nvfp4moe_router_select's probs with respect to the logits:
+ * dlogits [T, E] (logits' type, rows ld_out apart, caller-owned, every element
+ * written) from dprobs [T, K] FP32, which nvfp4moe_moe_expert_backward
+ * returns.  cfg, logits and bias are the forward's and ids its output; the
+ * choice itself and the bias get no gradient, and neither does a slot of
+ * weight 0 or one whose id lies outside [0, E).  An id that a token lists
+ * twice gets the sum of its slots' gradients.  With w the weights before the
+ * scale:
+ *   softmax, renormalize 1   scale w_k (dp_k - sum_j w_j dp_j) at the ids
+ *   sigmoid, renormalize 1   the same times (1 - sigmoid(l_k))
+ *   sigmoid, renormalize 0   scale w_k (1 - w_k) dp_k at the ids
+ *   softmax, renormalize 0   scale s_e ([e selected] dp_e - sum_j w_j dp_j) at every expert
+ * dlogits may not overlap the inputs.  Errors and requirements as for the
+ * forward (n_groups, top_groups and group_score are checked and not used). */
+NVFP4MOE_API int nvfp4moe_router_select_backward(const nvfp4moe_select_config* cfg, const void* logits, int64_t ld, int64_t T,
+                                                 const float* bias, const int32_t* ids, const float* dprobs, void* dlogits,
+                                                 int64_t ld_out, void* stream);
+
+/* MXFP4, the OCP microscaled 4-bit format: E2M1 elements with one E8M0 (power
+ * of two) scale per block of 32 along the row and no outer scale.  Its
+ * products run on the scaled FP4 matrix instruction, which takes these
+ * operands undecoded; NVFP4's E4M3 scales do not fit it.
+ *
+ * Quantization of a block with largest magnitude m: FLOOR (the OCP rule) takes
+ * the scale 2^k with k = floor(log2 m) - 2, RU the smallest k with
+ * m <= 6 * 2^k; k >= -127; the scale byte is k + 127 (0 for a zero block).
+ * Each element is the E2M1 value nearest to x / 2^k, ties to the even code,
+ * saturating at 6 (FLOOR can clip up to a quarter of the largest element),
+ * with x's sign.  A block that holds an Inf or NaN gets the scale byte 255
+ * (NaN) and codes 0: its values, and products with them, are NaN. */
+enum { NVFP4MOE_MXFP4_SCALE_FLOOR = 0, NVFP4MOE_MXFP4_SCALE_RU = 1 };
+
+/* n_mats MXFP4 matrices [rows, cols], stacked (host struct, device pointers).
+ * cols is a multiple of 32.
+ * NVFP4_LAYOUT_LOGICAL: codes [n_mats*rows][cols/2], element 2i in the low
+ *   nibble of byte i; scales [n_mats*rows][cols/32].
+ * NVFP4_LAYOUT_GEMM: the products' weight operand.  Each matrix is padded with
+ *   zeros to whole tiles of 16 rows x 128 columns (RT = ceil(rows/16) by
+ *   C = ceil(cols/128), Q = ceil(C/4)); for row r (rt = r/16, rl = r%16) of
+ *   matrix m and column k (c = k/128, q = k%128/32), with t = m*RT + rt:
+ *     code byte  = (t*C + c)*1024 + (q*16 + rl)*16 + (k%32)/2
+ *     scale byte = (t*Q + c/4)*256 + (q*16 + rl)*4 + c%4 */
+typedef struct {
+    uint8_t* codes;
+    uint8_t* scales;
+    int32_t n_mats;
+    int32_t rows;
+    int32_t cols;
+    int32_t layout; /* NVFP4_LAYOUT_* */
+} nvfp4moe_mxfp4_tensor;
+
+/* Bytes of the two planes of such a tensor (q's pointers are not read). */
+NVFP4MOE_API int nvfp4moe_mxfp4_bytes(const nvfp4moe_mxfp4_tensor* q, size_t* codes_bytes, size_t* scales_bytes);
+
+/* x [n_mats*rows, cols] BF16 (rows ld elements apart) -> q's planes, and back
+ * (exactly: every MXFP4 value is a BF16 number; out's rows are ld apart).
+ * Requirements: x / out 16-byte aligned, ld >= cols and a multiple of 8, codes
+ * 16-byte aligned (scales 4-byte in the GEMM layout), n_mats*rows*cols < 2^34.
+ * Zero rows or matrices are a no-op.  No synchronisation. */
+NVFP4MOE_API int nvfp4moe_mxfp4_quantize(const uint16_t* x, int64_t ld, const nvfp4moe_mxfp4_tensor* q, int32_t scale_round,
+                                         void* stream);
+NVFP4MOE_API int nvfp4moe_mxfp4_dequantize(const nvfp4moe_mxfp4_tensor* q, uint16_t* out, int64_t ld, void* stream);
+
+/* Dense MXFP4 linear: out [M, N] = bf16(Q(x) . Wq^T), with x [M, K] BF16 (rows
+ * ldx apart) quantized into the workspace by scale_round, Wq one GEMM-layout
+ * matrix [N, K] and FP32 accumulation.  M >= 0, K % 32 == 0, any N.
+ * Requirements: x 16-byte aligned, ldx >= K and a multiple of 8; out aligned to
+ * 2 bytes, ld_out >= N (8-byte stores where out, ld_out and N allow them);
+ * workspace 256-byte aligned, nvfp4moe_mxfp4_workspace_bytes(M, K, 1) bytes.
+ * Each output row depends on its own x row only, with the same bits in every
+ * batch (one order over K, no split-K).  M == 0 is a no-op; no
+ * synchronisation.
+ *
+ * The experts' products: x [R, K] holds the experts' rows one expert after
+ * another, expert e's in [offsets[e], offsets[e+1]) (device int32, E + 1 of
+ * them, E = Wq->n_mats <= 1024), and out[r] = bf16(Q(x[r]) . Wq[e]^T).  An
+ * expert may have no rows; rows before offsets[0] and from offsets[E] on are
+ * left as they were.  Offsets outside [0, R] are taken as the nearer end and a
+ * decreasing one as its predecessor.  The grid depends on R and E only.
+ * Workspace: nvfp4moe_mxfp4_workspace_bytes(R, K, E) bytes. */
+NVFP4MOE_API size_t nvfp4moe_mxfp4_workspace_bytes(int64_t M, int64_t K, int64_t n_mats);
+NVFP4MOE_API int nvfp4moe_mxfp4_linear(const uint16_t* x, int64_t M, int64_t ldx, const nvfp4moe_mxfp4_tensor* Wq,
+                                       uint16_t* out, int64_t ld_out, int32_t scale_round, void* workspace,
+                                       size_t workspace_bytes, void* stream);
+NVFP4MOE_API int nvfp4moe_mxfp4_grouped_linear(const uint16_t* x, int64_t R, int64_t ldx, const int32_t* offsets,
+                                               const nvfp4moe_mxfp4_tensor* Wq, uint16_t* out, int64_t ld_out,
+                                               int32_t scale_round, void* workspace, size_t workspace_bytes, void* stream);
+
+/* Clipping of gradients by their global norm, the end of a training step whose
+ * weight gradients nvfp4moe_moe_expert_backward gives.
+ *   norm = sqrt(sum of the squares of all elements of all tensors), in FP64
+ *   out  = in * (max_norm / norm) if norm > max_norm, else in
+ * the product taken in FP64 and rounded to FP32 (then to BF16 in BF16
+ * tensors).  If any element is Inf or NaN, norm is not finite and the
+ * gradients are left as they are (out = in), so that the caller can skip the
+ * step.  The norm has the same bits in every run of one plan.
+ *
+ * The tensors are given once, as a plan: nvfp4moe_grad_plan writes a table of
+ * n_chunks entries for n_grads tensors (host array) into host memory, which
+ * the caller copies to the device and may use as long as the tensors stay
+ * where they are.  in and out of a tensor are the same address (in place) or
+ * disjoint; no output may overlap another tensor (NVFP4_E_ARG).  Tensors of 0
+ * elements are allowed.  Each is contiguous and aligned to its element. */
+typedef struct {
+    const void* in;
+    void* out;
+    int64_t n;    /* elements */
+    int32_t type; /* NVFP4MOE_F32 or NVFP4MOE_BF16 */
+} nvfp4moe_grad;
+NVFP4MOE_API int nvfp4moe_grad_plan_bytes(const nvfp4moe_grad* grads, int32_t n_grads, size_t* bytes, int64_t* n_chunks);
+NVFP4MOE_API int nvfp4moe_grad_plan(const nvfp4moe_grad* grads, int32_t n_grads, void* plan_host, size_t plan_bytes);
+
+/* plan: device copy of the table (8-byte aligned, n_chunks entries; may be
+ * NULL if there are none); max_norm >= 0, +inf to take the norm only;
+ * norm_out: device double; workspace: nvfp4moe_clip_workspace_bytes() bytes,
+ * 8-byte aligned.  No synchronisation. */
+NVFP4MOE_API size_t nvfp4moe_clip_workspace_bytes(void);
+NVFP4MOE_API int nvfp4moe_clip_grad_norm(const void* plan, int64_t n_chunks, double max_norm, double* norm_out,
+                                         void* workspace, size_t workspace_bytes, void* stream);
+
 /* Dense NVFP4 linear (miniTE page, "how it differs": the NVFP4 linear with a
  * per-token outer scale g^x and a per-weight-row g^w, whose FP32 epilogue
  * multiplies the FP32 accumulator by g^x * g^w and casts to BF16; "how to

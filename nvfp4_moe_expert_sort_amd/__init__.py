@@ -22,6 +22,14 @@ SCALE_RU = 0
 SCALE_RNE = 1
 LAYOUT_LOGICAL = 0
 LAYOUT_GEMM = 1
+F32 = 0
+BF16 = 1
+SCORE_SOFTMAX = 0
+SCORE_SIGMOID = 1
+GROUP_MAX = 0
+GROUP_TOP2 = 1
+MXFP4_SCALE_FLOOR = 0
+MXFP4_SCALE_RU = 1
 
 # Every function the C header declares (checked against the header by the tests).
 EXPORTS = ["nvfp4_status_str", "nvfp4_quantize", "nvfp4moe_weight_bytes", "nvfp4moe_quantize_weights",
@@ -31,7 +39,11 @@ EXPORTS = ["nvfp4_status_str", "nvfp4_quantize", "nvfp4moe_weight_bytes", "nvfp4
            "nvfp4moe_moe_expert_forward_masked", "nvfp4moe_moe_expert_forward_unfused",
            "nvfp4moe_moe_expert_forward_noalloc", "nvfp4moe_backward_workspace_bytes", "nvfp4moe_moe_expert_backward",
            "nvfp4moe_moe_expert_forward_w4a16", "nvfp4moe_moe_expert_forward_online", "nvfp4moe_router_topk", "nvfp4_linear_workspace_bytes", "nvfp4_linear",
-           "nvfp4moe_selftest_batch_invariance"]
+           "nvfp4moe_selftest_batch_invariance", "nvfp4moe_router_logits", "nvfp4moe_router_select",
+           "nvfp4moe_router_select_backward", "nvfp4moe_mxfp4_bytes", "nvfp4moe_mxfp4_quantize",
+           "nvfp4moe_mxfp4_dequantize", "nvfp4moe_mxfp4_workspace_bytes", "nvfp4moe_mxfp4_linear",
+           "nvfp4moe_mxfp4_grouped_linear", "nvfp4moe_grad_plan_bytes", "nvfp4moe_grad_plan",
+           "nvfp4moe_clip_workspace_bytes", "nvfp4moe_clip_grad_norm"]
 
 
 class Nvfp4Error(RuntimeError):
@@ -58,6 +70,21 @@ class WsLayout(ctypes.Structure):
                [("rows_cap", ctypes.c_int64), ("m_align", ctypes.c_int32), ("n_part", ctypes.c_int32)]
 
 
+class SelectConfig(ctypes.Structure):
+    _fields_ = [("n_experts", ctypes.c_int32), ("top_k", ctypes.c_int32), ("score", ctypes.c_int32),
+                ("renormalize", ctypes.c_int32), ("scale", ctypes.c_float), ("n_groups", ctypes.c_int32),
+                ("top_groups", ctypes.c_int32), ("group_score", ctypes.c_int32), ("logits_type", ctypes.c_int32)]
+
+
+class Mxfp4Tensor(ctypes.Structure):
+    _fields_ = [("codes", ctypes.c_void_p), ("scales", ctypes.c_void_p), ("n_mats", ctypes.c_int32),
+                ("rows", ctypes.c_int32), ("cols", ctypes.c_int32), ("layout", ctypes.c_int32)]
+
+
+class Grad(ctypes.Structure):
+    _fields_ = [("in_", ctypes.c_void_p), ("out", ctypes.c_void_p), ("n", ctypes.c_int64), ("type", ctypes.c_int32)]
+
+
 _lib = None
 
 
@@ -71,6 +98,8 @@ def lib():
     L = ctypes.CDLL(LIB_PATH)
     vp, i32, i64, sz = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_size_t
     cfgp, qtp = ctypes.POINTER(Config), ctypes.POINTER(QTensor)
+    selp, mxp, gradp = ctypes.POINTER(SelectConfig), ctypes.POINTER(Mxfp4Tensor), ctypes.POINTER(Grad)
+    szp, i64p = ctypes.POINTER(sz), ctypes.POINTER(i64)
     sig = {
         "nvfp4_status_str": (ctypes.c_char_p, [ctypes.c_int]),
         "nvfp4_quantize": (ctypes.c_int, [vp, i64, i64, i64, vp, vp, vp, i32, i32, vp]),
@@ -98,6 +127,19 @@ def lib():
         "nvfp4_linear": (ctypes.c_int, [vp, i64, i64, qtp, vp, i32, vp, sz, vp]),
         "nvfp4moe_selftest_batch_invariance": (ctypes.c_int, [cfgp, qtp, qtp, ctypes.c_uint64, i32, i32, i32,
                                                               ctypes.POINTER(i64), vp]),
+        "nvfp4moe_router_logits": (ctypes.c_int, [vp, i32, i32, vp, i32, vp, vp]),
+        "nvfp4moe_router_select": (ctypes.c_int, [selp, vp, i64, i64, vp, vp, vp, vp]),
+        "nvfp4moe_router_select_backward": (ctypes.c_int, [selp, vp, i64, i64, vp, vp, vp, vp, i64, vp]),
+        "nvfp4moe_mxfp4_bytes": (ctypes.c_int, [mxp, szp, szp]),
+        "nvfp4moe_mxfp4_quantize": (ctypes.c_int, [vp, i64, mxp, i32, vp]),
+        "nvfp4moe_mxfp4_dequantize": (ctypes.c_int, [mxp, vp, i64, vp]),
+        "nvfp4moe_mxfp4_workspace_bytes": (sz, [i64, i64, i64]),
+        "nvfp4moe_mxfp4_linear": (ctypes.c_int, [vp, i64, i64, mxp, vp, i64, i32, vp, sz, vp]),
+        "nvfp4moe_mxfp4_grouped_linear": (ctypes.c_int, [vp, i64, i64, vp, mxp, vp, i64, i32, vp, sz, vp]),
+        "nvfp4moe_grad_plan_bytes": (ctypes.c_int, [gradp, i32, szp, i64p]),
+        "nvfp4moe_grad_plan": (ctypes.c_int, [gradp, i32, vp, sz]),
+        "nvfp4moe_clip_workspace_bytes": (sz, []),
+        "nvfp4moe_clip_grad_norm": (ctypes.c_int, [vp, i64, ctypes.c_double, vp, vp, sz, vp]),
     }
     for name, (res, args) in sig.items():
         f = getattr(L, name)
@@ -394,3 +436,269 @@ def selftest_batch_invariance(cfg: Config, weights: QuantWeights, seed: int, n_p
                                                   ctypes.byref(weights.W2q), seed, n_probe, max_decode_batch,
                                                   prefill_tokens, rep, _stream(stream))
     return st, dict(n_compared=rep[0], n_mismatched=rep[1], first_bad_probe=rep[2], first_bad_batch=rep[3])
+
+
+# --- expert selection, MXFP4 products, gradient clipping -------------------------------------------
+
+class _At:
+    """The device of `t` made current, and `stream` (default: that device's current one) made its current
+    stream, so that outputs are allocated where they are used.  Gives the stream's handle."""
+
+    def __init__(self, t, stream):
+        import torch
+        if not t.is_cuda:
+            raise ValueError(f"a GPU tensor is needed, got one on {t.device}")
+        if stream is not None and stream.device != t.device:
+            raise ValueError(f"the stream is on {stream.device}, the tensors on {t.device}")
+        self.torch, self.device, self.stream, self.inside = torch, t.device, stream, []
+
+    def __enter__(self):
+        cuda = self.torch.cuda
+        if self.device.index != cuda.current_device():
+            self.inside.append(cuda.device(self.device))
+            self.inside[-1].__enter__()
+        if self.stream is not None:
+            self.inside.append(cuda.stream(self.stream))
+            self.inside[-1].__enter__()
+        return ctypes.c_void_p(cuda.current_stream().cuda_stream)
+
+    def __exit__(self, *exc):
+        for c in reversed(self.inside):
+            c.__exit__(*exc)
+
+
+def _need(where, t, name, dtypes, shape, like, contiguous=True):
+    """ValueError unless t has one of the types, the shape and like's device, with rows of consecutive elements."""
+    if t.dtype not in dtypes or tuple(t.shape) != tuple(shape) or t.device != like.device:
+        raise ValueError(f"{where}: {name} must be {' or '.join(str(d) for d in dtypes)} of shape {tuple(shape)} on "
+                         f"{like.device}, got {t.dtype} {tuple(t.shape)} on {t.device}")
+    if not (t.is_contiguous() if contiguous else t.numel() == 0 or t.shape[-1] == 1 or t.stride(-1) == 1):
+        raise ValueError(f"{where}: {name} must {'be contiguous' if contiguous else 'have consecutive columns'}")
+
+
+def _ld(t):
+    """Elements from one row of a matrix to the next."""
+    return t.stride(0) if t.shape[0] > 1 else max(t.stride(0), t.shape[1])
+
+
+def _bf16_types():
+    import torch
+    return (torch.bfloat16, torch.int16, torch.uint16)
+
+
+def router_logits(x, w_router, out=None, stream=None):
+    """nvfp4moe_router_logits: x [T,H] BF16, w_router [E,H] BF16 -> logits [T,E] f32 (router_topk's)."""
+    import torch
+    T, H = x.shape
+    E = w_router.shape[0]
+    _need("router_logits", x, "x", _bf16_types(), (T, H), x)
+    _need("router_logits", w_router, "w_router", _bf16_types(), (E, H), x)
+    with _At(x, stream) as s:
+        if out is None:
+            out = torch.empty((T, E), dtype=torch.float32, device=x.device)
+        _need("router_logits", out, "out", (torch.float32,), (T, E), x)
+        _check(lib().nvfp4moe_router_logits(_ptr(x), T, H, _ptr(w_router), E, _ptr(out), s), "nvfp4moe_router_logits")
+    return out
+
+
+def _select_config(where, logits, k, bias, score, renormalize, scale, n_groups, top_groups, group_score):
+    import torch
+    T, E = logits.shape
+    _need(where, logits, "logits", (torch.float32, torch.bfloat16), (T, E), logits, contiguous=False)
+    if bias is not None:
+        _need(where, bias, "bias", (torch.float32,), (E,), logits)
+    return SelectConfig(E, k, score, 1 if renormalize else 0, scale, n_groups, top_groups, group_score,
+                        BF16 if logits.dtype == torch.bfloat16 else F32)
+
+
+def router_select(logits, k: int, bias=None, score: int = SCORE_SOFTMAX, renormalize: bool = True, scale: float = 1.0,
+                  n_groups: int = 1, top_groups: int = 1, group_score: int = GROUP_MAX, out=None, stream=None):
+    """nvfp4moe_router_select: logits [T,E] f32 or bf16 (rows may be strided), bias [E] f32 -> (ids [T,k] int32,
+    probs [T,k] f32); `out` may hold the two, preallocated."""
+    import torch
+    cfg = _select_config("router_select", logits, k, bias, score, renormalize, scale, n_groups, top_groups, group_score)
+    T = logits.shape[0]
+    with _At(logits, stream) as s:
+        if out is None:
+            out = (torch.empty((T, max(k, 0)), dtype=torch.int32, device=logits.device),
+                   torch.empty((T, max(k, 0)), dtype=torch.float32, device=logits.device))
+        ids, probs = out
+        _need("router_select", ids, "out ids", (torch.int32,), (T, k), logits)
+        _need("router_select", probs, "out probs", (torch.float32,), (T, k), logits)
+        _check(lib().nvfp4moe_router_select(ctypes.byref(cfg), _ptr(logits), _ld(logits), T, _ptr(bias), _ptr(ids),
+                                            _ptr(probs), s), "nvfp4moe_router_select")
+    return ids, probs
+
+
+def router_select_backward(logits, ids, dprobs, bias=None, score: int = SCORE_SOFTMAX, renormalize: bool = True,
+                           scale: float = 1.0, out=None, stream=None):
+    """nvfp4moe_router_select_backward: router_select's logits, bias and ids, and dprobs [T,k] f32 -> dlogits [T,E]
+    of the logits' type."""
+    import torch
+    T, k = ids.shape
+    cfg = _select_config("router_select_backward", logits, k, bias, score, renormalize, scale, 1, 1, GROUP_MAX)
+    _need("router_select_backward", ids, "ids", (torch.int32,), (logits.shape[0], k), logits)
+    _need("router_select_backward", dprobs, "dprobs", (torch.float32,), (T, k), logits)
+    with _At(logits, stream) as s:
+        if out is None:
+            out = torch.empty(tuple(logits.shape), dtype=logits.dtype, device=logits.device)
+        _need("router_select_backward", out, "out", (logits.dtype,), logits.shape, logits, contiguous=False)
+        _check(lib().nvfp4moe_router_select_backward(ctypes.byref(cfg), _ptr(logits), _ld(logits), T, _ptr(bias),
+                                                     _ptr(ids), _ptr(dprobs), _ptr(out), _ld(out), s),
+               "nvfp4moe_router_select_backward")
+    return out
+
+
+def mxfp4_quantize(x, scale_round: int = MXFP4_SCALE_FLOOR, out=None, stream=None):
+    """nvfp4moe_mxfp4_quantize, logical layout: x [rows, cols] BF16 (rows may be strided) -> (codes [rows, cols/2]
+    uint8, scales [rows, cols/32] uint8)."""
+    import torch
+    rows, cols = x.shape
+    _need("mxfp4_quantize", x, "x", _bf16_types(), (rows, cols), x, contiguous=False)
+    with _At(x, stream) as s:
+        if out is None:
+            out = (torch.empty((rows, cols // 2), dtype=torch.uint8, device=x.device),
+                   torch.empty((rows, cols // 32), dtype=torch.uint8, device=x.device))
+        codes, scales = out
+        _need("mxfp4_quantize", codes, "out codes", (torch.uint8,), (rows, cols // 2), x)
+        _need("mxfp4_quantize", scales, "out scales", (torch.uint8,), (rows, cols // 32), x)
+        q = Mxfp4Tensor(codes.data_ptr(), scales.data_ptr(), 1, rows, cols, LAYOUT_LOGICAL)
+        _check(lib().nvfp4moe_mxfp4_quantize(_ptr(x), _ld(x), ctypes.byref(q), scale_round, s), "nvfp4moe_mxfp4_quantize")
+    return codes, scales
+
+
+def mxfp4_dequantize(codes, scales, out=None, stream=None):
+    """nvfp4moe_mxfp4_dequantize, logical layout: codes [rows, cols/2], scales [rows, cols/32] uint8 -> [rows, cols]
+    bfloat16."""
+    import torch
+    rows, cols = codes.shape[0], 2 * codes.shape[1]
+    _need("mxfp4_dequantize", codes, "codes", (torch.uint8,), (rows, cols // 2), codes)
+    _need("mxfp4_dequantize", scales, "scales", (torch.uint8,), (rows, cols // 32), codes)
+    with _At(codes, stream) as s:
+        if out is None:
+            out = torch.empty((rows, cols), dtype=torch.bfloat16, device=codes.device)
+        _need("mxfp4_dequantize", out, "out", _bf16_types(), (rows, cols), codes, contiguous=False)
+        q = Mxfp4Tensor(codes.data_ptr(), scales.data_ptr(), 1, rows, cols, LAYOUT_LOGICAL)
+        _check(lib().nvfp4moe_mxfp4_dequantize(ctypes.byref(q), _ptr(out), _ld(out), s), "nvfp4moe_mxfp4_dequantize")
+    return out
+
+
+class Mxfp4Weights:
+    """Caller-owned MXFP4 weights of n_mats matrices [rows, cols], in the products' layout."""
+
+    def __init__(self, n_mats: int, rows: int, cols: int, device="cuda"):
+        import torch
+        self.shape = (n_mats, rows, cols)
+        q = Mxfp4Tensor(None, None, n_mats, rows, cols, LAYOUT_GEMM)
+        nc, ns = ctypes.c_size_t(), ctypes.c_size_t()
+        _check(lib().nvfp4moe_mxfp4_bytes(ctypes.byref(q), ctypes.byref(nc), ctypes.byref(ns)), "nvfp4moe_mxfp4_bytes")
+        self.codes = torch.empty((nc.value,), dtype=torch.uint8, device=device)
+        self.scales = torch.empty((ns.value,), dtype=torch.uint8, device=device)
+        self.Wq = Mxfp4Tensor(self.codes.data_ptr(), self.scales.data_ptr(), n_mats, rows, cols, LAYOUT_GEMM)
+
+    def quantize_from(self, w, scale_round: int = MXFP4_SCALE_FLOOR, stream=None):
+        """nvfp4moe_mxfp4_quantize: BF16 w [n_mats, rows, cols] -> these buffers, in place."""
+        _need("Mxfp4Weights.quantize_from", w, "w", _bf16_types(), self.shape, self.codes)
+        with _At(w, stream) as s:
+            _check(lib().nvfp4moe_mxfp4_quantize(_ptr(w), self.shape[2], ctypes.byref(self.Wq), scale_round, s),
+                   "nvfp4moe_mxfp4_quantize")
+        return self
+
+    def dequantize(self, stream=None):
+        """nvfp4moe_mxfp4_dequantize: the values, [n_mats, rows, cols] bfloat16."""
+        import torch
+        with _At(self.codes, stream) as s:
+            out = torch.empty(self.shape, dtype=torch.bfloat16, device=self.codes.device)
+            _check(lib().nvfp4moe_mxfp4_dequantize(ctypes.byref(self.Wq), _ptr(out), self.shape[2], s),
+                   "nvfp4moe_mxfp4_dequantize")
+        return out
+
+
+def mxfp4_workspace_bytes(M: int, K: int, n_mats: int = 1) -> int:
+    n = lib().nvfp4moe_mxfp4_workspace_bytes(M, K, n_mats)
+    if n == 0:
+        raise Nvfp4Error(2, "nvfp4moe_mxfp4_workspace_bytes")
+    return n
+
+
+def mxfp4_alloc_workspace(M: int, K: int, n_mats: int = 1, device="cuda"):
+    import torch
+    return torch.empty((mxfp4_workspace_bytes(M, K, n_mats),), dtype=torch.uint8, device=device)
+
+
+def _mxfp4_product(where, x, offsets, W, scale_round, workspace, out, stream):
+    import torch
+    M, K = x.shape
+    E, N, cols = W.shape
+    _need(where, x, "x", _bf16_types(), (M, cols), W.codes, contiguous=False)
+    if offsets is not None:
+        _need(where, offsets, "offsets", (torch.int32,), (E + 1,), x)
+    with _At(x, stream) as s:
+        if out is None:
+            out = torch.empty((M, N), dtype=x.dtype, device=x.device)
+        _need(where, out, "out", _bf16_types(), (M, N), x, contiguous=False)
+        if workspace is None:
+            workspace = mxfp4_alloc_workspace(M, K, E, x.device)
+        _need(where, workspace, "workspace", (torch.uint8,), workspace.shape, x)
+        a = (ctypes.byref(W.Wq), _ptr(out), _ld(out), scale_round, _ptr(workspace), workspace.numel(), s)
+        if offsets is None:
+            _check(lib().nvfp4moe_mxfp4_linear(_ptr(x), M, _ld(x), *a), "nvfp4moe_mxfp4_linear")
+        else:
+            _check(lib().nvfp4moe_mxfp4_grouped_linear(_ptr(x), M, _ld(x), _ptr(offsets), *a),
+                   "nvfp4moe_mxfp4_grouped_linear")
+    return out
+
+
+def mxfp4_linear(x, W: Mxfp4Weights, scale_round: int = MXFP4_SCALE_FLOOR, workspace=None, out=None, stream=None):
+    """nvfp4moe_mxfp4_linear: x [M,K] BF16 (rows may be strided), W one [N,K] matrix -> out [M,N] BF16.
+    `workspace` (mxfp4_alloc_workspace) may be shared by calls that follow each other on one stream."""
+    return _mxfp4_product("mxfp4_linear", x, None, W, scale_round, workspace, out, stream)
+
+
+def mxfp4_grouped_linear(x, offsets, W: Mxfp4Weights, scale_round: int = MXFP4_SCALE_FLOOR, workspace=None, out=None,
+                         stream=None):
+    """nvfp4moe_mxfp4_grouped_linear: x [R,K] BF16 with expert e's rows in [offsets[e], offsets[e+1]) (int32, on the
+    GPU), W of E matrices [N,K] -> out [R,N] BF16; rows outside the offsets are not written."""
+    return _mxfp4_product("mxfp4_grouped_linear", x, offsets, W, scale_round, workspace, out, stream)
+
+
+class GradSet:
+    """The tensors that clip_grad_norm works on: FP32 or BF16, contiguous, on one GPU.  `out` (default: in place)
+    receives the clipped ones.  Holds the tensors and their plan on the GPU; make a new one if they move."""
+
+    def __init__(self, grads, out=None):
+        import torch
+        self.grads = list(grads)
+        self.out = self.grads if out is None else list(out)
+        if not self.grads or len(self.out) != len(self.grads):
+            raise ValueError("GradSet: needs at least one gradient, and an output for each")
+        self.device = self.grads[0].device
+        types = {torch.float32: F32, torch.bfloat16: BF16}
+        for g, o in zip(self.grads, self.out):
+            _need("GradSet", g, "a gradient", tuple(types), g.shape, self.grads[0])
+            _need("GradSet", o, "an output", (g.dtype,), g.shape, self.grads[0])
+        if self.device.type != "cuda":
+            raise ValueError(f"GradSet: GPU tensors are needed, got some on {self.device}")
+        table = (Grad * len(self.grads))(*[Grad(g.data_ptr(), o.data_ptr(), g.numel(), types[g.dtype])
+                                           for g, o in zip(self.grads, self.out)])
+        size, n = ctypes.c_size_t(), ctypes.c_int64()
+        _check(lib().nvfp4moe_grad_plan_bytes(table, len(table), ctypes.byref(size), ctypes.byref(n)),
+               "nvfp4moe_grad_plan_bytes")
+        self.n_chunks = n.value
+        host = torch.empty((size.value // 8,), dtype=torch.int64)
+        _check(lib().nvfp4moe_grad_plan(table, len(table), _ptr(host), size.value), "nvfp4moe_grad_plan")
+        self.plan = host.to(self.device)
+
+
+def clip_grad_norm(grads: GradSet, max_norm: float, stream=None):
+    """nvfp4moe_clip_grad_norm: the global norm (float64 [1], on the GPU); the set's outputs hold the gradients scaled
+    to at most max_norm (unchanged if the norm is not finite).  max_norm = inf takes the norm only."""
+    import torch
+    with _At(grads.plan if grads.n_chunks else grads.grads[0], stream) as s:
+        norm = torch.empty((1,), dtype=torch.float64, device=grads.device)
+        ws = torch.empty((lib().nvfp4moe_clip_workspace_bytes(),), dtype=torch.uint8, device=grads.device)
+        _check(lib().nvfp4moe_clip_grad_norm(_ptr(grads.plan), grads.n_chunks, max_norm, _ptr(norm), _ptr(ws), ws.numel(),
+                                             s), "nvfp4moe_clip_grad_norm")
+        if stream is not None and grads.n_chunks:
+            grads.plan.record_stream(stream)
+    return norm

@@ -10,7 +10,8 @@ CSRC = os.path.join(HERE, "csrc")
 BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "lib", "libnvfp4moe.so")
 SOURCES = ["quant.hip", "route.hip", "gemm.hip", "gemm_w4a16.hip", "producer.hip", "backward.hip", "combine.hip",
-           "router.hip", "api.hip", "selftest.hip"]
+           "router.hip", "select.hip", "mxfp4_quant.hip", "mxfp4_gemm.hip", "grad_clip.hip", "api.hip", "api_ops.hip",
+           "selftest.hip"]
 
 # -ffp-contract=off and no fast-math: the quantizer's binary32 divisions and
 # products must be the IEEE operations the numeric contract names.  Packed

@@ -103,6 +103,98 @@ hipError_t launch_gemm_w4a16(int mode, const W16Params& P, int64_t mt_bound, hip
 hipError_t launch_router(const uint16_t* x, int32_t T, int32_t H, const uint16_t* w, int32_t E, int32_t K,
                          bool renorm, float* logits, int32_t* ids, float* probs, hipStream_t stream);
 
+// Router scores alone: logits [T, E] (FP32).
+hipError_t launch_router_scores(const uint16_t* x, int32_t T, int32_t H, const uint16_t* w, int32_t E, float* logits,
+                                hipStream_t stream);
+
+// Expert selection from logits and its gradient (select.hip).
+constexpr int kMaxGroups = 64;
+struct SelectParams {
+    const void* logits;  // FP32 or BF16 [T, E], rows ld apart
+    int64_t ld;
+    int64_t T;
+    int32_t E, K;
+    const float* bias;  // [E] or null
+    bool sigmoid, renorm, top2;
+    bool vec, vec_out;  // rows allow four-element loads / stores
+    float scale;
+    int32_t n_groups, group_size, top_groups;
+    uint32_t group_magic;  // ceil(2^22 / group_size): e / group_size = e * group_magic >> 22 for e < 1024
+    int32_t* ids;          // selection: out
+    float* probs;
+    const int32_t* ids_in;  // gradient
+    const float* dprobs;
+    void* dlogits;
+    int64_t ld_out;
+};
+hipError_t launch_router_select(const SelectParams& P, bool bf16, hipStream_t stream);
+hipError_t launch_router_select_backward(const SelectParams& P, bool bf16, hipStream_t stream);
+
+// MXFP4 quantizers (mxfp4_quant.hip) and products (mxfp4_gemm.hip).
+constexpr int kMxUnroll = 4;  // 8-element groups per thread
+struct MxRowsParams {
+    const uint16_t* x;
+    int64_t rows, ld;
+    uint32_t cols;
+    bool up, operand;        // operand: the products' row layout, else logical
+    uint8_t* codes;
+    uint8_t* scales;
+    int64_t ld_codes, ld_scales;  // bytes per row
+    int4* tiles;             // grouped product: its row tiles of bm rows, or null
+    int32_t* n_tiles;
+    const int32_t* offsets;  // [E + 1]
+    int32_t E, bm;
+    uint32_t groups;         // set by the launcher
+    double inv_groups;
+};
+hipError_t launch_mx_quant_rows(MxRowsParams P, hipStream_t stream);
+hipError_t launch_mx_quant_tiles(const uint16_t* x, int64_t n_mats, int32_t rows, int32_t cols, int64_t ld, uint8_t* codes,
+                                 uint8_t* scales, bool up, hipStream_t stream);
+struct MxDequantParams {
+    const uint8_t* codes;
+    const uint8_t* scales;
+    uint16_t* out;
+    int64_t rows, ld;
+    uint32_t cols, mat_rows;
+    bool tiled;
+    uint32_t groups, row_tiles, chunks, quads;  // set by the launcher
+    double inv_groups;
+};
+hipError_t launch_mx_dequant(MxDequantParams P, hipStream_t stream);
+struct MxGemmParams {
+    const uint8_t* a_codes;  // operand rows
+    const uint8_t* a_scales;
+    int64_t ld_a, ld_as;     // bytes per row
+    const uint8_t* w_codes;  // weight tiles
+    const uint8_t* w_scales;
+    int32_t row_tiles, chunks, quads;
+    int32_t N;
+    int32_t col_tiles;       // set by the launcher
+    bool vec_out;            // rows allow four-element stores
+    int64_t M;               // rows of a dense product
+    const int4* tiles;       // grouped product: {matrix, first row, rows, 0}
+    const int32_t* n_tiles;
+    uint16_t* out;
+    int64_t ld_out;
+};
+int mx_tile_rows(int64_t rows, int64_t E);
+hipError_t launch_mx_gemm(MxGemmParams P, int64_t tiles_bound, int bm, hipStream_t stream);
+
+// Gradient norm and clipping (grad_clip.hip): up to kGradChunk consecutive
+// elements of one tensor; `head` of them precede the first 16-byte boundary.
+constexpr int kGradBlocks = 2048;
+constexpr int64_t kGradChunk = 32768;
+struct GradChunk {
+    const void* in;
+    void* out;
+    uint32_t n;
+    uint16_t head;
+    uint8_t bf16;
+    uint8_t out_vec;  // out is 16-byte aligned where in is
+};
+hipError_t launch_clip_grad_norm(const GradChunk* plan, int64_t n_chunks, double max_norm, double* partial, double* norm_out,
+                                 hipStream_t stream);
+
 #ifdef __HIPCC__
 // Whether the 32-row tile rt of the sorted buffers holds rows of an expert:
 // below off[E] in the contiguous layout (capacity 0); inside its expert's

@@ -208,12 +208,17 @@ __global__ void __launch_bounds__(kTopkWaves * 64) router_topk_kernel(int32_t T,
     }
 }
 
+hipError_t launch_router_scores(const uint16_t* x, int32_t T, int32_t H, const uint16_t* w, int32_t E, float* logits,
+                                hipStream_t stream) {
+    const unsigned score_waves = (unsigned)(((T + kRouterTok - 1) / kRouterTok) * ((E + 31) / 32));
+    hipLaunchKernelGGL(router_scores_kernel, dim3(score_waves), dim3(64), 0, stream, x, T, H, w, E, logits);
+    return hipGetLastError();
+}
+
 hipError_t launch_router(const uint16_t* x, int32_t T, int32_t H, const uint16_t* w, int32_t E, int32_t K,
                          bool renorm, float* logits, int32_t* ids, float* probs, hipStream_t stream) {
     if (T <= 0) return hipSuccess;
-    const unsigned score_waves = (unsigned)(((T + kRouterTok - 1) / kRouterTok) * ((E + 31) / 32));
-    hipLaunchKernelGGL(router_scores_kernel, dim3(score_waves), dim3(64), 0, stream, x, T, H, w, E, logits);
-    hipError_t st = hipGetLastError();
+    hipError_t st = launch_router_scores(x, T, H, w, E, logits, stream);
     if (st != hipSuccess) return st;
     hipLaunchKernelGGL(router_topk_kernel, dim3((unsigned)((T + kTopkWaves - 1) / kTopkWaves)), dim3(kTopkWaves * 64),
                        0, stream, T, E, K, renorm ? 1 : 0, logits, ids, probs);
