@@ -491,7 +491,7 @@ NVFP4MOE_API int nvfp4moe_mxfp4_dequantize(const nvfp4moe_mxfp4_tensor* q, uint1
 
 /* Dense MXFP4 linear: out [M, N] = bf16(Q(x) . Wq^T), with x [M, K] BF16 (rows
  * ldx apart) quantized into the workspace by scale_round, Wq one GEMM-layout
- * matrix [N, K] and FP32 accumulation.  M >= 0, K % 32 == 0, any N.
+ * matrix [N, K] and FP32 accumulation.  M >= 0, K % 32 == 0, K < 2^24, any N.
  * Requirements: x 16-byte aligned, ldx >= K and a multiple of 8; out aligned to
  * 2 bytes, ld_out >= N (8-byte stores where out, ld_out and N allow them);
  * workspace 256-byte aligned, nvfp4moe_mxfp4_workspace_bytes(M, K, 1) bytes.

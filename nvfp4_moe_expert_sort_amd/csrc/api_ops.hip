@@ -89,7 +89,7 @@ struct MxWork {
 };
 constexpr int64_t kMxMinTile = 16;
 bool mx_work(int64_t M, int64_t K, int64_t E, MxWork* w) {
-    if (M < 0 || M >= ((int64_t)1 << 31) || K <= 0 || K % 32 != 0 || K >= ((int64_t)1 << 31) || E < 1 || E > kMaxExperts)
+    if (M < 0 || M >= ((int64_t)1 << 31) || K <= 0 || K % 32 != 0 || K >= ((int64_t)1 << 24) || E < 1 || E > kMaxExperts)
         return false;
     if (M > 0 && (K + 255) / 256 * 256 >= ((int64_t)1 << 34) / M) return false;
     w->ld_codes = (K + 255) / 256 * 128;
@@ -158,6 +158,7 @@ int mx_product(const uint16_t* x, int64_t M, int64_t ldx, const int32_t* offsets
     p.quads = (int32_t)sh.quads;
     p.N = (int32_t)N;
     p.vec_out = ld_out % 4 == 0 && aligned(out, 8);
+    p.vec_out8 = ld_out % 8 == 0 && aligned(out, 16);
     p.M = M;
     p.tiles = q.tiles;
     p.n_tiles = q.n_tiles;

@@ -81,7 +81,10 @@ __device__ void build_tiles(const MxRowsParams& P) {
     for (int i = 0; i < kPer; i++) {
         const int e = tid * kPer + i;
         if (e >= P.E) break;
-        for (int32_t r = off[e]; r < off[e + 1]; r += P.bm) P.tiles[at++] = int4{e, r, min(P.bm, off[e + 1] - r), 0};
+        const int32_t rows = off[e + 1] - off[e], tiles = (rows + P.bm - 1) / P.bm;
+        const int32_t high = tiles ? ((rows + tiles - 1) / tiles + 15) / 16 * 16 : 0;  // even shares of whole 16 rows, <= bm
+        for (int32_t i = 0; i < tiles; i++, at++)
+            P.tiles[at] = int4{e, off[e] + i * high, max(min(high, rows - i * high), 0), 0};
     }
     if (tid == 255) *P.n_tiles = at;  // every expert lies at or before this thread's
 }

@@ -170,7 +170,7 @@ struct MxGemmParams {
     int32_t row_tiles, chunks, quads;
     int32_t N;
     int32_t col_tiles;       // set by the launcher
-    bool vec_out;            // rows allow four-element stores
+    bool vec_out, vec_out8;  // rows allow four- and eight-element stores
     int64_t M;               // rows of a dense product
     const int4* tiles;       // grouped product: {matrix, first row, rows, 0}
     const int32_t* n_tiles;
