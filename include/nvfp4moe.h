@@ -417,7 +417,8 @@ typedef struct {
  *     token's available selected experts), computed so that the sum does not
  *     vanish however negative the logits are.
  * s and v are formed in FP64, so the choice does not depend on FP32 rounding;
- * with a bias (or TOP2) values closer than 2^-42 relative count as equal.
+ * with a bias (or TOP2) values closer than about 2^-40 relative may count as
+ * equal.
  *   ids [T, K] int32, probs [T, K] FP32: caller-owned outputs
  * Requirements: ld >= E; logits aligned to their element, ids, probs and bias
  * to 4 bytes (rows are read four elements at a time where ld and the pointer

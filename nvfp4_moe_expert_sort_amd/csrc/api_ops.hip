@@ -48,6 +48,7 @@ int select_params(const nvfp4moe_select_config* c, const void* logits, int64_t l
     P->renorm = c->renormalize != 0;
     P->top2 = c->group_score == NVFP4MOE_GROUP_TOP2;
     P->vec = ld % 4 == 0 && aligned(logits, 4 * elem);
+    P->vec_bias = aligned(bias, 16);
     P->scale = c->scale;
     P->n_groups = c->n_groups;
     P->group_size = size;

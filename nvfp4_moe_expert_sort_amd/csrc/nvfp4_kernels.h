@@ -116,9 +116,10 @@ struct SelectParams {
     int32_t E, K;
     const float* bias;  // [E] or null
     bool sigmoid, renorm, top2;
-    bool vec, vec_out;  // rows allow four-element loads / stores
+    bool vec, vec_bias, vec_out;  // rows, bias, rows of the gradient allow four-element accesses
     float scale;
     int32_t n_groups, group_size, top_groups;
+    int32_t lds_token;     // set by the launcher
     uint32_t group_magic;  // ceil(2^22 / group_size): e / group_size = e * group_magic >> 22 for e < 1024
     int32_t* ids;          // selection: out
     float* probs;
@@ -127,7 +128,7 @@ struct SelectParams {
     void* dlogits;
     int64_t ld_out;
 };
-hipError_t launch_router_select(const SelectParams& P, bool bf16, hipStream_t stream);
+hipError_t launch_router_select(SelectParams P, bool bf16, hipStream_t stream);
 hipError_t launch_router_select_backward(const SelectParams& P, bool bf16, hipStream_t stream);
 
 // MXFP4 quantizers (mxfp4_quant.hip) and products (mxfp4_gemm.hip).

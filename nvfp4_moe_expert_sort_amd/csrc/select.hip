@@ -14,7 +14,8 @@
 // compares a whole (value, id) key: the id sits in the key's low 10 mantissa
 // bits (complemented for v >= 0, so that the lower id is the larger key).
 // Without a bias v is an FP32 number whose low 29 bits are zero, and the
-// order is exact; with one, values closer than 2^-42 relative count as equal.
+// order is exact; with one, values are told apart down to about 2^-41 relative
+// (42 bits of key, scores within 2^-45).
 //
 // LT lanes (16, or 64 for more than 256 experts or 16 slots) share a token, so
 // a wavefront takes 4 tokens or one, each lane NV experts.  The lane sorts its
@@ -29,8 +30,10 @@ namespace nvfp4 {
 namespace {
 
 constexpr int kSelWaves = 4;         // wavefronts per workgroup
-constexpr double kUnavailable = -0x1p+1000;  // below every value, above "not kept" (-inf)
-constexpr double kNotKept = -__builtin_inf();
+// Keys below every value: an unavailable expert, and one that cannot be taken
+// (past E, or in a group that does not stay).  Only the high words differ.
+constexpr double kUnavailable = -0x1p+1000, kNotKept = -0x1p+1016;
+constexpr uint32_t kUnavailableHi = 0xFE700000u, kNotKeptHi = 0xFF700000u;
 
 __device__ __forceinline__ double max64(double a, double b) {
     double r;
@@ -40,6 +43,18 @@ __device__ __forceinline__ double max64(double a, double b) {
 __device__ __forceinline__ double min64(double a, double b) {
     double r;
     asm("v_min_f64 %0, %1, %2" : "=v"(r) : "v"(a), "v"(b));
+    return r;
+}
+
+__device__ __forceinline__ float max32(float a, float b) {
+    float r;
+    asm("v_max_f32 %0, %1, %2" : "=v"(r) : "v"(a), "v"(b));
+    return r;
+}
+
+__device__ __forceinline__ float min32(float a, float b) {
+    float r;
+    asm("v_min_f32 %0, %1, %2" : "=v"(r) : "v"(a), "v"(b));
     return r;
 }
 
@@ -75,13 +90,13 @@ __device__ __forceinline__ double tok_max(double v) {
 }
 template <int LT>
 __device__ __forceinline__ float tok_max(float v) {
-    v = fmaxf(v, ror<8>(v));
-    v = fmaxf(v, ror<4>(v));
-    v = fmaxf(v, ror<2>(v));
-    v = fmaxf(v, ror<1>(v));
+    v = max32(v, ror<8>(v));
+    v = max32(v, ror<4>(v));
+    v = max32(v, ror<2>(v));
+    v = max32(v, ror<1>(v));
     if (LT == 64) {
-        v = fmaxf(v, __shfl_xor(v, 16, kWave));
-        v = fmaxf(v, __shfl_xor(v, 32, kWave));
+        v = max32(v, __shfl_xor(v, 16, kWave));
+        v = max32(v, __shfl_xor(v, 32, kWave));
     }
     return v;
 }
@@ -98,40 +113,51 @@ __device__ __forceinline__ F tok_sum(F v) {
     return __shfl(v, 0, LT);
 }
 
-// e^x for x in [-708, 709]: x = n ln 2 + r, |r| <= ln 2 / 2, Taylor's series of
-// e^r to r^12 (the next term is below 1.7e-16), scaled by 2^n.
+// e^x for x in [-708, 708], within 2^-46 relative: x = n ln 2 + r with
+// |r| <= ln 2 / 2 (n is read from the low bits of t = x log2 e + 1.5 2^52),
+// Taylor's series of e^r to r^11 (the next term is below 2^-47), and n added
+// to the exponent.  The series is written as one block of instructions that
+// take the coefficients from scalar registers: from plain code the compiler
+// moves each into vector registers first, two moves a term.
 __device__ __forceinline__ double exp64(double x) {
-    const double n = __builtin_rint(x * 1.4426950408889634);
-    double r = __builtin_fma(-n, 0x1.62e42fefa39efp-1, x);
-    r = __builtin_fma(-n, 0x1.abc9e3b39803fp-56, r);
-    double p = 1.0 / 479001600.0;
-    p = __builtin_fma(p, r, 1.0 / 39916800.0);
-    p = __builtin_fma(p, r, 1.0 / 3628800.0);
-    p = __builtin_fma(p, r, 1.0 / 362880.0);
-    p = __builtin_fma(p, r, 1.0 / 40320.0);
-    p = __builtin_fma(p, r, 1.0 / 5040.0);
-    p = __builtin_fma(p, r, 1.0 / 720.0);
-    p = __builtin_fma(p, r, 1.0 / 120.0);
-    p = __builtin_fma(p, r, 1.0 / 24.0);
-    p = __builtin_fma(p, r, 1.0 / 6.0);
-    p = __builtin_fma(p, r, 0.5);
-    p = __builtin_fma(p, r, 1.0);
-    p = __builtin_fma(p, r, 1.0);
-    return __builtin_ldexp(p, (int)n);
+    double p, t, r;
+    asm("v_fma_f64 %1, %3, %4, %5\n\t"
+        "v_add_f64 %0, %1, -%5\n\t"
+        "v_fma_f64 %2, %0, %6, %3\n\t"
+        "v_fma_f64 %2, %0, %7, %2\n\t"
+        "v_fma_f64 %0, %2, %8, %9\n\t"
+        "v_fma_f64 %0, %0, %2, %10\n\t"
+        "v_fma_f64 %0, %0, %2, %11\n\t"
+        "v_fma_f64 %0, %0, %2, %12\n\t"
+        "v_fma_f64 %0, %0, %2, %13\n\t"
+        "v_fma_f64 %0, %0, %2, %14\n\t"
+        "v_fma_f64 %0, %0, %2, %15\n\t"
+        "v_fma_f64 %0, %0, %2, %16\n\t"
+        "v_fma_f64 %0, %0, %2, 0.5\n\t"
+        "v_fma_f64 %0, %0, %2, 1.0\n\t"
+        "v_fma_f64 %0, %0, %2, 1.0"
+        : "=&v"(p), "=&v"(t), "=&v"(r)
+        : "v"(x), "s"(1.4426950408889634), "v"(0x1.8p+52), "s"(-0x1.62e42fefa39efp-1), "s"(-0x1.abc9e3b39803fp-56),
+          "s"(1.0 / 39916800.0), "v"(1.0 / 3628800.0), "s"(1.0 / 362880.0), "s"(1.0 / 40320.0), "s"(1.0 / 5040.0),
+          "s"(1.0 / 720.0), "s"(1.0 / 120.0), "s"(1.0 / 24.0), "s"(1.0 / 6.0));
+    return __builtin_ldexp(p, (int)(uint32_t)__builtin_bit_cast(uint64_t, t));
 }
-// 1 / d for normal d > 0: the hardware estimate and two Newton steps.
+// 1 / d for normal d > 0, within 2^-45: the hardware estimate (2^-23) and one Newton step.
 __device__ __forceinline__ double rcp64(double d) {
-    double r = __builtin_amdgcn_rcp(d);
-    r = __builtin_fma(__builtin_fma(-d, r, 1.0), r, r);
+    const double r = __builtin_amdgcn_rcp(d);
     return __builtin_fma(__builtin_fma(-d, r, 1.0), r, r);
 }
-// e^x for x <= 0; 0 below the range of exp64.
-__device__ __forceinline__ double exp64_neg(double x) { return x < -708.0 ? 0.0 : exp64(x); }
-__device__ __forceinline__ double sigmoid64(float l) { return rcp64(1.0 + exp64(fmax(fmin(-(double)l, 708.0), -708.0))); }
+// e^x for x <= 0; below the range of exp64 its smallest value, 2^-1021.
+__device__ __forceinline__ double exp64_neg(double x) { return exp64(max64(x, -708.0)); }
+__device__ __forceinline__ double sigmoid64(float l) {
+    return rcp64(1.0 + exp64((double)__builtin_amdgcn_fmed3f(-l, -708.0f, 708.0f)));
+}
 
 constexpr float kFltMax = 3.402823466e+38f;
 // A logit as the definitions take it: -inf where it is unusable, at most the largest finite value.
-__device__ __forceinline__ float clean(float l) { return l > -__builtin_inff() ? fminf(l, kFltMax) : -__builtin_inff(); }
+__device__ __forceinline__ float clean(float l) {
+    return l > -__builtin_inff() ? __builtin_amdgcn_fmed3f(l, -kFltMax, kFltMax) : -__builtin_inff();
+}
 
 // Weight (before the scale) of a chosen expert in lane k < K, in FP64; `live`
 // is false in the other lanes and for unavailable experts.  `max_l`, `den`:
@@ -141,7 +167,7 @@ template <int LT>
 __device__ __forceinline__ double slot_weight(float l, bool live, bool sigmoid, bool renorm, float max_l, double den) {
     if (!renorm) {
         if (!live) return 0.0;
-        return sigmoid ? sigmoid64(l) : exp64_neg((double)l - (double)max_l) / den;
+        return sigmoid ? sigmoid64(l) : exp64_neg((double)l - (double)max_l) * rcp64(den);
     }
     // The sum over the selection, shifted by its largest term so that it
     // cannot vanish: sigma(l) e^-m = e^(l - m) / (1 + e^l) with m = min(top, 0).
@@ -156,7 +182,7 @@ __device__ __forceinline__ double slot_weight(float l, bool live, bool sigmoid, 
             w = sigmoid64(l);
     }
     const double sum = tok_sum<LT>(w);
-    return live ? w / sum : 0.0;
+    return live ? w * rcp64(sum) : 0.0;
 }
 
 // Batcher's odd-even merge network: a[0..N) descending, N a power of two.
@@ -204,9 +230,34 @@ __device__ __forceinline__ void load4(const uint16_t* __restrict__ row, int e0, 
 __device__ __forceinline__ float load1(const float* p) { return *p; }
 __device__ __forceinline__ float load1(const uint16_t* p) { return bf16_to_f32(*p); }
 
-__device__ __forceinline__ double key_of(double v, int e) {
-    const uint64_t u = __builtin_bit_cast(uint64_t, v + 0.0);  // -0 as +0
-    return __builtin_bit_cast(double, (u & ~1023ull) | (uint64_t)((u >> 63) ? e : 1023 - e));
+// A lane mask (all ones or zero) that the compiler takes as plain bits: from a
+// condition it would turn the choice between two array elements into a choice
+// of their index, and that into a search through the whole array.
+__device__ __forceinline__ uint32_t lane_mask(bool c) {
+    uint32_t m = c ? ~0u : 0u;
+    asm("" : "+v"(m));
+    return m;
+}
+__device__ __forceinline__ uint32_t able_mask(uint32_t able, int i) {
+    return (uint32_t)__builtin_amdgcn_sbfe((int32_t)able, (uint32_t)i, 1);
+}
+// v, or the key constant of that high word where the mask is zero.
+__device__ __forceinline__ double pick(uint32_t mask, double v, uint32_t other) {
+    const uint64_t u = __builtin_bit_cast(uint64_t, v);
+    const uint32_t hi = ((uint32_t)(u >> 32) & mask) | (other & ~mask), lo = (uint32_t)u & mask;
+    return __builtin_bit_cast(double, ((uint64_t)hi << 32) | lo);
+}
+__device__ __forceinline__ double blend(uint32_t m, double a, double b) {
+    const uint64_t x = __builtin_bit_cast(uint64_t, a), y = __builtin_bit_cast(uint64_t, b);
+    const uint32_t lo = ((uint32_t)x & m) | ((uint32_t)y & ~m), hi = ((uint32_t)(x >> 32) & m) | ((uint32_t)(y >> 32) & ~m);
+    return __builtin_bit_cast(double, ((uint64_t)hi << 32) | lo);
+}
+// v with expert e in its low 10 bits: e, or 1023 - e where v >= 0, so that of
+// equal values the lower expert is the larger key.
+__device__ __forceinline__ double tag(double v, int e) {
+    const uint64_t u = __builtin_bit_cast(uint64_t, v);
+    const uint32_t hi = (uint32_t)(u >> 32), id = (uint32_t)e ^ ~(uint32_t)((int32_t)hi >> 31);
+    return __builtin_bit_cast(double, ((uint64_t)hi << 32) | (((uint32_t)u & ~1023u) | (id & 1023u)));
 }
 __device__ __forceinline__ int key_expert(double key) {
     const uint64_t u = __builtin_bit_cast(uint64_t, key);
@@ -216,10 +267,14 @@ __device__ __forceinline__ int key_expert(double key) {
 
 }  // namespace
 
-// LT lanes per token, NV experts per lane (E <= LT * NV), lists of LEN keys
-// (the longest that K slots can take from one lane).
+// LT lanes per token, NV experts per lane (E <= LT * NV) in runs of four,
+// lists of LEN keys (the longest that K slots can take from one lane).
+//
+// T = 16384, E = 256, sigmoid with bias and groups: the FP64 scores are 16 x
+// 24 instructions of a wavefront's about 1000, the network and the slots 300;
+// reading the logits is a third of the kernel's time.
 template <int LT, int NV, int LEN, typename L>
-__global__ void __launch_bounds__(kSelWaves * 64) router_select_kernel(SelectParams P) {
+__global__ void __launch_bounds__(kSelWaves * 64, 4) router_select_kernel(SelectParams P) {
     constexpr int kTok = kWave / LT;     // tokens per wavefront
     constexpr int kGroupRounds = kMaxGroups / LT;
     extern __shared__ __attribute__((aligned(16))) double smem[];  // only with groups
@@ -229,87 +284,117 @@ __global__ void __launch_bounds__(kSelWaves * 64) router_select_kernel(SelectPar
     const L* row = (const L*)P.logits + tr * P.ld;
     const bool sigmoid = P.sigmoid, biased = P.bias != nullptr, grouped = P.n_groups > 1;
     const bool top2 = grouped && P.top2, scores = biased || top2;
+    const bool runs = (P.group_size & 3) == 0;  // a run of four experts lies in one group
 
-    float l[NV];
+    float l[NV], bias[NV];
 #pragma unroll
     for (int i = 0; i < NV / 4; i++) {
         float v[4];
         load4(row, (i * LT + lane) * 4, P.E, P.vec, v);
 #pragma unroll
-        for (int j = 0; j < 4; j++) l[4 * i + j] = clean(v[j]);
+        for (int j = 0; j < 4; j++) l[4 * i + j] = v[j];
     }
+    if (biased) {
+#pragma unroll
+        for (int i = 0; i < NV / 4; i++) {
+            float v[4];
+            load4(P.bias, (i * LT + lane) * 4, P.E, P.vec_bias, v);
+#pragma unroll
+            for (int j = 0; j < 4; j++) bias[4 * i + j] = clean(v[j]);
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < NV; i++) l[i] = clean(l[i]);
     float max_l = 0.0f;
     double den = 1.0;
-    const bool softmax_all = !sigmoid && (scores || !P.renorm);
-    if (softmax_all) {
+    if (!sigmoid && (scores || !P.renorm)) {
         float mx = l[0];
 #pragma unroll
         for (int i = 1; i < NV; i++) mx = fmaxf(mx, l[i]);
         max_l = fmaxf(tok_max<LT>(mx), -kFltMax);
-    }
-    if (softmax_all && !scores) {  // the denominator alone: FP32 terms, no choice depends on it
-        float sum = 0.0f;
+        if (!scores) {  // the denominator alone: FP32 terms, no choice depends on it
+            float sum = 0.0f;
 #pragma unroll
-        for (int i = 0; i < NV; i++) sum += __builtin_amdgcn_exp2f((l[i] - max_l) * 1.4426950408889634f);
-        den = (double)tok_sum<LT>(sum);
-    }
-    double key[NV];
-    double* gv = smem + (size_t)slot * (P.E + 8);  // this token's values, [expert in group][group]
-    if (scores) {
-        double sum = 0.0;
-#pragma unroll
-        for (int i = 0; i < NV; i++) {
-            double s;
-            if (sigmoid)
-                s = sigmoid64(fmaxf(l[i], -kFltMax));
-            else
-                s = exp64_neg((double)l[i] - (double)max_l);
-            if (!(l[i] > -__builtin_inff())) s = 0.0;
-            key[i] = s;
-            sum += s;
+            for (int i = 0; i < NV; i++) sum += __builtin_amdgcn_exp2f((l[i] - max_l) * 1.4426950408889634f);
+            den = (double)tok_sum<LT>(sum);
         }
-        if (!sigmoid) {
-            den = fmax(tok_sum<LT>(sum), 1e-300);  // a row with nothing usable: all scores 0
-            const double inv = 1.0 / den;
+    }
+    double key[NV];  // v, or the scores that TOP2 groups add up
+    if (scores) {
+        if (sigmoid) {
+#pragma unroll
+            for (int i = 0; i < NV; i++) key[i] = sigmoid64(l[i]);
+        } else {
+            double sum = 0.0;
+#pragma unroll
+            for (int i = 0; i < NV; i++) sum += key[i] = exp64_neg((double)l[i] - (double)max_l);
+            den = tok_sum<LT>(sum);
+            const double inv = rcp64(den);
 #pragma unroll
             for (int i = 0; i < NV; i++) key[i] *= inv;
         }
-    }
+        if (biased) {
 #pragma unroll
-    for (int i = 0; i < NV / 4; i++)
-#pragma unroll
-        for (int j = 0; j < 4; j++) {
-            const int n = 4 * i + j, e = (i * LT + lane) * 4 + j;
-            bool live = l[n] > -__builtin_inff();
-            double s = scores ? key[n] : 0.0;
-            if (biased && e < P.E) {
-                const float b = clean(P.bias[e]);
-                live = live && b > -__builtin_inff();
-                s += (double)b;
-            }
-            const double v = biased ? s : (double)l[n];
-            if (grouped && e < P.E) {
-                const int g = (int)(((uint32_t)e * P.group_magic) >> 22);
-                gv[(e - g * P.group_size) * P.n_groups + g] = live ? (top2 ? s : v) : kNotKept;
-            }
-            key[n] = e < P.E ? key_of(live ? v : kUnavailable, e) : kNotKept;
+            for (int i = 0; i < NV; i++) key[i] += (double)bias[i];
         }
+    } else {
+#pragma unroll
+        for (int i = 0; i < NV; i++) key[i] = (double)(l[i] + 0.0f);  // (-0 as +0)
+    }
+    // Unavailable experts: an unusable logit or bias.
+#pragma unroll
+    for (int i = 0; i < NV; i++) key[i] = pick(lane_mask((biased ? min32(l[i], bias[i]) : l[i]) > -__builtin_inff()), key[i], kUnavailableHi);
+    uint32_t able = 0;  // bit i: expert i of the lane exists and its group stays
+#pragma unroll
+    for (int i = 0; i < NV / 4; i++) able |= ((1u << min(max(P.E - (i * LT + lane) * 4, 0), 4)) - 1) << (4 * i);
     if (grouped) {
+        double* gv = smem + (size_t)slot * P.lds_token;  // this token's values, and its groups'
+        double* gs = gv + P.lds_token - P.n_groups;
+        if (runs) {  // the two best of each run: [run in group][best, second][group]
+#pragma unroll
+            for (int i = 0; i < NV / 4; i++) {
+                const int u = i * LT + lane;
+                const double a = max64(key[4 * i], key[4 * i + 1]), b = min64(key[4 * i], key[4 * i + 1]);
+                const double c = max64(key[4 * i + 2], key[4 * i + 3]), d = min64(key[4 * i + 2], key[4 * i + 3]);
+                if (u * 4 < P.E) {
+                    const int g = (int)(((uint32_t)(u * 4) * P.group_magic) >> 22);
+                    double* at = gv + (u - g * (P.group_size >> 2)) * 2 * P.n_groups + g;
+                    at[0] = max64(a, c);
+                    at[P.n_groups] = max64(min64(a, c), max64(b, d));
+                }
+            }
+        } else {
+#pragma unroll
+            for (int n = 0; n < NV; n++) {
+                const int e = ((n >> 2) * LT + lane) * 4 + (n & 3);
+                if (e < P.E) {
+                    const int g = (int)(((uint32_t)e * P.group_magic) >> 22);
+                    gv[(e - g * P.group_size) * P.n_groups + g] = key[n];
+                }
+            }
+        }
+        __syncthreads();
         // Lane g ranks group g (and g + LT, ...): its value, then the count of
         // groups before it; the kept ones become a bit mask.
-        double* gs = smem + (size_t)kSelWaves * kTok * (P.E + 8) + slot * kMaxGroups;
-        __syncthreads();
 #pragma unroll
         for (int r = 0; r < kGroupRounds; r++) {
             const int g = r * LT + lane;
             if (g < P.n_groups) {
                 double b1 = kNotKept, b2 = kNotKept;
-                for (int w = 0; w < P.group_size; w++) {
-                    const double v = gv[w * P.n_groups + g];
-                    b2 = max64(b2, min64(b1, v));
-                    b1 = max64(b1, v);
+                if (runs) {
+                    for (int w = 0; w < P.group_size / 4; w++) {
+                        const double c1 = gv[2 * w * P.n_groups + g], c2 = gv[(2 * w + 1) * P.n_groups + g];
+                        b2 = max64(min64(b1, c1), max64(b2, c2));
+                        b1 = max64(b1, c1);
+                    }
+                } else {
+                    for (int w = 0; w < P.group_size; w++) {
+                        const double v = gv[w * P.n_groups + g];
+                        b2 = max64(b2, min64(b1, v));
+                        b1 = max64(b1, v);
+                    }
                 }
-                gs[g] = top2 && b2 > kNotKept ? b1 + b2 : b1;
+                gs[g] = top2 && b2 > kUnavailable ? b1 + b2 : b1;
             }
         }
         __syncthreads();
@@ -330,29 +415,49 @@ __global__ void __launch_bounds__(kSelWaves * 64) router_select_kernel(SelectPar
             kept |= LT == 64 ? all : ((all >> ((threadIdx.x & 63) / LT * LT)) & ((1ull << (LT & 63)) - 1)) << (r * LT);
         }
 #pragma unroll
-        for (int n = 0; n < NV; n++) {
-            const int e = ((n >> 2) * LT + lane) * 4 + (n & 3);
-            const int g = (int)(((uint32_t)e * P.group_magic) >> 22);
-            if (!((kept >> (g & 63)) & 1)) key[n] = kNotKept;
+        for (int i = 0; i < NV / 4; i++) {
+            const uint32_t e0 = (i * LT + lane) * 4;
+            if (runs) {
+                able &= ((kept >> (((e0 * P.group_magic) >> 22) & 63)) & 1) ? ~0u : ~(15u << (4 * i));
+            } else {
+#pragma unroll
+                for (int j = 0; j < 4; j++)
+                    able &= ((kept >> ((((e0 + j) * P.group_magic) >> 22) & 63)) & 1) ? ~0u : ~(1u << (4 * i + j));
+            }
+        }
+        if (top2 && !biased) {  // groups by their scores, experts by their logits
+#pragma unroll
+            for (int i = 0; i < NV; i++) key[i] = pick(lane_mask(l[i] > -__builtin_inff()), (double)(l[i] + 0.0f), kUnavailableHi);
         }
     }
+#pragma unroll
+    for (int i = 0; i < NV; i++) key[i] = tag(pick(able_mask(able, i), key[i], kNotKeptHi), ((i >> 2) * LT + lane) * 4 + (i & 3));
     sort_desc(key);
     double mine = kNotKept;
-    for (int k = 0; k < P.K; k++) {
-        const double best = tok_max<LT>(key[0]);
-        if (lane == k) mine = best;
-        const bool pop = key[0] == best;  // keys are unique: one owner
+    // Slot k takes the best list head; its owner moves its list up (after slot
+    // k of at most LEN only LEN - 1 - k more keys of a list can be needed).
 #pragma unroll
-        for (int i = 0; i < LEN; i++) {
-            const double next = i + 1 < LEN ? key[i + 1] : kNotKept;
-            key[i] = pop ? next : key[i];
+    for (int k = 0; k < (LEN <= 8 ? LEN : 0); k++)
+        if (k < P.K) {
+            const double best = tok_max<LT>(key[0]);
+            if (lane == k) mine = best;
+            const uint32_t pop = lane_mask(key[0] == best);  // keys are unique: one owner
+#pragma unroll
+            for (int i = 0; i < (LEN < NV ? LEN - 1 - k : LEN); i++) key[i] = blend(pop, i + 1 < NV ? key[i + 1] : kNotKept, key[i]);
         }
-    }
+    if (LEN == NV)
+        for (int k = LEN <= 8 ? LEN : 0; k < P.K; k++) {
+            const double best = tok_max<LT>(key[0]);
+            if (lane == k) mine = best;
+            const uint32_t pop = lane_mask(key[0] == best);
+#pragma unroll
+            for (int i = 0; i < NV; i++) key[i] = blend(pop, i + 1 < NV ? key[i + 1] : kNotKept, key[i]);
+        }
     const bool have = lane < P.K;
     const int e = have ? min(key_expert(mine), P.E - 1) : 0;
-    const bool live = have && mine > kUnavailable * 0.5;
-    const float lk = live ? clean(load1(row + e)) : 0.0f;
-    const double w = slot_weight<LT>(lk, live, sigmoid, P.renorm, max_l, den);
+    const bool taken = have && mine > kUnavailable * 0.5;
+    const float lk = taken ? clean(load1(row + e)) : 0.0f;
+    const double w = slot_weight<LT>(lk, taken, sigmoid, P.renorm, max_l, den);
     if (have && t < P.T) {
         P.ids[t * P.K + lane] = e;
         P.probs[t * P.K + lane] = (float)(w * (double)P.scale);
@@ -461,7 +566,7 @@ namespace {
 template <int LT, int NV, int LEN, typename L>
 hipError_t select_run(const SelectParams& P, hipStream_t s) {
     constexpr int kTok = kSelWaves * (kWave / LT);
-    const size_t lds = P.n_groups > 1 ? (size_t)kTok * (P.E + 8 + kMaxGroups) * 8 : 0;
+    const size_t lds = P.n_groups > 1 ? (size_t)kTok * P.lds_token * sizeof(double) : 0;
     hipLaunchKernelGGL((router_select_kernel<LT, NV, LEN, L>), dim3((unsigned)((P.T + kTok - 1) / kTok)),
                        dim3(kSelWaves * 64), lds, s, P);
     return hipGetLastError();
@@ -501,7 +606,11 @@ hipError_t backward_type(const SelectParams& P, hipStream_t s) {
 
 }  // namespace
 
-hipError_t launch_router_select(const SelectParams& P, bool bf16, hipStream_t stream) {
+hipError_t launch_router_select(SelectParams P, bool bf16, hipStream_t stream) {
+    // LDS of a token, in doubles: two values a run of four experts where groups
+    // are whole runs, else one an expert; the groups' values; odd, so that the
+    // tokens of a wavefront start in different banks.
+    P.lds_token = ((P.group_size % 4 == 0 ? P.E / 2 : P.E) + P.n_groups) | 1;
     return bf16 ? select_type<uint16_t>(P, stream) : select_type<float>(P, stream);
 }
 hipError_t launch_router_select_backward(const SelectParams& P, bool bf16, hipStream_t stream) {
