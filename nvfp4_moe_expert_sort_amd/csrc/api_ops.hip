@@ -83,12 +83,11 @@ int mx_planes(const nvfp4moe_mxfp4_tensor* q) {
 }
 
 // Workspace of a product: the quantized operand rows, and the row tiles of a
-// grouped one (room for any tile height).
+// grouped one.
 struct MxWork {
     size_t codes, scales, n_tiles, tiles, total;
     int64_t ld_codes, ld_scales;
 };
-constexpr int64_t kMxMinTile = 16;
 bool mx_work(int64_t M, int64_t K, int64_t E, MxWork* w) {
     if (M < 0 || M >= ((int64_t)1 << 31) || K <= 0 || K % 32 != 0 || K >= ((int64_t)1 << 24) || E < 1 || E > kMaxExperts)
         return false;
@@ -99,7 +98,7 @@ bool mx_work(int64_t M, int64_t K, int64_t E, MxWork* w) {
     w->scales = up(M * w->ld_codes, kAlign);
     w->n_tiles = w->scales + up(M * w->ld_scales, kAlign);
     w->tiles = w->n_tiles + kAlign;
-    w->total = w->tiles + up((M / kMxMinTile + std::min(M, E) + 1) * 16, kAlign);
+    w->total = w->tiles + up((M / mx_tile_rows() + std::min(M, E) + 1) * 16, kAlign);
     return true;
 }
 
@@ -121,18 +120,40 @@ int mx_product(const uint16_t* x, int64_t M, int64_t ldx, const int32_t* offsets
     if (M == 0) return NVFP4_OK;
     if (!x || !out || (grouped && !offsets)) return NVFP4_E_NULL;
     if (!aligned(x, 16) || ldx % 8 != 0 || !aligned(out, 2) || !aligned(offsets, 4)) return NVFP4_E_ALIGN;
-    const int bm = mx_tile_rows(M, E);
+    const int bm = mx_tile_rows();
     const int64_t tiles = grouped ? M / bm + std::min(M, E) : (M + bm - 1) / bm;
     const int64_t col_tiles = (N + 63) / 64;  // at most
     if (tiles * col_tiles >= ((int64_t)1 << 31) - 8) return NVFP4_E_SHAPE;
     uint8_t* ws = (uint8_t*)workspace;
     hipStream_t s = (hipStream_t)stream;
+    const MxShape sh = mx_shape(Wq);
+    MxGemmParams p{};
+    p.w_codes = Wq->codes;
+    p.w_scales = Wq->scales;
+    p.row_tiles = (int32_t)sh.row_tiles;
+    p.chunks = (int32_t)sh.chunks;
+    p.quads = (int32_t)sh.quads;
+    p.N = (int32_t)N;
+    p.vec_out = ld_out % 4 == 0 && aligned(out, 8);
+    p.vec_out8 = ld_out % 8 == 0 && aligned(out, 16);
+    p.M = M;
+    p.out = out;
+    p.ld_out = ld_out;
+    const bool up = scale_round == NVFP4MOE_MXFP4_SCALE_RU;
+    if (mx_small(M, E, K)) {
+        p.x = x;
+        p.ldx = ldx;
+        p.cols = (uint32_t)K;
+        p.up = up;
+        p.offsets = offsets;
+        return hip_status(launch_mx_gemm_small(p, E, s));
+    }
     MxRowsParams q{};
     q.x = x;
     q.rows = M;
     q.ld = ldx;
     q.cols = (uint32_t)K;
-    q.up = scale_round == NVFP4MOE_MXFP4_SCALE_RU;
+    q.up = up;
     q.operand = true;
     q.codes = ws + w.codes;
     q.scales = ws + w.scales;
@@ -146,26 +167,13 @@ int mx_product(const uint16_t* x, int64_t M, int64_t ldx, const int32_t* offsets
         q.bm = bm;
     }
     if (launch_mx_quant_rows(q, s) != hipSuccess) return NVFP4_E_HIP;
-    const MxShape sh = mx_shape(Wq);
-    MxGemmParams p{};
     p.a_codes = q.codes;
     p.a_scales = q.scales;
     p.ld_a = w.ld_codes;
     p.ld_as = w.ld_scales;
-    p.w_codes = Wq->codes;
-    p.w_scales = Wq->scales;
-    p.row_tiles = (int32_t)sh.row_tiles;
-    p.chunks = (int32_t)sh.chunks;
-    p.quads = (int32_t)sh.quads;
-    p.N = (int32_t)N;
-    p.vec_out = ld_out % 4 == 0 && aligned(out, 8);
-    p.vec_out8 = ld_out % 8 == 0 && aligned(out, 16);
-    p.M = M;
     p.tiles = q.tiles;
     p.n_tiles = q.n_tiles;
-    p.out = out;
-    p.ld_out = ld_out;
-    return hip_status(launch_mx_gemm(p, tiles, bm, s));
+    return hip_status(launch_mx_gemm(p, tiles, s));
 }
 
 struct Range {

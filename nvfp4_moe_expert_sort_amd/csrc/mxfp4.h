@@ -26,6 +26,14 @@ __device__ __forceinline__ uint32_t mx_max2(uint32_t a, uint32_t b) {
 }
 __device__ __forceinline__ uint32_t mx_abs(uint32_t w) { return w & 0x7FFF7FFFu; }
 
+// Largest magnitude (BF16 bits) of a block whose elements four neighbouring lanes hold, eight each.
+__device__ __forceinline__ uint32_t mx_block_max(u32x4 v) {
+    uint32_t m = mx_max2(mx_max2(mx_abs(v[0]), mx_abs(v[1])), mx_max2(mx_abs(v[2]), mx_abs(v[3])));
+    m = max(m & 0xFFFFu, m >> 16);
+    m = max(m, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)m, 0xB1, 0xF, 0xF, true));         // lanes 1 0 3 2
+    return max(m, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)m, 0x4E, 0xF, 0xF, true));  // lanes 2 3 0 1
+}
+
 // Scale byte k + 127 of a block whose largest magnitude has the BF16 bits m
 // (15 bits): with m = 1.f x 2^e, k = e - 2 (floor), or e - 1 where 1.f > 1.5
 // and the scale is rounded up so that m <= 6 x 2^k.  Scales end at 2^-127,

@@ -6,13 +6,11 @@
 // the kernel, the tile and the number of rows: a row's result has the same
 // bits in every batch.
 //
-//   mx_gemm_wide_kernel    128 rows x 256 columns per workgroup: 8 x 4 tiles of
-//                          16 x 16 per wave; activations shared through LDS
-//                          (direct loads, two 256-column buffers), each wave's
-//                          weights straight from memory into registers
-//   mx_gemm_direct_kernel  16 MT rows x 16 columns per wave, both operands
-//                          straight from memory: few rows, bound by reading
-//                          the weights
+//   mx_gemm_wide_kernel    tiles of up to 128 rows x 256 or 64 columns:
+//                          activations shared through LDS by direct loads, each
+//                          wave's weights straight from memory into registers
+//   mx_gemm_small_kernel   up to about 32 rows a matrix: 16 columns per wave,
+//                          activations quantized into LDS by the workgroup
 #include <type_traits>
 
 #include "mxfp4.h"
@@ -31,16 +29,15 @@ struct MxTile {
 // list (workgroups are dealt to them round-robin), in which eight row tiles
 // walk through the column tiles together, so that they share an L2.
 __device__ __forceinline__ MxTile mx_tile(const MxGemmParams& P, int bm, int bn) {
-    const int32_t nm = P.tiles ? *P.n_tiles : (int32_t)((P.M + bm - 1) / bm);
-    const int64_t total = (int64_t)nm * P.col_tiles, per = (total + 7) / 8;
-    const int64_t at = (int64_t)(blockIdx.x >> 3);
-    const int64_t idx = (int64_t)(blockIdx.x & 7) * per + at;
+    // (tiles x column tiles < 2^31, checked on the host)
+    const uint32_t nm = P.tiles ? (uint32_t)*P.n_tiles : (uint32_t)((P.M + bm - 1) / bm);
+    const uint32_t total = nm * (uint32_t)P.col_tiles, per = (total + 7) / 8;
+    const uint32_t at = blockIdx.x >> 3, idx = (blockIdx.x & 7) * per + at;
     MxTile t{0, 0, 0, 0, at < per && idx < total};
     if (!t.live) return t;
-    const int32_t band = (int32_t)(idx / (8 * (int64_t)P.col_tiles));
-    const int32_t in = (int32_t)(idx - (int64_t)band * 8 * P.col_tiles);
-    const int32_t high = min(8, nm - band * 8);
-    const int32_t nt = in / high, mt = band * 8 + in - nt * high;
+    const uint32_t band = idx / (8 * (uint32_t)P.col_tiles), in = idx - band * 8 * (uint32_t)P.col_tiles;
+    const uint32_t high = min(8u, nm - band * 8);
+    const int32_t nt = (int32_t)(in / high), mt = (int32_t)(band * 8 + in - (uint32_t)nt * high);
     t.n0 = nt * bn;
     if (P.tiles) {
         const int4 e = P.tiles[mt];
@@ -90,8 +87,7 @@ __device__ __forceinline__ f32x4 mx_mfma_sel(int sel, u32x4 w, u32x4 a, f32x4 ac
 
 }  // namespace
 
-constexpr int kWideMT = 8, kWideNT = 4;
-constexpr int kWideBM = kWideMT * 16, kWideBN = kWideNT * 16 * 4;
+constexpr int kWideBM = 128;
 constexpr int kWideStages = 3;  // 256-column steps of activations in LDS
 
 struct WideLds {
@@ -113,17 +109,19 @@ __device__ __forceinline__ uint32_t lds_addr(const void* p) {
     return (uint32_t)(uintptr_t)(const __attribute__((address_space(3))) void*)p;
 }
 
-// The product of a tile of up to MT 16-row subtiles.  Loop over 128-column
-// chunks, four of them (a quad, one scale word) unrolled:
+// The product of a tile of up to MT 16-row subtiles, NT 16-column tiles per
+// wave.  Loop over 128-column chunks, four of them (a quad, one scale word)
+// unrolled:
 //   - activations come as 256-column steps, three LDS buffers deep: step s + 2
 //     is requested when all waves have read step s - 1;
-//   - a wave's weights are loaded two chunks ahead, each register group as
+//   - a wave's weights are loaded kAhead chunks ahead, each register group as
 //     soon as its last product has been issued;
 //   - the next chunk's activation fragments are read under the last column
 //     tile's products.
-template <int MT>
+template <int MT, int NT>
 __device__ __forceinline__ void wide_tile(const MxGemmParams& P, const MxTile& T, WideLds& S) {
     constexpr int kDma = MT / 2;  // loads per wave and step
+    constexpr int kAhead = NT == 1 ? 4 : 2;
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), q = lane >> 4, r = lane & 15;
     const int32_t chunks = P.chunks, quads = P.quads, steps = (chunks + 1) / 2;
 
@@ -152,30 +150,31 @@ __device__ __forceinline__ void wide_tile(const MxGemmParams& P, const MxTile& T
     auto stage_scales = [&](int g) {
         if (lane < MT * 4) dma16(s_base + (int64_t)min(g, quads - 1) * 16, ssrc, lds_s + (uint32_t)(g & 1) * (kWideBM * 16));
     };
-    const uint8_t* wc[kWideNT];
-    const uint8_t* wsp[kWideNT];
+    const uint8_t* wc[NT];
+    const uint8_t* wsp[NT];
 #pragma unroll
-    for (int t = 0; t < kWideNT; t++) {  // column tiles past the matrix repeat its last one
-        const int64_t tile = (int64_t)T.mat * P.row_tiles + min(T.n0 / 16 + wave * kWideNT + t, P.row_tiles - 1);
+    for (int t = 0; t < NT; t++) {  // column tiles past the matrix repeat its last one
+        const int64_t tile = (int64_t)T.mat * P.row_tiles + min(T.n0 / 16 + wave * NT + t, P.row_tiles - 1);
         wc[t] = P.w_codes + tile * chunks * 1024;
         wsp[t] = P.w_scales + tile * quads * 256;
     }
     const uint32_t lane16 = lane * 16, lane4 = lane * 4;
-    f32x4 acc[MT][kWideNT];
+    f32x4 acc[MT][NT];
 #pragma unroll
     for (int i = 0; i < MT; i++)
 #pragma unroll
-        for (int t = 0; t < kWideNT; t++) acc[i][t] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-    u32x4 w[2][kWideNT], a[MT];
-    uint32_t ws[kWideNT], wsn[kWideNT], as[MT];
+        for (int t = 0; t < NT; t++) acc[i][t] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+    u32x4 w[kAhead][NT], a[MT];
+    uint32_t ws[NT], wsn[NT], as[MT];
     const int a_off[2] = {r * 128 + ((q ^ ((r >> 1) & 7)) << 4), r * 128 + (((4 + q) ^ ((r >> 1) & 7)) << 4)};
     auto load_w = [&](int c, int t) { return *reinterpret_cast<const u32x4*>(wc[t] + (int64_t)min(c, chunks - 1) * 1024 + lane16); };
     auto load_ws = [&](int g, int t) { return *reinterpret_cast<const uint32_t*>(wsp[t] + (int64_t)min(g, quads - 1) * 256 + lane4); };
     auto read_a = [&](int c, int i) { return *reinterpret_cast<const u32x4*>(&S.a[(c >> 1) % kWideStages][a_off[c & 1] + i * 2048]); };
     auto read_s = [&](int g, int i) { return *reinterpret_cast<const uint32_t*>(&S.s[g & 1][(i * 16 + r) * 16 + q * 4]); };
-    // Step s (and the scales requested with it) has landed for every wave:
-    // at least kDma loads, step s + 1's, were issued after it.  Every wave has
-    // read step s - 1, whose buffer step s + 2 takes.
+    // Waits until a step has landed for every wave; every wave has then also
+    // read the step before, whose buffer the next request takes.  Loads return
+    // in order and the kDma loads of the next step were issued after it.  (A
+    // longer count that leaves the weights in flight too measured the same.)
     auto arrive = [&]() {
         asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" ::"n"(kDma) : "memory");
         __builtin_amdgcn_s_barrier();
@@ -185,11 +184,11 @@ __device__ __forceinline__ void wide_tile(const MxGemmParams& P, const MxTile& T
     stage(0);
     stage(1);
 #pragma unroll
-    for (int t = 0; t < kWideNT; t++) ws[t] = load_ws(0, t);
+    for (int t = 0; t < NT; t++) ws[t] = load_ws(0, t);
 #pragma unroll
-    for (int t = 0; t < kWideNT; t++) w[0][t] = load_w(0, t);
+    for (int b = 0; b < kAhead; b++)
 #pragma unroll
-    for (int t = 0; t < kWideNT; t++) w[1][t] = load_w(1, t);
+        for (int t = 0; t < NT; t++) w[b][t] = load_w(b, t);
     arrive();
     stage_scales(1);
     stage(2);
@@ -210,13 +209,13 @@ __device__ __forceinline__ void wide_tile(const MxGemmParams& P, const MxTile& T
         constexpr int H = decltype(half)::value;
 #pragma unroll
         for (int b = 0; b < 2; b++) {
-            constexpr int kLast = kWideNT - 1;
-            const int c = g * 4 + H + b;
+            constexpr int kLast = NT - 1;
+            const int c = g * 4 + H + b, k = (H + b) % kAhead;
 #pragma unroll
             for (int t = 0; t < kLast; t++) {
 #pragma unroll
-                for (int i = 0; i < MT; i++) acc[i][t] = mx_mfma_sel(H + b, w[b][t], a[i], acc[i][t], ws[t], as[i]);
-                w[b][t] = load_w(c + 2, t);
+                for (int i = 0; i < MT; i++) acc[i][t] = mx_mfma_sel(H + b, w[k][t], a[i], acc[i][t], ws[t], as[i]);
+                w[k][t] = load_w(c + kAhead, t);
                 pin(t);
             }
             if (b == 1) {
@@ -226,22 +225,22 @@ __device__ __forceinline__ void wide_tile(const MxGemmParams& P, const MxTile& T
             }
 #pragma unroll
             for (int i = 0; i < MT; i++) {
-                acc[i][kLast] = mx_mfma_sel(H + b, w[b][kLast], a[i], acc[i][kLast], ws[kLast], as[i]);
+                acc[i][kLast] = mx_mfma_sel(H + b, w[k][kLast], a[i], acc[i][kLast], ws[kLast], as[i]);
                 a[i] = read_a(c + 1, i);
                 if (H + b == 3) as[i] = read_s(g + 1, i);
             }
-            w[b][kLast] = load_w(c + 2, kLast);
+            w[k][kLast] = load_w(c + kAhead, kLast);
             pin(kLast);
         }
     };
     int g = 0;
     for (; (g + 1) * 4 <= chunks; g++) {
 #pragma unroll
-        for (int t = 0; t < kWideNT; t++) wsn[t] = load_ws(g + 1, t);
+        for (int t = 0; t < NT; t++) wsn[t] = load_ws(g + 1, t);
         step(g, std::integral_constant<int, 0>{});
         step(g, std::integral_constant<int, 2>{});
 #pragma unroll
-        for (int t = 0; t < kWideNT; t++) ws[t] = wsn[t];
+        for (int t = 0; t < NT; t++) ws[t] = wsn[t];
     }
     // The last, partial quad: activations are padded with zeros to whole
     // steps, so an odd last chunk's partner adds nothing.
@@ -249,126 +248,214 @@ __device__ __forceinline__ void wide_tile(const MxGemmParams& P, const MxTile& T
         step(g, std::integral_constant<int, 0>{});
         if (g * 4 + 2 < chunks) step(g, std::integral_constant<int, 2>{});
     }
-    // Epilogue: the wave's outputs go through LDS, up to 64 rows at a time, so
-    // that eight lanes store a row's whole 128 bytes.  The 16-byte pieces of a
-    // row are stored at piece ^ row % 8.
+    // Epilogue: the outputs go through LDS, up to 64 rows at a time, so that
+    // eight lanes store 128 bytes of a row: a wave's own 64 columns, or with
+    // NT = 1 the workgroup's.  The 16-byte pieces of a row are stored at
+    // piece ^ row % 8.
     asm volatile("s_waitcnt vmcnt(0)" ::: "memory");  // no load into LDS is in flight
     __syncthreads();
-    uint8_t* mine = reinterpret_cast<uint8_t*>(&S) + wave * (64 * 128);
-    const int32_t n0 = T.n0 + wave * (kWideNT * 16);
+    constexpr bool kOwn = NT == 4;
+    constexpr int kRows = MT < 4 ? MT * 16 : 64;
+    uint8_t* out = reinterpret_cast<uint8_t*>(&S) + (kOwn ? wave * (64 * 128) : 0);
+    const int piece0 = kOwn ? 0 : wave * 2, reader = kOwn ? lane : threadIdx.x;
+    const int32_t n = T.n0 + (kOwn ? wave * 64 : 0) + (reader & 7) * 8;
 #pragma unroll
     for (int i0 = 0; i0 < MT; i0 += 4) {
 #pragma unroll
         for (int i = i0; i < MT && i < i0 + 4; i++)
 #pragma unroll
-            for (int t = 0; t < kWideNT; t++) {
+            for (int t = 0; t < NT; t++) {
                 const f32x4 v = acc[i][t];
                 const int row = (i - i0) * 16 + r;
-                *reinterpret_cast<u32x2*>(mine + row * 128 + (((t * 2 + (q >> 1)) ^ (row & 7)) << 4) + (q & 1) * 8) =
+                *reinterpret_cast<u32x2*>(out + row * 128 + (((piece0 + t * 2 + (q >> 1)) ^ (row & 7)) << 4) + (q & 1) * 8) =
                     u32x2{bf16_hw(v[0]) | (bf16_hw(v[1]) << 16), bf16_hw(v[2]) | (bf16_hw(v[3]) << 16)};
             }
-        constexpr int kRows = MT < 4 ? MT * 16 : 64;
-        const int rows = min(T.rows - i0 * 16, min((MT - i0) * 16, kRows)), n = n0 + (lane & 7) * 8;
-        __builtin_amdgcn_wave_barrier();
-        for (int row = lane >> 3; row < rows; row += 8) {
-            const u32x4 v = *reinterpret_cast<const u32x4*>(mine + row * 128 + (((lane & 7) ^ (row & 7)) << 4));
+        const int rows = min(T.rows - i0 * 16, min((MT - i0) * 16, kRows));
+        if (kOwn)
+            __builtin_amdgcn_wave_barrier();
+        else
+            __syncthreads();
+        for (int row = reader >> 3; row < rows; row += kOwn ? 8 : 32) {
+            const u32x4 v = *reinterpret_cast<const u32x4*>(out + row * 128 + (((reader & 7) ^ (row & 7)) << 4));
             mx_store8(P, (int64_t)T.row0 + i0 * 16 + row, n, v);
         }
-        __builtin_amdgcn_wave_barrier();
+        if (kOwn)
+            __builtin_amdgcn_wave_barrier();
+        else
+            __syncthreads();
     }
 }
 
 }  // namespace
 
+template <int NT>
 __global__ void __launch_bounds__(256, 2) mx_gemm_wide_kernel(MxGemmParams P) {
     __shared__ __attribute__((aligned(1024))) WideLds S;
-    const MxTile T = mx_tile(P, kWideBM, kWideBN);
+    const MxTile T = mx_tile(P, kWideBM, NT * 64);
     if (!T.live) return;
     if (T.rows > 96)
-        wide_tile<8>(P, T, S);
+        wide_tile<8, NT>(P, T, S);
     else if (T.rows > 64)
-        wide_tile<6>(P, T, S);
+        wide_tile<6, NT>(P, T, S);
     else if (T.rows > 32)
-        wide_tile<4>(P, T, S);
+        wide_tile<4, NT>(P, T, S);
     else
-        wide_tile<2>(P, T, S);
+        wide_tile<2, NT>(P, T, S);
 }
 
-template <int MT>
-__global__ void __launch_bounds__(256) mx_gemm_direct_kernel(MxGemmParams P) {
-    const MxTile T = mx_tile(P, 16 * MT, 64);
-    if (!T.live) return;
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, q = lane >> 4, r = lane & 15;
-    const int32_t chunks = P.chunks, nt = T.n0 / 16 + wave;
-    if (nt >= P.row_tiles) return;
-    const int64_t tile = (int64_t)T.mat * P.row_tiles + nt;
-    const uint8_t* wc = P.w_codes + tile * chunks * 1024 + lane * 16;
-    const uint8_t* wsp = P.w_scales + tile * P.quads * 256 + lane * 4;
-    const uint8_t *ac[MT], *asp[MT];
+// Few rows: workgroup (x, y) takes every gridDim.x-th group of 64 columns of
+// matrix y, 16 per wave, and its rows kSmallMT * 16 at a time.  It quantizes the
+// rows itself, into LDS, while its first weights (12 KiB a wave) are on their way:
+// no launch, table or round trip through memory comes before them.  After that
+// it streams: each wave keeps a ring of kSmallRing quads of weights in flight
+// across its column groups.
+constexpr int kSmallRing = 3, kSmallMT = 2, kSmallBM = 16 * kSmallMT;
+
+__global__ void __launch_bounds__(256, 4) mx_gemm_small_kernel(MxGemmParams P) {
+    extern __shared__ __attribute__((aligned(16))) uint8_t smem[];  // codes [kSmallBM][lds_codes], scale words [kSmallBM][lds_scales]
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), q = lane >> 4, r = lane & 15;
+    int64_t row0 = 0, row1 = P.M;
+    if (P.offsets) {
+        // as build_tiles: clamped to [0, M], the largest of offsets 0..e
+        const int e = blockIdx.y;
+        int32_t lo = 0;
+        for (int i = lane; i <= e; i += 64) lo = max(lo, min(P.offsets[i], (int32_t)P.M));
+        const int32_t hi = min(P.offsets[e + 1], (int32_t)P.M);
 #pragma unroll
-    for (int i = 0; i < MT; i++) {
-        const int64_t row = T.row0 + min(i * 16 + r, T.rows - 1);
-        ac[i] = P.a_codes + row * P.ld_a + q * 16;
-        asp[i] = P.a_scales + row * P.ld_as + q * 4;
+        for (int o = 32; o > 0; o >>= 1) lo = max(lo, __shfl_xor(lo, o, kWave));
+        row0 = __builtin_amdgcn_readfirstlane(lo);
+        row1 = hi;
+        if (row0 >= row1) return;
     }
-    f32x4 acc[MT];
-#pragma unroll
-    for (int i = 0; i < MT; i++) acc[i] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-    struct Quad {
-        u32x4 w[4], a[MT][4];
-        uint32_t ws, as[MT];
+    const int32_t chunks = P.chunks, quads = P.quads;
+    const int32_t col_groups = (P.N + 63) / 64, mine = (col_groups - blockIdx.x + gridDim.x - 1) / gridDim.x;  // this workgroup's
+    const int64_t mat_tile = (int64_t)blockIdx.y * P.row_tiles;
+    const uint32_t lane16 = lane * 16, lane4 = lane * 4;
+    const uint32_t groups = (uint32_t)chunks * 16;  // 8-column groups of a row, padded to whole chunks
+    uint8_t* sc = smem + kSmallBM * P.lds_codes;
+    u32x4 w[kSmallRing][4];
+    uint32_t ws[kSmallRing];
+    // The load cursor: quad lg of column group lj (past the last it repeats the last quad).
+    int32_t lg, lj;
+    const uint8_t *lc, *ls;
+    auto column_group = [&](int j) {  // columns past the matrix repeat its last 16, and are not stored
+        const int64_t tile = mat_tile + min(((int32_t)blockIdx.x + j * (int32_t)gridDim.x) * 4 + wave, P.row_tiles - 1);
+        lc = P.w_codes + tile * chunks * 1024;
+        ls = P.w_scales + tile * quads * 256;
     };
-    auto load = [&](Quad& b, int g) {
-        g = min(g, P.quads - 1);
-#pragma unroll
-        for (int cc = 0; cc < 4; cc++) {
-            const int64_t c = min(g * 4 + cc, chunks - 1);
-            b.w[cc] = *reinterpret_cast<const u32x4*>(wc + c * 1024);
-#pragma unroll
-            for (int i = 0; i < MT; i++) b.a[i][cc] = *reinterpret_cast<const u32x4*>(ac[i] + c * 64);
-        }
-        b.ws = *reinterpret_cast<const uint32_t*>(wsp + (int64_t)g * 256);
-#pragma unroll
-        for (int i = 0; i < MT; i++) b.as[i] = *reinterpret_cast<const uint32_t*>(asp[i] + (int64_t)g * 16);
-    };
-    auto mul = [&](const Quad& b, int g) {
+    auto load = [&](int slot) {
 #pragma unroll
         for (int cc = 0; cc < 4; cc++)
-            if (g * 4 + cc < chunks) {
-#pragma unroll
-                for (int i = 0; i < MT; i++) acc[i] = mx_mfma_sel(cc, b.w[cc], b.a[i][cc], acc[i], b.ws, b.as[i]);
+            w[slot][cc] = *reinterpret_cast<const u32x4*>(lc + (int64_t)min(lg * 4 + cc, chunks - 1) * 1024 + lane16);
+        ws[slot] = *reinterpret_cast<const uint32_t*>(ls + (int64_t)lg * 256 + lane4);
+        if (++lg == quads) {
+            if (lj + 1 < mine) {
+                lg = 0;
+                column_group(++lj);
+            } else {
+                lg = quads - 1;
             }
+        }
     };
-    Quad b0, b1;
-    load(b0, 0);
-    for (int g = 0; g < P.quads; g += 2) {
-        load(b1, g + 1);
-        mul(b0, g);
-        load(b0, g + 2);
-        mul(b1, g + 1);
-    }
+    for (int64_t at = row0; at < row1; at += kSmallBM) {
+        const uint32_t rows = (uint32_t)min<int64_t>(kSmallBM, row1 - at);
+        lg = lj = 0;
+        column_group(0);
 #pragma unroll
-    for (int i = 0; i < MT; i++)
-        if (i * 16 + r < T.rows) mx_store4(P, (int64_t)T.row0 + i * 16 + r, nt * 16 + q * 4, acc[i]);
-}
-
-// Rows per tile of the kernel that mx_gemm launches for `rows` rows over E
-// matrices.
-int mx_tile_rows(int64_t rows, int64_t E) {
-    const int64_t per = (rows + E - 1) / E;
-    return per <= 16 ? 16 : per <= 32 ? 32 : per <= 64 ? 64 : kWideBM;
-}
-
-hipError_t launch_mx_gemm(MxGemmParams P, int64_t tiles_bound, int bm, hipStream_t stream) {
-    P.col_tiles = bm == kWideBM ? (P.N + kWideBN - 1) / kWideBN : (P.N + 63) / 64;
-    const int64_t blocks = (tiles_bound * P.col_tiles + 7) / 8 * 8;
-    const dim3 grid((unsigned)blocks), wg(256);
-    switch (bm) {
-        case 16: hipLaunchKernelGGL(mx_gemm_direct_kernel<1>, grid, wg, 0, stream, P); break;
-        case 32: hipLaunchKernelGGL(mx_gemm_direct_kernel<2>, grid, wg, 0, stream, P); break;
-        case 64: hipLaunchKernelGGL(mx_gemm_direct_kernel<4>, grid, wg, 0, stream, P); break;
-        default: hipLaunchKernelGGL(mx_gemm_wide_kernel, grid, wg, 0, stream, P); break;
+        for (int s = 0; s < kSmallRing; s++) load(s);
+        for (uint32_t i0 = threadIdx.x; i0 < rows * groups; i0 += 4 * 256) {
+            u32x4 v[4];
+            uint32_t row[4], col[4];
+#pragma unroll
+            for (int u = 0; u < 4; u++) {
+                const uint32_t i = i0 + u * 256;
+                row[u] = __umulhi(i, P.groups_magic);
+                col[u] = (i - row[u] * groups) * 8;
+                v[u] = u32x4{0u, 0u, 0u, 0u};
+                if (i < rows * groups && col[u] < P.cols) v[u] = *reinterpret_cast<const u32x4*>(P.x + (at + row[u]) * P.ldx + col[u]);
+            }
+#pragma unroll
+            for (int u = 0; u < 4; u++) {
+                const uint32_t byte = mx_scale_byte(mx_block_max(v[u]), P.up);
+                if (i0 + u * 256 >= rows * groups) continue;
+                *reinterpret_cast<uint32_t*>(smem + row[u] * P.lds_codes + col[u] / 2) = mx_encode8(v[u], byte);
+                const uint32_t b = col[u] / 32, c = b >> 2;
+                if ((threadIdx.x & 3) == 0) sc[row[u] * P.lds_scales + (c >> 2) * 16 + (b & 3) * 4 + (c & 3)] = (uint8_t)byte;
+            }
+        }
+        __syncthreads();
+        const bool two = rows > 16;
+        f32x4 acc[kSmallMT] = {};
+        int32_t g = 0, j = 0;  // the product cursor
+        while (j < mine) {
+#pragma unroll
+            for (int s = 0; s < kSmallRing; s++) {
+                if (j >= mine) break;
+#pragma unroll
+                for (int i = 0; i < kSmallMT; i++) {
+                    if (i > 0 && !two) break;
+                    const uint32_t as = *reinterpret_cast<const uint32_t*>(sc + (i * 16 + r) * P.lds_scales + g * 16 + q * 4);
+#pragma unroll
+                    for (int cc = 0; cc < 4; cc++)
+                        if (g * 4 + cc < chunks) {
+                            const u32x4 a = *reinterpret_cast<const u32x4*>(smem + (i * 16 + r) * P.lds_codes + (g * 4 + cc) * 64 + q * 16);
+                            acc[i] = mx_mfma_sel(cc, w[s][cc], a, acc[i], ws[s], as);
+                        }
+                }
+                load(s);
+                if (++g == quads) {
+                    const int32_t n = ((int32_t)blockIdx.x + j * (int32_t)gridDim.x) * 64 + wave * 16 + q * 4;
+                    for (int i = 0; i < kSmallMT; i++) {
+                        if (i * 16 + r < (int)rows) mx_store4(P, at + i * 16 + r, n, acc[i]);
+                        acc[i] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+                    }
+                    g = 0;
+                    j++;
+                }
+            }
+        }
+        if (at + kSmallBM < row1) __syncthreads();  // the next rows go into the same LDS
     }
+}
+
+// The small kernel is for up to 16 rows a matrix on average (a rule on what the
+// host knows; a matrix with more takes them kSmallBM at a time) of up to
+// kSmallElements elements together, which each of its workgroups quantizes, in
+// rows that fit LDS.
+constexpr int64_t kSmallRows = 16, kSmallElements = 32768;
+constexpr int32_t kSmallCols = 4096;
+constexpr int64_t kSmallBlocks = 1024, kWideBlocks = 144;
+bool mx_small(int64_t rows, int64_t E, int64_t K) {
+    return rows <= kSmallRows * E && rows * K <= kSmallElements * E && K <= kSmallCols;
+}
+
+hipError_t launch_mx_gemm_small(MxGemmParams P, int64_t E, hipStream_t stream) {
+    // Rows start 16 bytes further in the banks than the row before.
+    P.lds_codes = (P.chunks * 64 + 255) / 256 * 256 + 16;
+    P.lds_scales = (P.quads * 16 + 255) / 256 * 256 + 16;
+    P.groups_magic = (uint32_t)((((uint64_t)1 << 32) + P.chunks * 16 - 1) / (P.chunks * 16));
+    // About four workgroups for each of 256 CUs, as far as the columns give them.
+    const int64_t col_groups = (P.N + 63) / 64, used = E < P.M ? E : P.M;
+    int64_t share = (kSmallBlocks + used - 1) / used;
+    if (share > col_groups) share = col_groups;
+    const int64_t each = (col_groups + share - 1) / share;  // evenly
+    share = (col_groups + each - 1) / each;
+    hipLaunchKernelGGL(mx_gemm_small_kernel, dim3((unsigned)share, (unsigned)E), dim3(256),
+                       kSmallBM * (P.lds_codes + P.lds_scales), stream, P);
+    return hipGetLastError();
+}
+
+// The column width of a tile: 256, or 64 where 256 would leave CUs without a
+// workgroup.
+int mx_tile_rows() { return kWideBM; }
+hipError_t launch_mx_gemm(MxGemmParams P, int64_t tiles_bound, hipStream_t stream) {
+    const bool wide = tiles_bound * ((P.N + 255) / 256) >= kWideBlocks;
+    P.col_tiles = wide ? (P.N + 255) / 256 : (P.N + 63) / 64;
+    const dim3 grid((unsigned)((tiles_bound * P.col_tiles + 7) / 8 * 8)), wg(256);
+    if (wide)
+        hipLaunchKernelGGL(mx_gemm_wide_kernel<4>, grid, wg, 0, stream, P);
+    else
+        hipLaunchKernelGGL(mx_gemm_wide_kernel<1>, grid, wg, 0, stream, P);
     return hipGetLastError();
 }
 

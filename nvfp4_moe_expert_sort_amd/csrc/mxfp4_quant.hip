@@ -119,11 +119,7 @@ __global__ void __launch_bounds__(256) mx_quant_rows_kernel(MxRowsParams P) {
     }
 #pragma unroll
     for (int u = 0; u < kMxUnroll; u++) {
-        uint32_t m = mx_max2(mx_max2(mx_abs(v[u][0]), mx_abs(v[u][1])), mx_max2(mx_abs(v[u][2]), mx_abs(v[u][3])));
-        m = max(m & 0xFFFFu, m >> 16);
-        m = max(m, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)m, 0xB1, 0xF, 0xF, true));  // lanes 1 0 3 2
-        m = max(m, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)m, 0x4E, 0xF, 0xF, true));  // lanes 2 3 0 1
-        const uint32_t byte = mx_scale_byte(m, P.up);
+        const uint32_t byte = mx_scale_byte(mx_block_max(v[u]), P.up);
         const uint32_t code = mx_encode8(v[u], byte);
         if (row[u] == 0xFFFFFFFFu) continue;
         *reinterpret_cast<uint32_t*>(P.codes + (int64_t)row[u] * P.ld_codes + col[u] / 2) = code;

@@ -177,9 +177,19 @@ struct MxGemmParams {
     const int32_t* n_tiles;
     uint16_t* out;
     int64_t ld_out;
+    // mx_gemm_small: BF16 rows, quantized in the kernel
+    const uint16_t* x;
+    int64_t ldx;
+    uint32_t cols;
+    bool up;
+    const int32_t* offsets;  // [E + 1] of a grouped product, or null
+    int32_t lds_codes, lds_scales;  // bytes per row in LDS; set by the launcher
+    uint32_t groups_magic;   // ceil(2^32 / 8-column groups of a row); set by the launcher
 };
-int mx_tile_rows(int64_t rows, int64_t E);
-hipError_t launch_mx_gemm(MxGemmParams P, int64_t tiles_bound, int bm, hipStream_t stream);
+bool mx_small(int64_t rows, int64_t E, int64_t K);
+hipError_t launch_mx_gemm_small(MxGemmParams P, int64_t E, hipStream_t stream);
+int mx_tile_rows();  // rows of a product's row tile
+hipError_t launch_mx_gemm(MxGemmParams P, int64_t tiles_bound, hipStream_t stream);
 
 // Gradient norm and clipping (grad_clip.hip): up to kGradChunk consecutive
 // elements of one tensor; `head` of them precede the first 16-byte boundary.
