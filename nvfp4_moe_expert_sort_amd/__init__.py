@@ -7,9 +7,7 @@ missing: there is no CPU fallback.
 """
 from __future__ import annotations
 
-import contextlib
 import ctypes
-import functools
 import os
 
 HERE = os.path.dirname(os.path.abspath(__file__))
@@ -440,310 +438,16 @@ def selftest_batch_invariance(cfg: Config, weights: QuantWeights, seed: int, n_p
     return st, dict(n_compared=rep[0], n_mismatched=rep[1], first_bad_probe=rep[2], first_bad_batch=rep[3])
 
 
-# --- expert selection, MXFP4 products, gradient clipping -------------------------------------------
-#
-# These calls take a few microseconds on the GPU at decode sizes, so the binding's own time counts: arguments are
-# checked once, pointers and the raw stream go to ctypes as integers, and the device and stream are switched only where
-# they are not the current ones.
+# --- expert selection, MXFP4 products, gradient clipping: ops.py, loaded (with torch) on first use -----
 
-def _elsewhere(t, stream):
-    """Whether `t`'s device or `stream` is not the current one (then the call runs again inside _there)."""
-    import torch
-    if not t.is_cuda:
-        raise ValueError(f"a GPU tensor is needed, got one on {t.device}")
-    return stream is not None or t.device.index != torch.cuda.current_device()
+_OPS = ("router_logits", "router_select", "router_select_backward", "mxfp4_quantize", "mxfp4_dequantize", "Mxfp4Weights",
+        "mxfp4_workspace_bytes", "mxfp4_alloc_workspace", "mxfp4_linear", "mxfp4_grouped_linear", "GradSet",
+        "clip_grad_norm")
 
 
-@contextlib.contextmanager
-def _there(t, stream):
-    """`t`'s device and `stream` (default: that device's current one) made current, so that outputs are allocated
-    where they are used."""
-    import torch
-    if stream is not None and stream.device != t.device:
-        raise ValueError(f"the stream is on {stream.device}, the tensors on {t.device}")
-    with torch.cuda.device(t.device), torch.cuda.stream(stream):
-        yield
-
-
-def _raw_stream(t):
-    import torch
-    return torch._C._cuda_getCurrentRawStream(t.device.index)
-
-
-def _need(where, t, name, dtypes, shape, device, contiguous=True):
-    """ValueError unless t has one of the types, the shape and the device, with rows of consecutive elements."""
-    if t.dtype not in dtypes or t.shape != shape or t.device != device:
-        raise ValueError(f"{where}: {name} must be {' or '.join(str(d) for d in dtypes)} of shape {tuple(shape)} on "
-                         f"{device}, got {t.dtype} {tuple(t.shape)} on {t.device}")
-    if not t.is_contiguous() and (contiguous or (t.numel() and t.shape[-1] > 1 and t.stride(-1) != 1)):
-        raise ValueError(f"{where}: {name} must {'be contiguous' if contiguous else 'have consecutive columns'}")
-
-
-def _ld(t):
-    """Elements from one row of a matrix to the next."""
-    rows, cols = t.shape
-    return t.stride(0) if rows > 1 else max(t.stride(0), cols)
-
-
-@functools.lru_cache(None)
-def _bf16_types():
-    import torch
-    return (torch.bfloat16, torch.int16, torch.uint16)
-
-
-@functools.lru_cache(256)
-def _select_config(*fields):
-    """A pointer to the SelectConfig of these values."""
-    return ctypes.pointer(SelectConfig(*fields))
-
-
-def router_logits(x, w_router, out=None, stream=None):
-    """nvfp4moe_router_logits: x [T,H] BF16, w_router [E,H] BF16 -> logits [T,E] f32 (router_topk's)."""
-    import torch
-    if _elsewhere(x, stream):
-        with _there(x, stream):
-            return router_logits(x, w_router, out)
-    T, H = x.shape
-    E = w_router.shape[0]
-    _need("router_logits", x, "x", _bf16_types(), (T, H), x.device)
-    _need("router_logits", w_router, "w_router", _bf16_types(), (E, H), x.device)
-    if out is None:
-        out = torch.empty((T, E), dtype=torch.float32, device=x.device)
-    else:
-        _need("router_logits", out, "out", (torch.float32,), (T, E), x.device)
-    _check(lib().nvfp4moe_router_logits(x.data_ptr(), T, H, w_router.data_ptr(), E, out.data_ptr(), _raw_stream(x)),
-           "nvfp4moe_router_logits")
-    return out
-
-
-def _logits_type(where, logits, bias):
-    """Checks logits and bias; their type as the library names it."""
-    import torch
-    _need(where, logits, "logits", (torch.float32, torch.bfloat16), logits.shape, logits.device, contiguous=False)
-    if bias is not None:
-        _need(where, bias, "bias", (torch.float32,), logits.shape[1:], logits.device)
-    return F32 if logits.dtype == torch.float32 else BF16
-
-
-def router_select(logits, k: int, bias=None, score: int = SCORE_SOFTMAX, renormalize: bool = True, scale: float = 1.0,
-                  n_groups: int = 1, top_groups: int = 1, group_score: int = GROUP_MAX, out=None, stream=None):
-    """nvfp4moe_router_select: logits [T,E] f32 or bf16 (rows may be strided), bias [E] f32 -> (ids [T,k] int32,
-    probs [T,k] f32); `out` may hold the two, preallocated."""
-    import torch
-    T, E = logits.shape
-    kind = _logits_type("router_select", logits, bias)
-    if _elsewhere(logits, stream):
-        with _there(logits, stream):
-            return router_select(logits, k, bias, score, renormalize, scale, n_groups, top_groups, group_score, out)
-    if out is None:
-        ids = torch.empty((T, max(k, 0)), dtype=torch.int32, device=logits.device)
-        probs = torch.empty((T, max(k, 0)), dtype=torch.float32, device=logits.device)
-    else:
-        ids, probs = out
-        _need("router_select", ids, "out ids", (torch.int32,), (T, k), logits.device)
-        _need("router_select", probs, "out probs", (torch.float32,), (T, k), logits.device)
-    cfg = _select_config(E, k, score, 1 if renormalize else 0, scale, n_groups, top_groups, group_score, kind)
-    st = lib().nvfp4moe_router_select(cfg, logits.data_ptr(), _ld(logits), T, None if bias is None else bias.data_ptr(),
-                                      ids.data_ptr(), probs.data_ptr(), _raw_stream(logits))
-    _check(st, "nvfp4moe_router_select")
-    return ids, probs
-
-
-def router_select_backward(logits, ids, dprobs, bias=None, score: int = SCORE_SOFTMAX, renormalize: bool = True,
-                           scale: float = 1.0, out=None, stream=None):
-    """nvfp4moe_router_select_backward: router_select's logits, bias and ids, and dprobs [T,k] f32 -> dlogits [T,E]
-    of the logits' type."""
-    import torch
-    T, E = logits.shape
-    k = ids.shape[-1]
-    kind = _logits_type("router_select_backward", logits, bias)
-    _need("router_select_backward", ids, "ids", (torch.int32,), (T, k), logits.device)
-    _need("router_select_backward", dprobs, "dprobs", (torch.float32,), (T, k), logits.device)
-    if _elsewhere(logits, stream):
-        with _there(logits, stream):
-            return router_select_backward(logits, ids, dprobs, bias, score, renormalize, scale, out)
-    if out is None:
-        out = torch.empty((T, E), dtype=logits.dtype, device=logits.device)
-    else:
-        _need("router_select_backward", out, "out", (logits.dtype,), (T, E), logits.device, contiguous=False)
-    cfg = _select_config(E, k, score, 1 if renormalize else 0, scale, 1, 1, GROUP_MAX, kind)
-    st = lib().nvfp4moe_router_select_backward(cfg, logits.data_ptr(), _ld(logits), T,
-                                               None if bias is None else bias.data_ptr(), ids.data_ptr(),
-                                               dprobs.data_ptr(), out.data_ptr(), _ld(out), _raw_stream(logits))
-    _check(st, "nvfp4moe_router_select_backward")
-    return out
-
-
-def mxfp4_quantize(x, scale_round: int = MXFP4_SCALE_FLOOR, out=None, stream=None):
-    """nvfp4moe_mxfp4_quantize, logical layout: x [rows, cols] BF16 (rows may be strided) -> (codes [rows, cols/2]
-    uint8, scales [rows, cols/32] uint8)."""
-    import torch
-    rows, cols = x.shape
-    _need("mxfp4_quantize", x, "x", _bf16_types(), (rows, cols), x.device, contiguous=False)
-    if _elsewhere(x, stream):
-        with _there(x, stream):
-            return mxfp4_quantize(x, scale_round, out)
-    if out is None:
-        codes = torch.empty((rows, cols // 2), dtype=torch.uint8, device=x.device)
-        scales = torch.empty((rows, cols // 32), dtype=torch.uint8, device=x.device)
-    else:
-        codes, scales = out
-        _need("mxfp4_quantize", codes, "out codes", (torch.uint8,), (rows, cols // 2), x.device)
-        _need("mxfp4_quantize", scales, "out scales", (torch.uint8,), (rows, cols // 32), x.device)
-    q = Mxfp4Tensor(codes.data_ptr(), scales.data_ptr(), 1, rows, cols, LAYOUT_LOGICAL)
-    _check(lib().nvfp4moe_mxfp4_quantize(x.data_ptr(), _ld(x), q, scale_round, _raw_stream(x)), "nvfp4moe_mxfp4_quantize")
-    return codes, scales
-
-
-def mxfp4_dequantize(codes, scales, out=None, stream=None):
-    """nvfp4moe_mxfp4_dequantize, logical layout: codes [rows, cols/2], scales [rows, cols/32] uint8 -> [rows, cols]
-    bfloat16."""
-    import torch
-    rows, half = codes.shape
-    cols = 2 * half
-    _need("mxfp4_dequantize", codes, "codes", (torch.uint8,), (rows, half), codes.device)
-    _need("mxfp4_dequantize", scales, "scales", (torch.uint8,), (rows, cols // 32), codes.device)
-    if _elsewhere(codes, stream):
-        with _there(codes, stream):
-            return mxfp4_dequantize(codes, scales, out)
-    if out is None:
-        out = torch.empty((rows, cols), dtype=torch.bfloat16, device=codes.device)
-    else:
-        _need("mxfp4_dequantize", out, "out", _bf16_types(), (rows, cols), codes.device, contiguous=False)
-    q = Mxfp4Tensor(codes.data_ptr(), scales.data_ptr(), 1, rows, cols, LAYOUT_LOGICAL)
-    _check(lib().nvfp4moe_mxfp4_dequantize(q, out.data_ptr(), _ld(out), _raw_stream(codes)), "nvfp4moe_mxfp4_dequantize")
-    return out
-
-
-class Mxfp4Weights:
-    """Caller-owned MXFP4 weights of n_mats matrices [rows, cols], in the products' layout."""
-
-    def __init__(self, n_mats: int, rows: int, cols: int, device="cuda"):
-        import torch
-        self.shape = (n_mats, rows, cols)
-        q = Mxfp4Tensor(None, None, n_mats, rows, cols, LAYOUT_GEMM)
-        nc, ns = ctypes.c_size_t(), ctypes.c_size_t()
-        _check(lib().nvfp4moe_mxfp4_bytes(q, ctypes.byref(nc), ctypes.byref(ns)), "nvfp4moe_mxfp4_bytes")
-        self.codes = torch.empty((nc.value,), dtype=torch.uint8, device=device)
-        self.scales = torch.empty((ns.value,), dtype=torch.uint8, device=device)
-        self.Wq = Mxfp4Tensor(self.codes.data_ptr(), self.scales.data_ptr(), n_mats, rows, cols, LAYOUT_GEMM)
-
-    def quantize_from(self, w, scale_round: int = MXFP4_SCALE_FLOOR, stream=None):
-        """nvfp4moe_mxfp4_quantize: BF16 w [n_mats, rows, cols] -> these buffers, in place."""
-        _need("Mxfp4Weights.quantize_from", w, "w", _bf16_types(), self.shape, self.codes.device)
-        if _elsewhere(w, stream):
-            with _there(w, stream):
-                return self.quantize_from(w, scale_round)
-        _check(lib().nvfp4moe_mxfp4_quantize(w.data_ptr(), self.shape[2], self.Wq, scale_round, _raw_stream(w)),
-               "nvfp4moe_mxfp4_quantize")
-        return self
-
-    def dequantize(self, stream=None):
-        """nvfp4moe_mxfp4_dequantize: the values, [n_mats, rows, cols] bfloat16."""
-        import torch
-        if _elsewhere(self.codes, stream):
-            with _there(self.codes, stream):
-                return self.dequantize()
-        out = torch.empty(self.shape, dtype=torch.bfloat16, device=self.codes.device)
-        _check(lib().nvfp4moe_mxfp4_dequantize(self.Wq, out.data_ptr(), self.shape[2], _raw_stream(out)),
-               "nvfp4moe_mxfp4_dequantize")
-        return out
-
-
-def mxfp4_workspace_bytes(M: int, K: int, n_mats: int = 1) -> int:
-    n = lib().nvfp4moe_mxfp4_workspace_bytes(M, K, n_mats)
-    if n == 0:
-        raise Nvfp4Error(2, "nvfp4moe_mxfp4_workspace_bytes")
-    return n
-
-
-def mxfp4_alloc_workspace(M: int, K: int, n_mats: int = 1, device="cuda"):
-    import torch
-    return torch.empty((mxfp4_workspace_bytes(M, K, n_mats),), dtype=torch.uint8, device=device)
-
-
-def _mxfp4_product(where, x, offsets, W, scale_round, workspace, out, stream):
-    import torch
-    E, N, K = W.shape
-    M = x.shape[0]
-    device = W.codes.device
-    _need(where, x, "x", _bf16_types(), (M, K), device, contiguous=False)
-    if offsets is not None:
-        _need(where, offsets, "offsets", (torch.int32,), (E + 1,), device)
-    if _elsewhere(x, stream):
-        with _there(x, stream):
-            return _mxfp4_product(where, x, offsets, W, scale_round, workspace, out, None)
-    if out is None:
-        out = torch.empty((M, N), dtype=x.dtype, device=device)
-    else:
-        _need(where, out, "out", _bf16_types(), (M, N), device, contiguous=False)
-    if workspace is None:
-        workspace = mxfp4_alloc_workspace(M, K, E, device)
-    else:
-        _need(where, workspace, "workspace", (torch.uint8,), (workspace.numel(),), device)
-    a = (W.Wq, out.data_ptr(), _ld(out), scale_round, workspace.data_ptr(), workspace.numel(), _raw_stream(x))
-    if offsets is None:
-        st = lib().nvfp4moe_mxfp4_linear(x.data_ptr(), M, _ld(x), *a)
-    else:
-        st = lib().nvfp4moe_mxfp4_grouped_linear(x.data_ptr(), M, _ld(x), offsets.data_ptr(), *a)
-    _check(st, where)
-    return out
-
-
-def mxfp4_linear(x, W: Mxfp4Weights, scale_round: int = MXFP4_SCALE_FLOOR, workspace=None, out=None, stream=None):
-    """nvfp4moe_mxfp4_linear: x [M,K] BF16 (rows may be strided), W one [N,K] matrix -> out [M,N] BF16.
-    `workspace` (mxfp4_alloc_workspace) may be shared by calls that follow each other on one stream."""
-    return _mxfp4_product("nvfp4moe_mxfp4_linear", x, None, W, scale_round, workspace, out, stream)
-
-
-def mxfp4_grouped_linear(x, offsets, W: Mxfp4Weights, scale_round: int = MXFP4_SCALE_FLOOR, workspace=None, out=None,
-                         stream=None):
-    """nvfp4moe_mxfp4_grouped_linear: x [R,K] BF16 with expert e's rows in [offsets[e], offsets[e+1]) (int32, on the
-    GPU), W of E matrices [N,K] -> out [R,N] BF16; rows outside the offsets are not written."""
-    return _mxfp4_product("nvfp4moe_mxfp4_grouped_linear", x, offsets, W, scale_round, workspace, out, stream)
-
-
-class GradSet:
-    """The tensors that clip_grad_norm works on: FP32 or BF16, contiguous, on one GPU.  `out` (default: in place)
-    receives the clipped ones.  Holds the tensors and their plan on the GPU; make a new one if they move."""
-
-    def __init__(self, grads, out=None):
-        import torch
-        self.grads = list(grads)
-        self.out = self.grads if out is None else list(out)
-        if not self.grads or len(self.out) != len(self.grads):
-            raise ValueError("GradSet: needs at least one gradient, and an output for each")
-        self.device = self.grads[0].device
-        types = {torch.float32: F32, torch.bfloat16: BF16}
-        for g, o in zip(self.grads, self.out):
-            _need("GradSet", g, "a gradient", tuple(types), g.shape, self.device)
-            _need("GradSet", o, "an output", (g.dtype,), g.shape, self.device)
-        if self.device.type != "cuda":
-            raise ValueError(f"GradSet: GPU tensors are needed, got some on {self.device}")
-        table = (Grad * len(self.grads))(*[Grad(g.data_ptr(), o.data_ptr(), g.numel(), types[g.dtype])
-                                           for g, o in zip(self.grads, self.out)])
-        size, n = ctypes.c_size_t(), ctypes.c_int64()
-        _check(lib().nvfp4moe_grad_plan_bytes(table, len(table), ctypes.byref(size), ctypes.byref(n)),
-               "nvfp4moe_grad_plan_bytes")
-        self.n_chunks = n.value
-        host = torch.empty((size.value // 8,), dtype=torch.int64)
-        _check(lib().nvfp4moe_grad_plan(table, len(table), host.data_ptr(), size.value), "nvfp4moe_grad_plan")
-        self.plan = host.to(self.device)
-
-
-def clip_grad_norm(grads: GradSet, max_norm: float, stream=None):
-    """nvfp4moe_clip_grad_norm: the global norm (float64 [1], on the GPU); the set's outputs hold the gradients scaled
-    to at most max_norm (unchanged if the norm is not finite).  max_norm = inf takes the norm only."""
-    import torch
-    if _elsewhere(grads.plan, stream):
-        with _there(grads.plan, stream):
-            norm = clip_grad_norm(grads, max_norm)
-        if stream is not None and grads.n_chunks:
-            grads.plan.record_stream(stream)
-        return norm
-    words = lib().nvfp4moe_clip_workspace_bytes() // 8
-    buf = torch.empty((1 + words,), dtype=torch.float64, device=grads.device)  # the norm, then the partial sums
-    at = buf.data_ptr()
-    _check(lib().nvfp4moe_clip_grad_norm(grads.plan.data_ptr(), grads.n_chunks, max_norm, at, at + 8, 8 * words,
-                                         _raw_stream(buf)), "nvfp4moe_clip_grad_norm")
-    return buf[:1]
+def __getattr__(name):
+    if name not in _OPS:
+        raise AttributeError(f"module {__name__!r} has no attribute {name!r}")
+    from . import ops
+    globals().update({n: getattr(ops, n) for n in _OPS})
+    return globals()[name]
