@@ -160,14 +160,14 @@ __device__ __forceinline__ float clean(float l) {
 }
 
 // Weight (before the scale) of a chosen expert in lane k < K, in FP64; `live`
-// is false in the other lanes and for unavailable experts.  `max_l`, `den`:
-// the softmax's maximum and denominator over all usable logits (only read for
-// softmax weights without renormalisation).
+// is false in the other lanes and for unavailable experts.  `max_l`, `inv`:
+// the softmax's maximum and inverse denominator over all usable logits (only
+// read for softmax weights without renormalisation).
 template <int LT>
-__device__ __forceinline__ double slot_weight(float l, bool live, bool sigmoid, bool renorm, float max_l, double den) {
+__device__ __forceinline__ double slot_weight(float l, bool live, bool sigmoid, bool renorm, float max_l, double inv) {
     if (!renorm) {
         if (!live) return 0.0;
-        return sigmoid ? sigmoid64(l) : exp64_neg((double)l - (double)max_l) * rcp64(den);
+        return sigmoid ? sigmoid64(l) : exp64_neg((double)l - (double)max_l) * inv;
     }
     // The sum over the selection, shifted by its largest term so that it
     // cannot vanish: sigma(l) e^-m = e^(l - m) / (1 + e^l) with m = min(top, 0).
@@ -183,6 +183,13 @@ __device__ __forceinline__ double slot_weight(float l, bool live, bool sigmoid, 
     }
     const double sum = tok_sum<LT>(w);
     return live ? w * rcp64(sum) : 0.0;
+}
+
+// Keeps LDS accesses before it before those after it: a wavefront's LDS
+// instructions take effect in order, so its lanes see each other's.
+__device__ __forceinline__ void lds_order() {
+    asm volatile("" ::: "memory");
+    __builtin_amdgcn_wave_barrier();
 }
 
 // Batcher's odd-even merge network: a[0..N) descending, N a power of two.
@@ -306,7 +313,7 @@ __global__ void __launch_bounds__(kSelWaves * 64, 4) router_select_kernel(Select
 #pragma unroll
     for (int i = 0; i < NV; i++) l[i] = clean(l[i]);
     float max_l = 0.0f;
-    double den = 1.0;
+    double inv = 1.0;  // 1 / the softmax's denominator
     if (!sigmoid && (scores || !P.renorm)) {
         float mx = l[0];
 #pragma unroll
@@ -316,7 +323,7 @@ __global__ void __launch_bounds__(kSelWaves * 64, 4) router_select_kernel(Select
             float sum = 0.0f;
 #pragma unroll
             for (int i = 0; i < NV; i++) sum += __builtin_amdgcn_exp2f((l[i] - max_l) * 1.4426950408889634f);
-            den = (double)tok_sum<LT>(sum);
+            inv = rcp64(fmax((double)tok_sum<LT>(sum), 1e-300));
         }
     }
     double key[NV];  // v, or the scores that TOP2 groups add up
@@ -328,8 +335,7 @@ __global__ void __launch_bounds__(kSelWaves * 64, 4) router_select_kernel(Select
             double sum = 0.0;
 #pragma unroll
             for (int i = 0; i < NV; i++) sum += key[i] = exp64_neg((double)l[i] - (double)max_l);
-            den = tok_sum<LT>(sum);
-            const double inv = rcp64(den);
+            inv = rcp64(tok_sum<LT>(sum));
 #pragma unroll
             for (int i = 0; i < NV; i++) key[i] *= inv;
         }
@@ -457,7 +463,7 @@ __global__ void __launch_bounds__(kSelWaves * 64, 4) router_select_kernel(Select
     const int e = have ? min(key_expert(mine), P.E - 1) : 0;
     const bool taken = have && mine > kUnavailable * 0.5;
     const float lk = taken ? clean(load1(row + e)) : 0.0f;
-    const double w = slot_weight<LT>(lk, taken, sigmoid, P.renorm, max_l, den);
+    const double w = slot_weight<LT>(lk, taken, sigmoid, P.renorm, max_l, inv);
     if (have && t < P.T) {
         P.ids[t * P.K + lane] = e;
         P.probs[t * P.K + lane] = (float)(w * (double)P.scale);
@@ -469,8 +475,8 @@ __global__ void __launch_bounds__(kSelWaves * 64, 4) router_select_kernel(Select
 //   renormalised  d_k = c w_k (dp_k - sum_j dp_j w_j), times (1 - sigma_k) for sigmoid scores;
 //   sigmoid       d_k = c w_k dp_k (1 - sigma_k);
 //   softmax       d_k = c w_k dp_k at the chosen experts, and -c s_e sum_j dp_j w_j at every expert.
-// One pass: lane k forms d_k in FP64 (K values a token), slots of one expert
-// are added in slot order into the token's row in LDS, and the row is written
+// One pass: lane k forms d_k in FP64 (K values a token) and puts it into the
+// token's row in LDS, which only its own wavefront uses, and the row is written
 // whole, so the kernel is bound by writing [T, E].
 template <int LT, int NV, typename L>
 __global__ void __launch_bounds__(kSelWaves * 64) router_select_backward_kernel(SelectParams P) {
@@ -488,52 +494,66 @@ __global__ void __launch_bounds__(kSelWaves * 64) router_select_backward_kernel(
         dp = P.dprobs[tr * P.K + lane];
     }
     float l[NV];
-    float max_l = 0.0f;
-    double den = 1.0;
     if (dense) {
-        float mx = -kFltMax;
 #pragma unroll
         for (int i = 0; i < NV / 4; i++) {
             float v[4];
             load4(row, (i * LT + lane) * 4, P.E, P.vec, v);
 #pragma unroll
-            for (int j = 0; j < 4; j++) mx = fmaxf(mx, l[4 * i + j] = clean(v[j]));
+            for (int j = 0; j < 4; j++) l[4 * i + j] = v[j];
         }
+    }
+    const bool in = e >= 0 && e < P.E;
+    const float lk = in ? clean(load1(row + e)) : 0.0f;
+    const bool live = in && lk > -__builtin_inff() && !(P.bias && !(P.bias[in ? e : 0] > -__builtin_inff()));
+    // An expert listed twice: every lane leaves its number at its expert; a
+    // lane that finds another's there has a double.
+    uint32_t* tags = reinterpret_cast<uint32_t*>(rows[slot]);
+    if (live) tags[e] = lane;
+    lds_order();
+    const bool twice = __ballot(live && tags[e] != (uint32_t)lane) != 0;
+    lds_order();
+#pragma unroll
+    for (int i = 0; i < NV / 4; i++)
+        *reinterpret_cast<float4*>(&rows[slot][(i * LT + lane) * 4]) = float4{0.0f, 0.0f, 0.0f, 0.0f};
+    float max_l = 0.0f;
+    double inv = 1.0;  // 1 / the softmax's denominator
+    if (dense) {
+        float mx = -kFltMax;
+#pragma unroll
+        for (int i = 0; i < NV; i++) mx = max32(mx, l[i] = clean(l[i]));
         max_l = tok_max<LT>(mx);
         float sum = 0.0f;
 #pragma unroll
         for (int i = 0; i < NV; i++) sum += l[i] = __builtin_amdgcn_exp2f((l[i] - max_l) * 1.4426950408889634f);
-        den = fmax((double)tok_sum<LT>(sum), 1e-300);
+        inv = rcp64(fmax((double)tok_sum<LT>(sum), 1e-300));
     }
-#pragma unroll
-    for (int i = 0; i < NV / 4; i++)
-        *reinterpret_cast<float4*>(&rows[slot][(i * LT + lane) * 4]) = float4{0.0f, 0.0f, 0.0f, 0.0f};
-    const bool in = e >= 0 && e < P.E;
-    const float lk = in ? clean(load1(row + e)) : 0.0f;
-    const bool live = in && lk > -__builtin_inff() && !(P.bias && !(P.bias[in ? e : 0] > -__builtin_inff()));
-    const double w = slot_weight<LT>(lk, live, sigmoid, P.renorm, max_l, den);
-    const double mean = tok_sum<LT>(live ? w * (double)dp : 0.0);
+    const double w = slot_weight<LT>(lk, live, sigmoid, P.renorm, max_l, inv);
+    double mean = 0.0;
+    if (P.renorm || dense) mean = tok_sum<LT>(live ? w * (double)dp : 0.0);
     double d = 0.0;
     if (live) {
         d = w * (P.renorm ? (double)dp - mean : (double)dp) * (double)P.scale;
         if (sigmoid) d *= sigmoid64(-lk);  // 1 - sigma(l)
     }
-    // A repeated expert: its first slot takes the sum, in slot order.
-    float acc = 0.0f;
+    float acc = (float)d;
     bool first = live;
-    for (int k = 0; k < P.K; k++) {
-        const int ek = __shfl(live ? e : -1, k, LT);
-        const float dk = __shfl((float)d, k, LT);
-        if (ek == e) {
-            acc += dk;
-            first = first && k >= lane;
+    if (twice) {  // its first slot takes the sum, in slot order
+        acc = 0.0f;
+        for (int k = 0; k < P.K; k++) {
+            const int ek = __shfl(live ? e : -1, k, LT);
+            const float dk = __shfl((float)d, k, LT);
+            if (ek == e) {
+                acc += dk;
+                first = first && k >= lane;
+            }
         }
     }
-    __syncthreads();
+    lds_order();
     if (first) rows[slot][e] = acc;
-    __syncthreads();
+    lds_order();
     if (t >= P.T) return;
-    const float all = dense ? (float)(-mean * (double)P.scale / den) : 0.0f;
+    const float all = dense ? (float)(-mean * (double)P.scale * inv) : 0.0f;
     L* out = (L*)P.dlogits + t * P.ld_out;
 #pragma unroll
     for (int i = 0; i < NV / 4; i++) {
