@@ -182,7 +182,10 @@ struct Range {
     bool write;
 };
 
-int grad_chunks(const nvfp4moe_grad* g, int32_t n, int64_t* chunks) {
+// Checks the tensors; the elements per chunk and the number of chunks.  A chunk
+// is one workgroup's turn: kGradChunk elements, and fewer (down to 2048) while
+// that would give the grid less than one chunk for each workgroup.
+int grad_chunks(const nvfp4moe_grad* g, int32_t n, int64_t* chunk, int64_t* chunks) {
     if (n < 0) return NVFP4_E_SHAPE;
     if (n > 0 && !g) return NVFP4_E_NULL;
     int64_t total = 0;
@@ -193,9 +196,12 @@ int grad_chunks(const nvfp4moe_grad* g, int32_t n, int64_t* chunks) {
         if (!g[i].in || !g[i].out) return NVFP4_E_NULL;
         const size_t elem = g[i].type == NVFP4MOE_BF16 ? 2 : 4;
         if (!aligned(g[i].in, elem) || !aligned(g[i].out, elem)) return NVFP4_E_ALIGN;
-        total += (g[i].n + kGradChunk - 1) / kGradChunk;
+        total += g[i].n;
     }
-    *chunks = total;
+    *chunk = kGradChunk;
+    while (*chunk > 2048 && total < *chunk * kGradBlocks) *chunk /= 2;
+    *chunks = 0;
+    for (int32_t i = 0; i < n; i++) *chunks += (g[i].n + *chunk - 1) / *chunk;
     return NVFP4_OK;
 }
 
@@ -326,15 +332,16 @@ int nvfp4moe_mxfp4_grouped_linear(const uint16_t* x, int64_t R, int64_t ldx, con
 
 int nvfp4moe_grad_plan_bytes(const nvfp4moe_grad* grads, int32_t n_grads, size_t* bytes, int64_t* n_chunks) {
     if (!bytes || !n_chunks) return NVFP4_E_NULL;
-    const int st = grad_chunks(grads, n_grads, n_chunks);
+    int64_t chunk = 0;
+    const int st = grad_chunks(grads, n_grads, &chunk, n_chunks);
     if (st != NVFP4_OK) return st;
     *bytes = (size_t)*n_chunks * sizeof(GradChunk);
     return NVFP4_OK;
 }
 
 int nvfp4moe_grad_plan(const nvfp4moe_grad* grads, int32_t n_grads, void* plan_host, size_t plan_bytes) {
-    int64_t n_chunks = 0;
-    const int st = grad_chunks(grads, n_grads, &n_chunks);
+    int64_t chunk = 0, n_chunks = 0;
+    const int st = grad_chunks(grads, n_grads, &chunk, &n_chunks);
     if (st != NVFP4_OK) return st;
     if (plan_bytes < (size_t)n_chunks * sizeof(GradChunk)) return NVFP4_E_WORKSPACE;
     if (n_chunks == 0) return NVFP4_OK;
@@ -367,11 +374,11 @@ int nvfp4moe_grad_plan(const nvfp4moe_grad* grads, int32_t n_grads, void* plan_h
     for (int32_t i = 0; i < n_grads; i++) {
         const nvfp4moe_grad& g = grads[i];
         const size_t elem = g.type == NVFP4MOE_BF16 ? 2 : 4;
-        for (int64_t at = 0; at < g.n; at += kGradChunk, c++) {
+        for (int64_t at = 0; at < g.n; at += chunk, c++) {
             *c = GradChunk{};
             c->in = (const uint8_t*)g.in + at * elem;
             c->out = (uint8_t*)g.out + at * elem;
-            c->n = (uint32_t)std::min<int64_t>(kGradChunk, g.n - at);
+            c->n = (uint32_t)std::min<int64_t>(chunk, g.n - at);
             const size_t off = (uintptr_t)c->in % 16;
             c->head = (uint16_t)std::min<size_t>(c->n, off ? (16 - off) / elem : 0);
             c->bf16 = g.type == NVFP4MOE_BF16;

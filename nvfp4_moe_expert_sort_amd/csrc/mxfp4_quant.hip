@@ -103,11 +103,34 @@ __global__ void __launch_bounds__(256) mx_quant_rows_kernel(MxRowsParams P) {
         block--;
     }
     const uint32_t total = P.groups * (uint32_t)P.rows;  // 8-element groups
+    // A wave takes kMxUnroll KiB of consecutive groups (where rows follow each other).
+    const uint32_t g0 = (block * 4 + (threadIdx.x >> 6)) * (kMxUnroll * 64) + (threadIdx.x & 63);
     u32x4 v[kMxUnroll];
+    if (P.flat) {
+        // Rows without gaps, in and out: element 8 g of the input is group g's,
+        // bytes 4 g of the codes and scale g / 4 (its bytes within the 16 of a
+        // 512-column quad transposed for an operand).
+#pragma unroll
+        for (int u = 0; u < kMxUnroll; u++) {
+            const uint32_t g = g0 + u * 64;
+            v[u] = u32x4{0u, 0u, 0u, 0u};
+            if (g < total) v[u] = *reinterpret_cast<const u32x4*>(P.x + (int64_t)g * 8);
+        }
+#pragma unroll
+        for (int u = 0; u < kMxUnroll; u++) {
+            const uint32_t g = g0 + u * 64, b = g >> 2;
+            const uint32_t byte = mx_scale_byte(mx_block_max(v[u]), P.up);
+            const uint32_t code = mx_encode8(v[u], byte);
+            if (g >= total) continue;
+            *reinterpret_cast<uint32_t*>(P.codes + (int64_t)g * 4) = code;
+            if ((g & 3) == 0) P.scales[P.operand ? (b & ~15u) | ((b & 3) << 2) | ((b >> 2) & 3) : b] = (uint8_t)byte;
+        }
+        return;
+    }
     uint32_t row[kMxUnroll], col[kMxUnroll];
 #pragma unroll
     for (int u = 0; u < kMxUnroll; u++) {
-        const uint32_t g = (block * kMxUnroll + u) * 256u + threadIdx.x;
+        const uint32_t g = g0 + u * 64;
         v[u] = u32x4{0u, 0u, 0u, 0u};
         row[u] = 0xFFFFFFFFu;
         col[u] = 0;
@@ -200,6 +223,7 @@ __global__ void __launch_bounds__(256) mx_dequant_kernel(MxDequantParams P) {
 hipError_t launch_mx_quant_rows(MxRowsParams P, hipStream_t stream) {
     P.groups = (uint32_t)((P.operand ? (P.cols + 255) / 256 * 256 : P.cols) / 8);
     P.inv_groups = 1.0 / P.groups;
+    P.flat = P.ld == P.cols && (!P.operand || P.cols % 512 == 0);
     const uint64_t per = 256 * kMxUnroll, total = (uint64_t)P.groups * P.rows;
     hipLaunchKernelGGL(mx_quant_rows_kernel, dim3((unsigned)((total + per - 1) / per) + (P.tiles ? 1u : 0u)), dim3(256), 0,
                        stream, P);

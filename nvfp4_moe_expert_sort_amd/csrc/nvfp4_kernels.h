@@ -138,6 +138,7 @@ struct MxRowsParams {
     int64_t rows, ld;
     uint32_t cols;
     bool up, operand;        // operand: the products' row layout, else logical
+    bool flat;               // rows without gaps, in and out; set by the launcher
     uint8_t* codes;
     uint8_t* scales;
     int64_t ld_codes, ld_scales;  // bytes per row

@@ -144,6 +144,25 @@ def test_select_masked_rows_and_low_masks(gpu):
     assert ids[3].tolist() == [0, 1, 2, 3] and probs[3].tolist() == [0.25] * 4
 
 
+def test_select_signaling_nan(gpu):
+    """Signaling NaN patterns are NaN too."""
+    import torch
+    m, dev = gpu
+    l = torch.randn(5, 70, device=dev)
+    quiet = l.clone()
+    for t, e in ((0, 3), (1, 69), (2, 0), (4, 33)):
+        l.view(torch.int32)[t, e] = 0x7F800001 if t % 2 else -0x7FFFFF  # 0xFF800001
+        quiet[t, e] = torch.nan
+    bias = torch.zeros(70, device=dev)
+    bias.view(torch.int32)[5] = 0x7F800100
+    qb = bias.clone()
+    qb[5] = torch.nan
+    for kw, qw in ((dict(), dict()), (dict(bias=bias), dict(bias=qb)), (dict(score=1, renormalize=False),) * 2):
+        a, b = m.router_select(l, 6, **kw), m.router_select(quiet, 6, **qw)
+        assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+    assert 5 not in m.router_select(l, 6, bias=bias)[0].flatten().tolist()
+
+
 def test_select_strides_alignment_and_untouched_neighbours(gpu):
     import torch
     m, dev = gpu

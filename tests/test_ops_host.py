@@ -137,8 +137,9 @@ def test_grad_plan(m):
     L = m.lib()
     size, n = ctypes.c_size_t(), ctypes.c_int64()
     a = ctypes.byref(size), ctypes.byref(n)
-    # a long FP32 tensor, an empty one, a BF16 one that starts 6 bytes before a boundary and whose output starts elsewhere
-    t = _table(m, (0x100000, 0x100000, 70000, 0), (None, None, 0, 0), (0x20000A, 0x300004, 5, 1), (0x40000A, 0x50000A, 20, 1))
+    # an FP32 tensor of three chunks, an empty one, a BF16 one that starts 6 bytes before a boundary and whose output
+    # starts elsewhere, one whose output does not
+    t = _table(m, (0x100000, 0x100000, 5000, 0), (None, None, 0, 0), (0x20000A, 0x300004, 5, 1), (0x40000A, 0x50000A, 20, 1))
     assert L.nvfp4moe_grad_plan_bytes(t, 4, *a) == 0 and n.value == 5 and size.value == 5 * 24
     buf = np.zeros(size.value // 8, np.uint64)
     p = buf.ctypes.data_as(ctypes.c_void_p)
@@ -148,9 +149,10 @@ def test_grad_plan(m):
     got = [(int(r[0]), int(r[1]), int(r[2]) & 0xFFFFFFFF, int(r[2]) >> 32 & 0xFFFF, int(r[2]) >> 48 & 0xFF, int(r[2]) >> 56)
            for r in buf.reshape(5, 3)]
     at = 0x100000
-    assert got == [(at, at, 32768, 0, 0, 1), (at + 4 * 32768, at + 4 * 32768, 32768, 0, 0, 1),
-                   (at + 8 * 32768, at + 8 * 32768, 70000 - 65536, 0, 0, 1),
+    assert got == [(at, at, 2048, 0, 0, 1), (at + 8192, at + 8192, 2048, 0, 0, 1), (at + 16384, at + 16384, 5000 - 4096, 0, 0, 1),
                    (0x20000A, 0x300004, 5, 3, 1, 0), (0x40000A, 0x50000A, 20, 3, 1, 1)]
+    big = _table(m, (0x100000, 0x100000, 603979776, 0))  # chunks of 32768 elements
+    assert L.nvfp4moe_grad_plan_bytes(big, 1, *a) == 0 and n.value == 603979776 // 32768
 
 
 def test_grad_plan_refusals(m):
