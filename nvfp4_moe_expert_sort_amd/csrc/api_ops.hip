@@ -6,7 +6,6 @@
 
 #include <algorithm>
 #include <cmath>
-#include <new>
 #include <vector>
 
 #include "../../include/nvfp4moe.h"
@@ -353,7 +352,7 @@ int nvfp4moe_grad_plan(const nvfp4moe_grad* grads, int32_t n_grads, void* plan_h
     std::vector<Range> ranges;
     try {
         ranges.reserve(2 * (size_t)n_grads);
-    } catch (const std::bad_alloc&) {
+    } catch (...) {  // no exception crosses the ABI
         return NVFP4_E_WORKSPACE;
     }
     for (int32_t i = 0; i < n_grads; i++) {

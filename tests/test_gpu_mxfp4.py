@@ -155,6 +155,21 @@ def test_linear_sizes(gpu, N, K):
         assert np.array_equal(y, rows[:M])  # every batch size, every kernel: the same bits
 
 
+@pytest.mark.parametrize("K", [4064, 4096, 4128, 8192])
+def test_linear_long_rows(gpu, K):
+    """Rows at the few-row kernel's longest and beyond, with its largest share of LDS."""
+    m, dev = gpu
+    rng = np.random.default_rng(K)
+    w, wv = _weights(m, dev, _bits(rng, (1, 80, K), 0.05))
+    bits = _bits(rng, (40, K))
+    xv = R.mxfp4_values(*R.mxfp4_quantize(bits, False))
+    x = to_dev(bits, dev)
+    full = to_host(m.mxfp4_linear(x, w))
+    _check_product(R.bf16_values(full), xv, wv[0])
+    for M in (1, 3, 7, 8, 9, 17):
+        assert np.array_equal(to_host(m.mxfp4_linear(x[:M], w)), full[:M])
+
+
 @pytest.mark.parametrize("M,N,K", [(5, 33, 128), (40, 64, 640), (200, 300, 1152)])
 def test_linear_exact_sums(gpu, M, N, K):
     """Elements that quantize to themselves under one common scale: the sums are exact, so the bits are."""
@@ -234,7 +249,7 @@ def test_grouped_offsets(gpu, off):
 
 
 @pytest.mark.parametrize("E,rows,N,K,skew", [(1, 70, 40, 96, 0.0), (3, 9, 64, 128, 0.0), (8, 700, 200, 320, 0.5),
-                                             (8, 2500, 96, 256, 1.5), (128, 512, 80, 256, 0.5), (700, 900, 33, 64, 1.0),
+                                             (8, 2500, 96, 256, 1.5), (128, 512, 80, 256, 0.5), (64, 300, 320, 768, 2.5), (700, 900, 33, 64, 1.0),
                                              (1024, 3000, 16, 32, 0.3), (60, 1, 48, 512, 0.0)])
 def test_grouped_against_fp64(gpu, E, rows, N, K, skew):
     import torch
