@@ -107,7 +107,8 @@ int mx_product(const uint16_t* x, int64_t M, int64_t ldx, const int32_t* offsets
     if (scale_round != NVFP4MOE_MXFP4_SCALE_FLOOR && scale_round != NVFP4MOE_MXFP4_SCALE_RU) return NVFP4_E_ARG;
     int st = mx_tensor(Wq);
     if (st != NVFP4_OK) return st;
-    if (Wq->layout != NVFP4_LAYOUT_GEMM || Wq->rows < 1 || Wq->n_mats < 1 || (!grouped && Wq->n_mats != 1)) return NVFP4_E_SHAPE;
+    if (Wq->layout != NVFP4_LAYOUT_GEMM || Wq->rows < 1 || Wq->n_mats < 1) return NVFP4_E_SHAPE;
+    if (!grouped && Wq->n_mats != 1) return NVFP4_E_SHAPE;
     const int64_t K = Wq->cols, N = Wq->rows, E = Wq->n_mats;
     MxWork w;
     if (!mx_work(M, K, E, &w)) return NVFP4_E_SHAPE;
@@ -278,7 +279,8 @@ int nvfp4moe_mxfp4_quantize(const uint16_t* x, int64_t ld, const nvfp4moe_mxfp4_
     if (!aligned(x, 16) || ld % 8 != 0) return NVFP4_E_ALIGN;
     const bool ru = scale_round == NVFP4MOE_MXFP4_SCALE_RU;
     if (q->layout == NVFP4_LAYOUT_GEMM)
-        return hip_status(launch_mx_quant_tiles(x, q->n_mats, q->rows, q->cols, ld, q->codes, q->scales, ru, (hipStream_t)stream));
+        return hip_status(launch_mx_quant_tiles(x, q->n_mats, q->rows, q->cols, ld, q->codes, q->scales, ru,
+                                                (hipStream_t)stream));
     MxRowsParams p{};
     p.x = x;
     p.rows = rows;

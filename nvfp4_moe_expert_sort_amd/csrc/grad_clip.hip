@@ -11,6 +11,10 @@
 // their total are taken in one fixed order, so the norm has the same bits in
 // every run.  The second pass walks the plan backwards: what the first read
 // last is still in the 256 MB last-level cache.
+//
+// 604 M FP32 gradients (2.4 GB): 422 us for the norm (5.7 TB/s), 919 us to scale
+// them into other buffers (5.25 TB/s); a plain copy moves 5.2-5.5.  61 tensors
+// of up to 65537 elements: 3.2 + 4.0 us.
 #include "nvfp4_device.h"
 #include "nvfp4_kernels.h"
 

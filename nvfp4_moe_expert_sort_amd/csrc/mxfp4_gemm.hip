@@ -100,8 +100,9 @@ namespace {
 // 16 bytes per lane from base + off to LDS at `lds` + 16 lane (one vmcnt event).
 // The builtin would make the compiler wait for every load in flight before
 // each LDS read, since it cannot tell the buffers apart; here the waits are
-// written out (`arrive`).  m0, which the compiler does not list as clobbered,
-// has no other user in these kernels.
+// written out (`arrive`).  The load has no output register, and its address
+// register is read when it issues.  m0, which the compiler does not list as
+// clobbered, has no other user in these kernels.
 __device__ __forceinline__ void dma16(const uint8_t* base, uint32_t off, uint32_t lds) {
     asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, %1" ::"v"(off), "s"(base), "s"(lds) : "memory");
 }
@@ -109,6 +110,12 @@ __device__ __forceinline__ uint32_t lds_addr(const void* p) {
     return (uint32_t)(uintptr_t)(const __attribute__((address_space(3))) void*)p;
 }
 
+// 8192 x 4096 x 4096: 66-81 us, 3.4-4.2 PFLOP/s.  The matrix pipe is busy in
+// 59 % of the cycles, and the card holds 1.4-1.7 GHz there: with zeros for
+// operands the same cycles take 50 us, so power is what bounds it.  32768 rows
+// over 128 experts of 1536 x 2048: 92 us for 350 MB (weights, quantized rows,
+// outputs), of which the copy rate allows 67.
+//
 // The product of a tile of up to MT 16-row subtiles, NT 16-column tiles per
 // wave.  Loop over 128-column chunks, four of them (a quad, one scale word)
 // unrolled:
@@ -167,9 +174,15 @@ __device__ __forceinline__ void wide_tile(const MxGemmParams& P, const MxTile& T
     u32x4 w[kAhead][NT], a[MT];
     uint32_t ws[NT], wsn[NT], as[MT];
     const int a_off[2] = {r * 128 + ((q ^ ((r >> 1) & 7)) << 4), r * 128 + (((4 + q) ^ ((r >> 1) & 7)) << 4)};
-    auto load_w = [&](int c, int t) { return *reinterpret_cast<const u32x4*>(wc[t] + (int64_t)min(c, chunks - 1) * 1024 + lane16); };
-    auto load_ws = [&](int g, int t) { return *reinterpret_cast<const uint32_t*>(wsp[t] + (int64_t)min(g, quads - 1) * 256 + lane4); };
-    auto read_a = [&](int c, int i) { return *reinterpret_cast<const u32x4*>(&S.a[(c >> 1) % kWideStages][a_off[c & 1] + i * 2048]); };
+    auto load_w = [&](int c, int t) {
+        return *reinterpret_cast<const u32x4*>(wc[t] + (int64_t)min(c, chunks - 1) * 1024 + lane16);
+    };
+    auto load_ws = [&](int g, int t) {
+        return *reinterpret_cast<const uint32_t*>(wsp[t] + (int64_t)min(g, quads - 1) * 256 + lane4);
+    };
+    auto read_a = [&](int c, int i) {
+        return *reinterpret_cast<const u32x4*>(&S.a[(c >> 1) % kWideStages][a_off[c & 1] + i * 2048]);
+    };
     auto read_s = [&](int g, int i) { return *reinterpret_cast<const uint32_t*>(&S.s[g & 1][(i * 16 + r) * 16 + q * 4]); };
     // Waits until a step has landed for every wave; every wave has then also
     // read the step before, whose buffer the next request takes.  Loads return
@@ -306,13 +319,17 @@ __global__ void __launch_bounds__(256, 2) mx_gemm_wide_kernel(MxGemmParams P) {
 // Few rows: workgroup (x, y) takes every gridDim.x-th group of 64 columns of
 // matrix y, 16 per wave, and its rows kSmallMT * 16 at a time.  It quantizes the
 // rows itself, into LDS, while its first weights (12 KiB a wave) are on their way:
-// no launch, table or round trip through memory comes before them.  After that
-// it streams: each wave keeps a ring of kSmallRing quads of weights in flight
+// no launch, table or round trip through memory comes before them.  Bound by
+// reading the weights: 512 rows over 128 experts of 1536 x 2048 take 36 us for
+// 214 MB (6 TB/s, part of it from the last-level cache; 43 us and 5.0 TB/s from
+// memory); 7 x 4096 x 2048 takes 6.1 us, a launch and one chain of loads.  After
+// the first it streams: each wave keeps a ring of kSmallRing quads of weights in flight
 // across its column groups.
 constexpr int kSmallRing = 3, kSmallMT = 2, kSmallBM = 16 * kSmallMT;
 
 __global__ void __launch_bounds__(256, 4) mx_gemm_small_kernel(MxGemmParams P) {
-    extern __shared__ __attribute__((aligned(16))) uint8_t smem[];  // codes [kSmallBM][lds_codes], scale words [kSmallBM][lds_scales]
+    // codes [kSmallBM][lds_codes], then scale words [kSmallBM][lds_scales]
+    extern __shared__ __attribute__((aligned(16))) uint8_t smem[];
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), q = lane >> 4, r = lane & 15;
     int64_t row0 = 0, row1 = P.M;
     if (P.offsets) {
@@ -328,7 +345,8 @@ __global__ void __launch_bounds__(256, 4) mx_gemm_small_kernel(MxGemmParams P) {
         if (row0 >= row1) return;
     }
     const int32_t chunks = P.chunks, quads = P.quads;
-    const int32_t col_groups = (P.N + 63) / 64, mine = (col_groups - blockIdx.x + gridDim.x - 1) / gridDim.x;  // this workgroup's
+    const int32_t col_groups = (P.N + 63) / 64;
+    const int32_t mine = (col_groups - blockIdx.x + gridDim.x - 1) / gridDim.x;  // this workgroup's
     const int64_t mat_tile = (int64_t)blockIdx.y * P.row_tiles;
     const uint32_t lane16 = lane * 16, lane4 = lane * 4;
     const uint32_t groups = (uint32_t)chunks * 16;  // 8-column groups of a row, padded to whole chunks
@@ -372,7 +390,8 @@ __global__ void __launch_bounds__(256, 4) mx_gemm_small_kernel(MxGemmParams P) {
                 row[u] = __umulhi(i, P.groups_magic);
                 col[u] = (i - row[u] * groups) * 8;
                 v[u] = u32x4{0u, 0u, 0u, 0u};
-                if (i < rows * groups && col[u] < P.cols) v[u] = *reinterpret_cast<const u32x4*>(P.x + (at + row[u]) * P.ldx + col[u]);
+                if (i < rows * groups && col[u] < P.cols)
+                    v[u] = *reinterpret_cast<const u32x4*>(P.x + (at + row[u]) * P.ldx + col[u]);
             }
 #pragma unroll
             for (int u = 0; u < 4; u++) {
@@ -398,7 +417,8 @@ __global__ void __launch_bounds__(256, 4) mx_gemm_small_kernel(MxGemmParams P) {
 #pragma unroll
                     for (int cc = 0; cc < 4; cc++)
                         if (g * 4 + cc < chunks) {
-                            const u32x4 a = *reinterpret_cast<const u32x4*>(smem + (i * 16 + r) * P.lds_codes + (g * 4 + cc) * 64 + q * 16);
+                            const u32x4 a = *reinterpret_cast<const u32x4*>(smem + (i * 16 + r) * P.lds_codes +
+                                                                            (g * 4 + cc) * 64 + q * 16);
                             acc[i] = mx_mfma_sel(cc, w[s][cc], a, acc[i], ws[s], as);
                         }
                 }
@@ -421,10 +441,14 @@ __global__ void __launch_bounds__(256, 4) mx_gemm_small_kernel(MxGemmParams P) {
 // The small kernel is for up to 16 rows a matrix on average (a rule on what the
 // host knows; a matrix with more takes them kSmallBM at a time) of up to
 // kSmallElements elements together, which each of its workgroups quantizes, in
-// rows that fit LDS.
+// rows that fit LDS.  Against the tile kernel, quantizer included: 8 rows of
+// 4096 for one matrix of 4096 columns 8.8 against 11.0 us, 16 rows of 768 for
+// each of 128 x 2048 columns 22.7 against 25.6, 16 rows of 2048 for each of
+// 128 x 1536 columns 52 against 48 (8 rows: 47 each).
 constexpr int64_t kSmallRows = 16, kSmallElements = 32768;
 constexpr int32_t kSmallCols = 4096;
-constexpr int64_t kSmallBlocks = 1024, kWideBlocks = 144;
+constexpr int64_t kSmallBlocks = 1024;  // workgroups of the small kernel
+constexpr int64_t kWideBlocks = 144;    // tiles that make 256 columns worth it
 bool mx_small(int64_t rows, int64_t E, int64_t K) {
     return rows <= kSmallRows * E && rows * K <= kSmallElements * E && K <= kSmallCols;
 }
@@ -446,7 +470,15 @@ hipError_t launch_mx_gemm_small(MxGemmParams P, int64_t E, hipStream_t stream) {
 }
 
 // The column width of a tile: 256, or 64 where 256 would leave CUs without a
-// workgroup.
+// workgroup (512 x 4096 x 4096, 64 tiles of 256: 21.3 against 16.9 us; 1024
+// rows, 128 tiles: 24.7 against 23.7; 4096 x 1536 x 2048, 192 tiles: 20.4
+// against 22.3).
+//
+// Measured and not taken: tiles of 256 rows by 8 waves (8192 x 4096 x 4096 with
+// its quantizer 84.6 against 83.4 us), 96-row tiles for grouped products (132
+// against 125 us), weights four chunks ahead in tiles of up to 96 rows (no
+// change), non-temporal output stores (the grouped product 119 against 125 us,
+// but with a kernel that reads the output 153 against 151).
 int mx_tile_rows() { return kWideBM; }
 hipError_t launch_mx_gemm(MxGemmParams P, int64_t tiles_bound, hipStream_t stream) {
     const bool wide = tiles_bound * ((P.N + 255) / 256) >= kWideBlocks;

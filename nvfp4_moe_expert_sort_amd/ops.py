@@ -16,6 +16,7 @@ from . import (BF16, F32, GROUP_MAX, LAYOUT_GEMM, LAYOUT_LOGICAL, MXFP4_SCALE_FL
                Nvfp4Error, SelectConfig, _check, lib)
 
 _BF16 = (torch.bfloat16, torch.int16, torch.uint16)  # storage of BF16 bits
+_TYPES = {torch.float32: F32, torch.bfloat16: BF16}
 
 
 def _elsewhere(t, stream):
@@ -40,18 +41,21 @@ def _raw_stream(t):
 
 
 def _need(where, t, name, dtypes, shape, device, contiguous=True):
-    """ValueError unless t has one of the types, the shape and the device, with rows of consecutive elements."""
+    """ValueError unless t has one of the types, the shape, the device and (by default) contiguous elements."""
     if t.dtype not in dtypes or t.shape != shape or t.device != device:
         raise ValueError(f"{where}: {name} must be {' or '.join(str(d) for d in dtypes)} of shape {tuple(shape)} on "
                          f"{device}, got {t.dtype} {tuple(t.shape)} on {t.device}")
-    if not t.is_contiguous() and (contiguous or (t.numel() and t.shape[-1] > 1 and t.stride(-1) != 1)):
-        raise ValueError(f"{where}: {name} must {'be contiguous' if contiguous else 'have consecutive columns'}")
+    if contiguous and not t.is_contiguous():
+        raise ValueError(f"{where}: {name} must be contiguous")
 
 
-def _ld(t):
-    """Elements from one row of a matrix to the next."""
+def _ld(where, t, name):
+    """Elements from one row of a matrix to the next; ValueError unless its columns are consecutive."""
     rows, cols = t.shape
-    return t.stride(0) if rows > 1 else max(t.stride(0), cols)
+    ld, step = t.stride()
+    if step != 1 and cols > 1 and rows:
+        raise ValueError(f"{where}: {name} must have consecutive columns, got strides {(ld, step)}")
+    return ld if rows > 1 else max(ld, cols)
 
 
 @functools.lru_cache(256)
@@ -78,20 +82,23 @@ def router_logits(x, w_router, out=None, stream=None):
     return out
 
 
-def _logits_type(where, logits, bias):
-    """Checks logits and bias; their type as the library names it."""
-    _need(where, logits, "logits", (torch.float32, torch.bfloat16), logits.shape, logits.device, contiguous=False)
+def _logits(where, logits, bias):
+    """Checks logits and bias; the logits' type as the library names it, and their row stride."""
+    kind = _TYPES.get(logits.dtype)
+    if kind is None or logits.dim() != 2:
+        raise ValueError(f"{where}: logits must be a matrix of float32 or bfloat16, got {logits.dtype} "
+                         f"{tuple(logits.shape)}")
     if bias is not None:
         _need(where, bias, "bias", (torch.float32,), logits.shape[1:], logits.device)
-    return F32 if logits.dtype == torch.float32 else BF16
+    return kind, _ld(where, logits, "logits")
 
 
 def router_select(logits, k: int, bias=None, score: int = SCORE_SOFTMAX, renormalize: bool = True, scale: float = 1.0,
                   n_groups: int = 1, top_groups: int = 1, group_score: int = GROUP_MAX, out=None, stream=None):
     """nvfp4moe_router_select: logits [T,E] f32 or bf16 (rows may be strided), bias [E] f32 -> (ids [T,k] int32,
     probs [T,k] f32); `out` may hold the two, preallocated."""
+    kind, ld = _logits("router_select", logits, bias)
     T, E = logits.shape
-    kind = _logits_type("router_select", logits, bias)
     if _elsewhere(logits, stream):
         with _there(logits, stream):
             return router_select(logits, k, bias, score, renormalize, scale, n_groups, top_groups, group_score, out)
@@ -103,7 +110,7 @@ def router_select(logits, k: int, bias=None, score: int = SCORE_SOFTMAX, renorma
         _need("router_select", ids, "out ids", (torch.int32,), (T, k), logits.device)
         _need("router_select", probs, "out probs", (torch.float32,), (T, k), logits.device)
     cfg = _select_config(E, k, score, 1 if renormalize else 0, scale, n_groups, top_groups, group_score, kind)
-    st = lib().nvfp4moe_router_select(cfg, logits.data_ptr(), _ld(logits), T, None if bias is None else bias.data_ptr(),
+    st = lib().nvfp4moe_router_select(cfg, logits.data_ptr(), ld, T, None if bias is None else bias.data_ptr(),
                                       ids.data_ptr(), probs.data_ptr(), _raw_stream(logits))
     _check(st, "nvfp4moe_router_select")
     return ids, probs
@@ -113,9 +120,9 @@ def router_select_backward(logits, ids, dprobs, bias=None, score: int = SCORE_SO
                            scale: float = 1.0, out=None, stream=None):
     """nvfp4moe_router_select_backward: router_select's logits, bias and ids, and dprobs [T,k] f32 -> dlogits [T,E]
     of the logits' type."""
+    kind, ld = _logits("router_select_backward", logits, bias)
     T, E = logits.shape
     k = ids.shape[-1]
-    kind = _logits_type("router_select_backward", logits, bias)
     _need("router_select_backward", ids, "ids", (torch.int32,), (T, k), logits.device)
     _need("router_select_backward", dprobs, "dprobs", (torch.float32,), (T, k), logits.device)
     if _elsewhere(logits, stream):
@@ -126,9 +133,10 @@ def router_select_backward(logits, ids, dprobs, bias=None, score: int = SCORE_SO
     else:
         _need("router_select_backward", out, "out", (logits.dtype,), (T, E), logits.device, contiguous=False)
     cfg = _select_config(E, k, score, 1 if renormalize else 0, scale, 1, 1, GROUP_MAX, kind)
-    st = lib().nvfp4moe_router_select_backward(cfg, logits.data_ptr(), _ld(logits), T,
+    st = lib().nvfp4moe_router_select_backward(cfg, logits.data_ptr(), ld, T,
                                                None if bias is None else bias.data_ptr(), ids.data_ptr(),
-                                               dprobs.data_ptr(), out.data_ptr(), _ld(out), _raw_stream(logits))
+                                               dprobs.data_ptr(), out.data_ptr(), _ld("router_select_backward", out, "out"),
+                                               _raw_stream(logits))
     _check(st, "nvfp4moe_router_select_backward")
     return out
 
@@ -149,7 +157,8 @@ def mxfp4_quantize(x, scale_round: int = MXFP4_SCALE_FLOOR, out=None, stream=Non
         _need("mxfp4_quantize", codes, "out codes", (torch.uint8,), (rows, cols // 2), x.device)
         _need("mxfp4_quantize", scales, "out scales", (torch.uint8,), (rows, cols // 32), x.device)
     q = Mxfp4Tensor(codes.data_ptr(), scales.data_ptr(), 1, rows, cols, LAYOUT_LOGICAL)
-    _check(lib().nvfp4moe_mxfp4_quantize(x.data_ptr(), _ld(x), q, scale_round, _raw_stream(x)), "nvfp4moe_mxfp4_quantize")
+    _check(lib().nvfp4moe_mxfp4_quantize(x.data_ptr(), _ld("mxfp4_quantize", x, "x"), q, scale_round, _raw_stream(x)),
+           "nvfp4moe_mxfp4_quantize")
     return codes, scales
 
 
@@ -168,7 +177,8 @@ def mxfp4_dequantize(codes, scales, out=None, stream=None):
     else:
         _need("mxfp4_dequantize", out, "out", _BF16, (rows, cols), codes.device, contiguous=False)
     q = Mxfp4Tensor(codes.data_ptr(), scales.data_ptr(), 1, rows, cols, LAYOUT_LOGICAL)
-    _check(lib().nvfp4moe_mxfp4_dequantize(q, out.data_ptr(), _ld(out), _raw_stream(codes)), "nvfp4moe_mxfp4_dequantize")
+    _check(lib().nvfp4moe_mxfp4_dequantize(q, out.data_ptr(), _ld("mxfp4_dequantize", out, "out"), _raw_stream(codes)),
+           "nvfp4moe_mxfp4_dequantize")
     return out
 
 
@@ -234,11 +244,12 @@ def _mxfp4_product(where, x, offsets, W, scale_round, workspace, out, stream):
         workspace = mxfp4_alloc_workspace(M, K, E, device)
     else:
         _need(where, workspace, "workspace", (torch.uint8,), (workspace.numel(),), device)
-    a = (W.Wq, out.data_ptr(), _ld(out), scale_round, workspace.data_ptr(), workspace.numel(), _raw_stream(x))
+    ldx = _ld(where, x, "x")
+    a = (W.Wq, out.data_ptr(), _ld(where, out, "out"), scale_round, workspace.data_ptr(), workspace.numel(), _raw_stream(x))
     if offsets is None:
-        st = lib().nvfp4moe_mxfp4_linear(x.data_ptr(), M, _ld(x), *a)
+        st = lib().nvfp4moe_mxfp4_linear(x.data_ptr(), M, ldx, *a)
     else:
-        st = lib().nvfp4moe_mxfp4_grouped_linear(x.data_ptr(), M, _ld(x), offsets.data_ptr(), *a)
+        st = lib().nvfp4moe_mxfp4_grouped_linear(x.data_ptr(), M, ldx, offsets.data_ptr(), *a)
     _check(st, where)
     return out
 
@@ -266,13 +277,12 @@ class GradSet:
         if not self.grads or len(self.out) != len(self.grads):
             raise ValueError("GradSet: needs at least one gradient, and an output for each")
         self.device = self.grads[0].device
-        types = {torch.float32: F32, torch.bfloat16: BF16}
         for g, o in zip(self.grads, self.out):
-            _need("GradSet", g, "a gradient", tuple(types), g.shape, self.device)
+            _need("GradSet", g, "a gradient", tuple(_TYPES), g.shape, self.device)
             _need("GradSet", o, "an output", (g.dtype,), g.shape, self.device)
         if self.device.type != "cuda":
             raise ValueError(f"GradSet: GPU tensors are needed, got some on {self.device}")
-        table = (Grad * len(self.grads))(*[Grad(g.data_ptr(), o.data_ptr(), g.numel(), types[g.dtype])
+        table = (Grad * len(self.grads))(*[Grad(g.data_ptr(), o.data_ptr(), g.numel(), _TYPES[g.dtype])
                                            for g, o in zip(self.grads, self.out)])
         size, n = ctypes.c_size_t(), ctypes.c_int64()
         _check(lib().nvfp4moe_grad_plan_bytes(table, len(table), ctypes.byref(size), ctypes.byref(n)),
