@@ -113,7 +113,8 @@ __device__ __forceinline__ F tok_sum(F v) {
     return __shfl(v, 0, LT);
 }
 
-// e^x for x in [-708, 708], within 2^-46 relative: x = n ln 2 + r with
+// e^x for x in [-746, 709], within 2^-46 relative (below -708 rounded as FP64
+// denormals are, 0 at -746): x = n ln 2 + r with
 // |r| <= ln 2 / 2 (n is read from the low bits of t = x log2 e + 1.5 2^52),
 // Taylor's series of e^r to r^11 (the next term is below 2^-47), and n added
 // to the exponent.  The series is written as one block of instructions that
@@ -147,10 +148,13 @@ __device__ __forceinline__ double rcp64(double d) {
     const double r = __builtin_amdgcn_rcp(d);
     return __builtin_fma(__builtin_fma(-d, r, 1.0), r, r);
 }
-// e^x for x <= 0; below the range of exp64 its smallest value, 2^-1021.
-__device__ __forceinline__ double exp64_neg(double x) { return exp64(max64(x, -708.0)); }
+// e^x for x <= 0, 0 where FP64 has no number so small: experts masked with the
+// type's lowest value have scores of exactly 0 and tie.
+__device__ __forceinline__ double exp64_neg(double x) { return exp64(max64(x, -746.0)); }
+// 1 / (1 + e^-l), as e^l / (1 + e^l) below 0 for the same reason.
 __device__ __forceinline__ double sigmoid64(float l) {
-    return rcp64(1.0 + exp64((double)__builtin_amdgcn_fmed3f(-l, -708.0f, 708.0f)));
+    const double e = exp64(-(double)fminf(fabsf(l), 746.0f));
+    return (l < 0.0f ? e : 1.0) * rcp64(1.0 + e);
 }
 
 constexpr float kFltMax = 3.402823466e+38f;
@@ -337,7 +341,7 @@ __global__ void __launch_bounds__(kSelWaves * 64, 4) router_select_kernel(Select
             double sum = 0.0;
 #pragma unroll
             for (int i = 0; i < NV; i++) sum += key[i] = exp64_neg((double)l[i] - (double)max_l);
-            inv = rcp64(tok_sum<LT>(sum));
+            inv = rcp64(fmax(tok_sum<LT>(sum), 1e-300));  // (no usable expert: 0)
 #pragma unroll
             for (int i = 0; i < NV; i++) key[i] *= inv;
         }

@@ -144,6 +144,26 @@ def test_select_masked_rows_and_low_masks(gpu):
     assert ids[3].tolist() == [0, 1, 2, 3] and probs[3].tolist() == [0.25] * 4
 
 
+@pytest.mark.parametrize("sigmoid", [False, True])
+@pytest.mark.parametrize("biased", [False, True])
+def test_select_scores_that_vanish_tie(gpu, sigmoid, biased):
+    """A score that FP64 cannot hold is 0: of groups whose experts are masked with the lowest value, one with a single
+    usable expert ties with one that has two, and so the lower group stays."""
+    m, dev = gpu
+    rng = np.random.default_rng(12)
+    T, E, G = 24, 64, 16
+    l = rng.standard_normal((T, E)).astype(np.float32).reshape(T, G, 4)
+    low = rng.random((T, G)) < 0.7
+    for value in (-R.FLT_MAX, -2000.0):
+        a = np.where(low[..., None], np.float32(value), l)
+        a[rng.random(a.shape) < 0.4] = -np.inf
+        a = a.reshape(T, E)
+        bias = to_dev(np.zeros(E, np.float32), dev) if biased else None
+        for renorm in (False, True):
+            _check(m, to_dev(a.astype(np.float32), dev), 9, bias, sigmoid=sigmoid, renorm=renorm, n_groups=G, top_groups=9,
+                   top2=True)
+
+
 def test_select_signaling_nan(gpu):
     """Signaling NaN patterns are NaN too."""
     import torch
