@@ -113,8 +113,8 @@ __device__ __forceinline__ F tok_sum(F v) {
     return __shfl(v, 0, LT);
 }
 
-// e^x for x in [-746, 709], within 2^-46 relative (below -708 rounded as FP64
-// denormals are, 0 at -746): x = n ln 2 + r with
+// e^x for x in [-746, 746], within 2^-46 relative where FP64 has such a normal
+// number (0 at -746, inf from 709.8 on): x = n ln 2 + r with
 // |r| <= ln 2 / 2 (n is read from the low bits of t = x log2 e + 1.5 2^52),
 // Taylor's series of e^r to r^11 (the next term is below 2^-47), and n added
 // to the exponent.  The series is written as one block of instructions that
@@ -151,10 +151,12 @@ __device__ __forceinline__ double rcp64(double d) {
 // e^x for x <= 0, 0 where FP64 has no number so small: experts masked with the
 // type's lowest value have scores of exactly 0 and tie.
 __device__ __forceinline__ double exp64_neg(double x) { return exp64(max64(x, -746.0)); }
-// 1 / (1 + e^-l), as e^l / (1 + e^l) below 0 for the same reason.
+// 1 / (1 + e^-l), 0 where e^-l exceeds FP64 for the same reason: there the
+// Newton step of 1 / inf is a NaN, which the clamp to [0, 1] (a modifier of its
+// last instruction) makes 0.
 __device__ __forceinline__ double sigmoid64(float l) {
-    const double e = exp64(-(double)fminf(fabsf(l), 746.0f));
-    return (l < 0.0f ? e : 1.0) * rcp64(1.0 + e);
+    const double d = 1.0 + exp64((double)__builtin_amdgcn_fmed3f(-l, -746.0f, 746.0f));
+    return fmin(fmax(rcp64(d), 0.0), 1.0);
 }
 
 constexpr float kFltMax = 3.402823466e+38f;
