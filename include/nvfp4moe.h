@@ -419,7 +419,8 @@ typedef struct {
  * s and v are formed in FP64, so the choice does not depend on FP32 rounding;
  * with a bias (or TOP2) values closer than about 2^-40 relative may count as
  * equal.
- *   ids [T, K] int32, probs [T, K] FP32: caller-owned outputs
+ *   ids [T, K] int32, probs [T, K] FP32: caller-owned outputs, which may not
+ *   overlap the inputs
  * Requirements: ld >= E; logits aligned to their element, ids, probs and bias
  * to 4 bytes (rows are read four elements at a time where ld and the pointer
  * allow it).  T == 0 is a no-op.  No workspace, no synchronisation; each
@@ -485,7 +486,8 @@ NVFP4MOE_API int nvfp4moe_mxfp4_bytes(const nvfp4moe_mxfp4_tensor* q, size_t* co
  * (exactly: every MXFP4 value is a BF16 number; out's rows are ld apart).
  * Requirements: x / out 16-byte aligned, ld >= cols and a multiple of 8, codes
  * 16-byte aligned (scales 4-byte in the GEMM layout), n_mats*rows*cols < 2^34.
- * Zero rows or matrices are a no-op.  No synchronisation. */
+ * Zero rows or matrices are a no-op; outputs may not overlap inputs.  No
+ * synchronisation. */
 NVFP4MOE_API int nvfp4moe_mxfp4_quantize(const uint16_t* x, int64_t ld, const nvfp4moe_mxfp4_tensor* q, int32_t scale_round,
                                          void* stream);
 NVFP4MOE_API int nvfp4moe_mxfp4_dequantize(const nvfp4moe_mxfp4_tensor* q, uint16_t* out, int64_t ld, void* stream);
@@ -494,7 +496,9 @@ NVFP4MOE_API int nvfp4moe_mxfp4_dequantize(const nvfp4moe_mxfp4_tensor* q, uint1
  * ldx apart) quantized into the workspace by scale_round, Wq one GEMM-layout
  * matrix [N, K] and FP32 accumulation.  M >= 0, K % 32 == 0, K < 2^24, any N.
  * Requirements: x 16-byte aligned, ldx >= K and a multiple of 8; out aligned to
- * 2 bytes, ld_out >= N (8-byte stores where out, ld_out and N allow them);
+ * 2 bytes, ld_out >= N (8-byte stores where out, ld_out and N allow them); no
+ * element of out shares memory with x, Wq or the workspace (x is still read
+ * while out is written);
  * workspace 256-byte aligned, nvfp4moe_mxfp4_workspace_bytes(M, K, 1) bytes.
  * Each output row depends on its own x row only, with the same bits in every
  * batch (one order over K, no split-K).  M == 0 is a no-op; no

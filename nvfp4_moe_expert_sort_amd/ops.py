@@ -256,7 +256,8 @@ def _mxfp4_product(where, x, offsets, W, scale_round, workspace, out, stream):
 
 def mxfp4_linear(x, W: Mxfp4Weights, scale_round: int = MXFP4_SCALE_FLOOR, workspace=None, out=None, stream=None):
     """nvfp4moe_mxfp4_linear: x [M,K] BF16 (rows may be strided), W one [N,K] matrix -> out [M,N] BF16.
-    `workspace` (mxfp4_alloc_workspace) may be shared by calls that follow each other on one stream."""
+    `workspace` (mxfp4_alloc_workspace) may be shared by calls that follow each other on one stream; `out` may not share
+    elements with x."""
     return _mxfp4_product("nvfp4moe_mxfp4_linear", x, None, W, scale_round, workspace, out, stream)
 
 
