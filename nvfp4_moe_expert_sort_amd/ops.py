@@ -55,7 +55,7 @@ def _ld(where, t, name):
     ld, step = t.stride()
     if step != 1 and cols > 1 and rows:
         raise ValueError(f"{where}: {name} must have consecutive columns, got strides {(ld, step)}")
-    return ld if rows > 1 else max(ld, cols)
+    return ld if rows > 1 else cols  # (a single row's stride means nothing)
 
 
 @functools.lru_cache(256)

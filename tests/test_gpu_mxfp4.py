@@ -273,6 +273,23 @@ def test_grouped_against_fp64(gpu, E, rows, N, K, skew):
     assert np.array_equal(alone[0], y[r])
 
 
+def test_one_row_of_any_stride(gpu):
+    """The row stride of a single row means nothing: one that no matrix of several rows may have is accepted."""
+    import torch
+    m, dev = gpu
+    w = m.Mxfp4Weights(1, 40, 96, dev).quantize_from(torch.randn(1, 40, 96, device=dev).to(torch.bfloat16))
+    wide = torch.randn(1, 101, device=dev).to(torch.bfloat16)
+    x = wide[:, :96]
+    assert x.stride() == (101, 1)
+    out = torch.empty(1, 43, device=dev, dtype=torch.bfloat16)
+    assert torch.equal(m.mxfp4_linear(x, w, out=out[:, :40]), m.mxfp4_linear(x.clone(), w))
+    same = x.contiguous().clone()
+    for a, b in zip(m.mxfp4_quantize(x), m.mxfp4_quantize(same)):
+        assert torch.equal(a, b)
+    codes, scales = m.mxfp4_quantize(same)
+    assert torch.equal(m.mxfp4_dequantize(codes, scales, out=wide[:, :96]), m.mxfp4_dequantize(codes, scales))
+
+
 def test_empty_products_and_refusals(gpu):
     import torch
     m, dev = gpu
