@@ -421,10 +421,11 @@ typedef struct {
  * equal.
  *   ids [T, K] int32, probs [T, K] FP32: caller-owned outputs, which may not
  *   overlap the inputs
- * Requirements: ld >= E; logits aligned to their element, ids, probs and bias
- * to 4 bytes (rows are read four elements at a time where ld and the pointer
- * allow it).  T == 0 is a no-op.  No workspace, no synchronisation; each
- * token's result depends on its own row only. */
+ * Requirements: T < 2^31 (more than some 2^26 tokens take several launches);
+ * ld >= E; logits aligned to their element, ids, probs and bias to 4 bytes
+ * (rows are read four elements at a time where ld and the pointer allow it).
+ * T == 0 is a no-op.  No workspace, no synchronisation; each token's result
+ * depends on its own row only. */
 NVFP4MOE_API int nvfp4moe_router_select(const nvfp4moe_select_config* cfg, const void* logits, int64_t ld, int64_t T,
                                         const float* bias, int32_t* ids, float* probs, void* stream);
 

@@ -22,6 +22,8 @@
 // keys once with a network; every slot then takes the maximum of the lanes'
 // list heads (rotations within a row of 16 lanes) and the owner moves its list
 // up.
+#include <algorithm>
+
 #include "nvfp4_device.h"
 #include "nvfp4_kernels.h"
 
@@ -599,13 +601,38 @@ __global__ void __launch_bounds__(kSelWaves * 64) router_select_backward_kernel(
 
 namespace {
 
+// A dispatch holds fewer than 2^32 work-items, so this many tokens at most go
+// into one launch; more take several.
+template <int LT>
+constexpr int64_t kTokensPerLaunch = (((int64_t)1 << 32) / (kSelWaves * 64) - 1) * kSelWaves * (kWave / LT);
+// P for its tokens [t0, T), as many as one launch takes.
+template <int LT, typename L>
+SelectParams launch_share(SelectParams P, int64_t t0) {
+    P.logits = (const L*)P.logits + t0 * P.ld;
+    P.T = std::min(P.T - t0, kTokensPerLaunch<LT>);
+    if (P.ids) {
+        P.ids += t0 * P.K;
+        P.probs += t0 * P.K;
+    } else {
+        P.ids_in += t0 * P.K;
+        P.dprobs += t0 * P.K;
+        P.dlogits = (L*)P.dlogits + t0 * P.ld_out;
+    }
+    return P;
+}
+
 template <int LT, int NV, int LEN, typename L>
 hipError_t select_run(const SelectParams& P, hipStream_t s) {
     constexpr int kTok = kSelWaves * (kWave / LT);
     const size_t lds = P.n_groups > 1 ? (size_t)kTok * P.lds_token * sizeof(double) : 0;
-    hipLaunchKernelGGL((router_select_kernel<LT, NV, LEN, L>), dim3((unsigned)((P.T + kTok - 1) / kTok)),
-                       dim3(kSelWaves * 64), lds, s, P);
-    return hipGetLastError();
+    for (int64_t t0 = 0; t0 < P.T; t0 += kTokensPerLaunch<LT>) {
+        const SelectParams Q = launch_share<LT, L>(P, t0);
+        hipLaunchKernelGGL((router_select_kernel<LT, NV, LEN, L>), dim3((unsigned)((Q.T + kTok - 1) / kTok)),
+                           dim3(kSelWaves * 64), lds, s, Q);
+        const hipError_t e = hipGetLastError();
+        if (e != hipSuccess) return e;
+    }
+    return hipSuccess;
 }
 template <int LT, int NV, typename L>
 hipError_t select_len(const SelectParams& P, hipStream_t s) {
@@ -629,9 +656,14 @@ hipError_t select_type(const SelectParams& P, hipStream_t s) {
 template <int LT, int NV, typename L>
 hipError_t backward_run(const SelectParams& P, hipStream_t s) {
     constexpr int kTok = kSelWaves * (kWave / LT);
-    hipLaunchKernelGGL((router_select_backward_kernel<LT, NV, L>), dim3((unsigned)((P.T + kTok - 1) / kTok)),
-                       dim3(kSelWaves * 64), 0, s, P);
-    return hipGetLastError();
+    for (int64_t t0 = 0; t0 < P.T; t0 += kTokensPerLaunch<LT>) {
+        const SelectParams Q = launch_share<LT, L>(P, t0);
+        hipLaunchKernelGGL((router_select_backward_kernel<LT, NV, L>), dim3((unsigned)((Q.T + kTok - 1) / kTok)),
+                           dim3(kSelWaves * 64), 0, s, Q);
+        const hipError_t e = hipGetLastError();
+        if (e != hipSuccess) return e;
+    }
+    return hipSuccess;
 }
 template <typename L>
 hipError_t backward_type(const SelectParams& P, hipStream_t s) {

@@ -83,3 +83,24 @@ def test_clip_past_32_bits(gpu):
     assert abs(norm - 0.5 * n ** 0.5) <= 1e-12 * norm
     want = torch.tensor(0.5 / norm, dtype=torch.float64).float().to(torch.bfloat16)
     assert bool((g[-100:] == want.to(dev)).all()) and bool((g[:100] == want.to(dev)).all()) and float(g.min()) == float(g.max())
+
+
+@pytest.mark.parametrize("T,E,k", [((1 << 28) + 21, 2, 1), ((1 << 26) + 7, 17, 17)])
+def test_select_more_tokens_than_one_launch_takes(gpu, T, E, k):
+    """16 lanes a token reach 2^32 work-items at 2^28 tokens, 64 lanes (17 slots) at 2^26."""
+    import torch
+    m, dev = gpu
+    n = 1 << 20
+    block = torch.randn(n, E, device=dev).to(torch.bfloat16)
+    l = block.repeat(T // n, 1)
+    l = torch.cat([l, block[:T - len(l)]])
+    ids, probs = m.router_select(l, k)
+    want, p = m.router_select(block, k)
+    dp = torch.randn(n, k, device=dev)
+    back = m.router_select_backward(block, want, dp, renormalize=False)
+    dps = torch.cat([dp.repeat(T // n, 1), dp[:T - T // n * n]])
+    got = m.router_select_backward(l, ids, dps, renormalize=False)
+    for t in range(0, T, n):
+        h = min(n, T - t)
+        for a, b in ((ids, want), (probs, p), (got, back)):
+            assert torch.equal(a[t:t + h], b[:h]), t
