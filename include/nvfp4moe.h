@@ -495,7 +495,8 @@ NVFP4MOE_API int nvfp4moe_mxfp4_dequantize(const nvfp4moe_mxfp4_tensor* q, uint1
 
 /* Dense MXFP4 linear: out [M, N] = bf16(Q(x) . Wq^T), with x [M, K] BF16 (rows
  * ldx apart) quantized into the workspace by scale_round, Wq one GEMM-layout
- * matrix [N, K] and FP32 accumulation.  M >= 0, K % 32 == 0, K < 2^24, any N.
+ * matrix [N, K] and FP32 accumulation.  M >= 0, K % 32 == 0, K < 2^24, any N
+ * (fewer than 2^24 tiles of 128 rows x 256 columns).
  * Requirements: x 16-byte aligned, ldx >= K and a multiple of 8; out aligned to
  * 2 bytes, ld_out >= N (8-byte stores where out, ld_out and N allow them); no
  * element of out shares memory with x, Wq or the workspace (x is still read

@@ -122,8 +122,9 @@ int mx_product(const uint16_t* x, int64_t M, int64_t ldx, const int32_t* offsets
     if (!aligned(x, 16) || ldx % 8 != 0 || !aligned(out, 2) || !aligned(offsets, 4)) return NVFP4_E_ALIGN;
     const int bm = mx_tile_rows();
     const int64_t tiles = grouped ? M / bm + std::min(M, E) : (M + bm - 1) / bm;
-    const int64_t col_tiles = (N + 63) / 64;  // at most
-    if (tiles * col_tiles >= ((int64_t)1 << 31) - 8) return NVFP4_E_SHAPE;
+    // One workgroup of 256 threads a tile, and a dispatch holds fewer than 2^32
+    // work-items.  (Tiles of 64 columns are taken for a few hundred at most.)
+    if (tiles * ((N + 255) / 256) >= ((int64_t)1 << 24) - 8) return NVFP4_E_SHAPE;
     uint8_t* ws = (uint8_t*)workspace;
     hipStream_t s = (hipStream_t)stream;
     const MxShape sh = mx_shape(Wq);

@@ -29,7 +29,7 @@ struct MxTile {
 // list (workgroups are dealt to them round-robin), in which eight row tiles
 // walk through the column tiles together, so that they share an L2.
 __device__ __forceinline__ MxTile mx_tile(const MxGemmParams& P, int bm, int bn) {
-    // (tiles x column tiles < 2^31, checked on the host)
+    // (tiles x column tiles < 2^24, checked on the host)
     const uint32_t nm = P.tiles ? (uint32_t)*P.n_tiles : (uint32_t)((P.M + bm - 1) / bm);
     const uint32_t total = nm * (uint32_t)P.col_tiles, per = (total + 7) / 8;
     const uint32_t at = blockIdx.x >> 3, idx = (blockIdx.x & 7) * per + at;

@@ -129,6 +129,17 @@ def test_mxfp4_refuses_bad_arguments(m):
     assert lin(M=0, x=None, out=None) == grp(R=0, x=None, out=None, off=None) == 0
 
 
+def test_mxfp4_refuses_more_tiles_than_a_launch_takes(m):
+    """A workgroup of 256 threads a tile of 128 rows x 256 columns, fewer than 2^32 work-items a dispatch."""
+    L = m.lib()
+    for mats, N, M in ((1, 1 << 26, 64 * 128), (2, 1 << 25, 126 * 128)):  # 2^24 tiles each
+        ws = L.nvfp4moe_mxfp4_workspace_bytes(M, 32, mats)
+        q = _q(m, mats, N, 32)
+        if mats == 1:
+            assert L.nvfp4moe_mxfp4_linear(FAKE, M, 32, q, FAKE, N, 0, FAKE, ws, None) == SHAPE
+        assert L.nvfp4moe_mxfp4_grouped_linear(FAKE, M, 32, FAKE, q, FAKE, N, 0, FAKE, ws, None) == SHAPE
+
+
 def _table(m, *grads):
     return (m.Grad * len(grads))(*[m.Grad(*g) for g in grads])
 
