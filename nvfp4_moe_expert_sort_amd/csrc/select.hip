@@ -324,38 +324,28 @@ __global__ void __launch_bounds__(kSelWaves * 64, 4) router_select_kernel(Select
     for (int i = 0; i < NV; i++) l[i] = clean(l[i]);
     float max_l = 0.0f;
     double inv = 1.0;  // 1 / the softmax's denominator
-    if (!sigmoid && (scores || !P.renorm)) {
+    double key[NV];    // v, or the scores that TOP2 groups add up
+    if (sigmoid && scores) {
+#pragma unroll
+        for (int i = 0; i < NV; i++) key[i] = sigmoid64(l[i]);
+    } else if (!sigmoid && (scores || !P.renorm)) {
         float mx = l[0];
 #pragma unroll
         for (int i = 1; i < NV; i++) mx = fmaxf(mx, l[i]);
         max_l = fmaxf(tok_max<LT>(mx), -kFltMax);
-        if (!scores) {  // the denominator alone: FP32 terms, no choice depends on it
-            float sum = 0.0f;
+        double sum = 0.0;
 #pragma unroll
-            for (int i = 0; i < NV; i++) sum += __builtin_amdgcn_exp2f((l[i] - max_l) * 1.4426950408889634f);
-            inv = rcp64(fmax((double)tok_sum<LT>(sum), 1e-300));
-        }
+        for (int i = 0; i < NV; i++) sum += key[i] = exp64_neg((double)l[i] - (double)max_l);
+        inv = rcp64(fmax(tok_sum<LT>(sum), 1e-300));  // (no usable expert: 0)
+#pragma unroll
+        for (int i = 0; i < NV; i++) key[i] *= inv;
     }
-    double key[NV];  // v, or the scores that TOP2 groups add up
-    if (scores) {
-        if (sigmoid) {
-#pragma unroll
-            for (int i = 0; i < NV; i++) key[i] = sigmoid64(l[i]);
-        } else {
-            double sum = 0.0;
-#pragma unroll
-            for (int i = 0; i < NV; i++) sum += key[i] = exp64_neg((double)l[i] - (double)max_l);
-            inv = rcp64(fmax(tok_sum<LT>(sum), 1e-300));  // (no usable expert: 0)
-#pragma unroll
-            for (int i = 0; i < NV; i++) key[i] *= inv;
-        }
-        if (biased) {
-#pragma unroll
-            for (int i = 0; i < NV; i++) key[i] += (double)bias[i];
-        }
-    } else {
+    if (!scores) {
 #pragma unroll
         for (int i = 0; i < NV; i++) key[i] = (double)(l[i] + 0.0f);  // (-0 as +0)
+    } else if (biased) {
+#pragma unroll
+        for (int i = 0; i < NV; i++) key[i] += (double)bias[i];
     }
     // Unavailable experts: an unusable logit or bias.
 #pragma unroll

@@ -370,3 +370,24 @@ def test_select_on_a_side_stream_and_in_a_graph(gpu):
         want = m.router_select(l, 8)
         back = m.router_select_backward(l, want[0], dp)
         assert torch.equal(out[0], want[0]) and torch.equal(out[1], want[1]) and torch.equal(dl, back)
+
+
+@pytest.mark.parametrize("E,k", [(5, 3), (128, 8), (256, 8), (256, 20), (700, 8)])
+@pytest.mark.parametrize("std", [0.5, 4.0, 30.0])
+def test_select_softmax_over_all_is_formed_in_fp64(gpu, E, k, std):
+    """Weights without renormalisation: one rounding of an FP64 value (scores within 2^-43, so 1.01 x 2^-24), and the
+    same bits with a bias of zero."""
+    import torch
+    m, dev = gpu
+    rng = np.random.default_rng(E + k)
+    for bf16 in (False, True):
+        l = _logits(rng, 57, E, bf16, std).to(dev)
+        l[5] = -torch.inf
+        l[6, ::3] = -torch.inf
+        for groups in (dict(), dict(n_groups=4, top_groups=1)) if E % 4 == 0 else (dict(),):
+            ids, probs, ref = _select(m, l, k, renorm=False, **groups)
+            for t, (i, p) in enumerate(ref):
+                assert ids[t].tolist() == i.tolist()
+                assert (np.abs(probs[t] - p) <= 1.01 * U * np.abs(p) + 2.0 ** -149).all(), (t, probs[t], p)
+            zero = m.router_select(l, k, bias=torch.zeros(E, device=dev), renormalize=False, **groups)
+            assert np.array_equal(zero[1].cpu().numpy(), probs)
