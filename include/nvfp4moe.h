@@ -441,6 +441,7 @@ NVFP4MOE_API int nvfp4moe_router_select(const nvfp4moe_select_config* cfg, const
  *   sigmoid, renormalize 1   the same times (1 - sigmoid(l_k))
  *   sigmoid, renormalize 0   scale w_k (1 - w_k) dp_k at the ids
  *   softmax, renormalize 0   scale s_e ([e selected] dp_e - sum_j w_j dp_j) at every expert
+ * formed in FP64 and rounded at the end.
  * dlogits may not overlap the inputs.  Errors and requirements as for the
  * forward (n_groups, top_groups and group_score are checked and not used). */
 NVFP4MOE_API int nvfp4moe_router_select_backward(const nvfp4moe_select_config* cfg, const void* logits, int64_t ld, int64_t T,

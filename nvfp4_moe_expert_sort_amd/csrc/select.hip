@@ -150,6 +150,11 @@ __device__ __forceinline__ double rcp64(double d) {
     const double r = __builtin_amdgcn_rcp(d);
     return __builtin_fma(__builtin_fma(-d, r, 1.0), r, r);
 }
+// The same within some 2^-52, by a second step: for weights whose distance from 1 counts.
+__device__ __forceinline__ double rcp64_full(double d) {
+    const double r = rcp64(d);
+    return __builtin_fma(__builtin_fma(-d, r, 1.0), r, r);
+}
 // e^x for x <= 0, 0 where FP64 has no number so small: experts masked with the
 // type's lowest value have scores of exactly 0 and tie.
 __device__ __forceinline__ double exp64_neg(double x) { return exp64(max64(x, -746.0)); }
@@ -190,7 +195,7 @@ __device__ __forceinline__ double slot_weight(float l, bool live, bool sigmoid, 
             w = sigmoid64(l);
     }
     const double sum = tok_sum<LT>(w);
-    return live ? w * rcp64(sum) : 0.0;
+    return live ? w * rcp64_full(sum) : 0.0;
 }
 
 // Keeps LDS accesses before it before those after it: a wavefront's LDS
@@ -480,10 +485,12 @@ __global__ void __launch_bounds__(kSelWaves * 64, 4) router_select_kernel(Select
 // dp the upstream gradient and w the weights of the chosen experts:
 //   renormalised  d_k = c w_k (dp_k - sum_j dp_j w_j), times (1 - sigma_k) for sigmoid scores;
 //   sigmoid       d_k = c w_k dp_k (1 - sigma_k);
-//   softmax       d_k = c w_k dp_k at the chosen experts, and -c s_e sum_j dp_j w_j at every expert.
-// One pass: lane k forms d_k in FP64 (K values a token) and puts it into the
-// token's row in LDS, which only its own wavefront uses, and the row is written
-// whole.  T = 4096, E = 256, FP32, renormalised: 4.4 us for 4.3 MB (a launch and
+//   softmax       d_k = c w_k (dp_k - sum_j dp_j w_j) at the chosen experts, and -c s_e sum_j dp_j w_j at the others.
+// One pass: lane k forms d_k and puts it into the token's row in LDS, which only
+// its own wavefront uses, and the row is written whole.  All of it is FP64, the
+// softmax's terms too: dp_k - sum_j dp_j w_j is a small difference where one
+// expert has nearly all the weight.  Each value is rounded to FP32 once, and a
+// BF16 one from there (half a step of BF16 and 2^-24 more).  T = 4096, E = 256, FP32, renormalised: 4.4 us for 4.3 MB (a launch and
 // one chain of loads); T = 32749, E = 128, BF16, softmax over all: 7.2 us for
 // 18.9 MB, of which the copy rate allows 3.6.
 template <int LT, int NV, typename L>
@@ -521,57 +528,63 @@ __global__ void __launch_bounds__(kSelWaves * 64) router_select_backward_kernel(
     lds_order();
     const bool twice = __ballot(live && tags[e] != (uint32_t)lane) != 0;
     lds_order();
-#pragma unroll
-    for (int i = 0; i < NV / 4; i++)
-        *reinterpret_cast<float4*>(&rows[slot][(i * LT + lane) * 4]) = float4{0.0f, 0.0f, 0.0f, 0.0f};
     float max_l = 0.0f;
     double inv = 1.0;  // 1 / the softmax's denominator
+    double s[NV];      // its terms
     if (dense) {
         float mx = -kFltMax;
 #pragma unroll
         for (int i = 0; i < NV; i++) mx = max32(mx, l[i] = clean(l[i]));
         max_l = tok_max<LT>(mx);
-        float sum = 0.0f;
+        double sum = 0.0;
 #pragma unroll
-        for (int i = 0; i < NV; i++) sum += l[i] = __builtin_amdgcn_exp2f((l[i] - max_l) * 1.4426950408889634f);
-        inv = rcp64(fmax((double)tok_sum<LT>(sum), 1e-300));
+        for (int i = 0; i < NV; i++) sum += s[i] = exp64_neg((double)l[i] - (double)max_l);
+        inv = rcp64_full(fmax(tok_sum<LT>(sum), 1e-300));
     }
     const double w = slot_weight<LT>(lk, live, sigmoid, P.renorm, max_l, inv);
     double mean = 0.0;
     if (P.renorm || dense) mean = tok_sum<LT>(live ? w * (double)dp : 0.0);
-    double d = 0.0;
-    if (live) {
-        d = w * (P.renorm ? (double)dp - mean : (double)dp) * (double)P.scale;
-        if (sigmoid) d *= sigmoid64(-lk);  // 1 - sigma(l)
-    }
-    float acc = (float)d;
+    // dp and the slots of the lane's expert: its first slot takes them all
+    double up = (double)dp, slots = 1.0;
     bool first = live;
-    if (twice) {  // its first slot takes the sum, in slot order
-        acc = 0.0f;
+    if (twice) {
+        up = slots = 0.0;
         for (int k = 0; k < P.K; k++) {
             const int ek = __shfl(live ? e : -1, k, LT);
-            const float dk = __shfl((float)d, k, LT);
+            const float dk = __shfl(dp, k, LT);
             if (ek == e) {
-                acc += dk;
+                up += (double)dk;
+                slots += 1.0;
                 first = first && k >= lane;
             }
         }
     }
+    double d = 0.0;
+    if (first) {
+        d = w * (up - (P.renorm ? slots : 1.0) * mean) * (double)P.scale;
+        if (sigmoid) d *= sigmoid64(-lk);  // 1 - sigma(l)
+    }
+    const double all = -mean * (double)P.scale * inv;
+#pragma unroll
+    for (int i = 0; i < NV / 4; i++) {
+        float4 q = {0.0f, 0.0f, 0.0f, 0.0f};
+        if (dense) {  // (+0 where the term is 0)
+            q.x = (float)__builtin_fma(s[4 * i], all, 0.0), q.y = (float)__builtin_fma(s[4 * i + 1], all, 0.0);
+            q.z = (float)__builtin_fma(s[4 * i + 2], all, 0.0), q.w = (float)__builtin_fma(s[4 * i + 3], all, 0.0);
+        }
+        *reinterpret_cast<float4*>(&rows[slot][(i * LT + lane) * 4]) = q;
+    }
     lds_order();
-    if (first) rows[slot][e] = acc;
+    if (first) rows[slot][e] = (float)d;
     lds_order();
     if (t >= P.T) return;
-    const float all = dense ? (float)(-mean * (double)P.scale * inv) : 0.0f;
     L* out = (L*)P.dlogits + t * P.ld_out;
 #pragma unroll
     for (int i = 0; i < NV / 4; i++) {
         const int e0 = (i * LT + lane) * 4;
         if (e0 >= P.E) continue;
         const float4 q = *reinterpret_cast<const float4*>(&rows[slot][e0]);
-        float v[4] = {q.x, q.y, q.z, q.w};
-        if (dense)
-#pragma unroll
-            for (int j = 0; j < 4; j++) v[j] = __builtin_fmaf(l[4 * i + j], all, v[j]);
+        const float v[4] = {q.x, q.y, q.z, q.w};
         if constexpr (sizeof(L) == 4) {
             if (P.vec_out && e0 + 4 <= P.E)
                 *reinterpret_cast<float4*>(out + e0) = float4{v[0], v[1], v[2], v[3]};

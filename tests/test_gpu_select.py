@@ -1,10 +1,10 @@
 """GPU expert selection (nvfp4moe_router_select) and its gradient against the FP64 plain forms of tests/plain_ops.py.
 
-Bars: ids equal.  probs: formed in FP64 and rounded once, half a step of FP32 (2^-24 relative); the softmax over all
-experts without a bias has a denominator of FP32 terms: three roundings in each exponent (3 x 2^-24 |x|, which over a
-softmax's terms sums to at most 3 ln E <= 21 steps of 2^-24), one step (2) of the exponential, at most 22 additions:
-48 x 2^-24.  Gradients: one rounding of an FP64 value, or with that denominator the same 48 steps on each of the two
-terms that are added (and 3 |l - max| more on the one whose exponential is its own)."""
+Bars: ids equal.  probs: formed in FP64 and rounded once, half a step of FP32 (2^-24 relative).  Gradients: one rounding
+of an FP64 value (in BF16 a second one).  The first tests allow the softmax over all experts what FP32 terms would need:
+three roundings in each exponent (3 x 2^-24 |x|, which over a softmax's terms sums to at most 3 ln E <= 21 steps of
+2^-24), one step (2) of the exponential, at most 22 additions: 48 x 2^-24 on each of the two terms of a gradient (and
+3 |l - max| more on the one whose exponential is its own); the last ones hold it to FP64."""
 import numpy as np
 import pytest
 
@@ -391,3 +391,30 @@ def test_select_softmax_over_all_is_formed_in_fp64(gpu, E, k, std):
                 assert (np.abs(probs[t] - p) <= 1.01 * U * np.abs(p) + 2.0 ** -149).all(), (t, probs[t], p)
             zero = m.router_select(l, k, bias=torch.zeros(E, device=dev), renormalize=False, **groups)
             assert np.array_equal(zero[1].cpu().numpy(), probs)
+
+
+@pytest.mark.parametrize("E,k", [(7, 3), (128, 8), (250, 16), (250, 20), (600, 8)])
+@pytest.mark.parametrize("gap", [0.0, 5.0, 12.0, 20.0, 34.0])
+def test_select_backward_of_confident_tokens(gpu, E, k, gap):
+    """Softmax over all experts with one logit `gap` above the others: s_e (dp_e - mean) vanishes as 1 - s does, and is
+    formed in FP64.  With r = 1 - max s, the mean is off by some 2^-50 of the largest dp for the top weight and by
+    2^-45 r of it for the others (the exponential's 2^-46), so at expert e the bar is one rounding and
+    s_e (2^-49 + 2^-44 r) sum |dp|.  With repeated ids too."""
+    import torch
+    m, dev = gpu
+    rng = np.random.default_rng(E + int(gap))
+    for bf16 in (False, True):
+        l = _logits(rng, 40, E, False, 1.0)
+        l[torch.arange(40), torch.from_numpy(rng.integers(0, E, 40))] += gap
+        l = (l.to(torch.bfloat16) if bf16 else l).to(dev)
+        ids = m.router_select(l, k)[0].cpu().numpy()
+        ids[30:, 1] = ids[30:, 0]
+        dp = rng.standard_normal((40, k)).astype(np.float32)
+        got = _np(m.router_select_backward(l, torch.from_numpy(ids).to(dev), torch.from_numpy(dp).to(dev), renormalize=False,
+                                           scale=2.5))
+        rnd, step = (2.0 ** -8, 2.0 ** -133) if bf16 else (1.01 * U, 2.0 ** -149)
+        for t, row in enumerate(_np(l)):
+            ref = R.select_backward_row(row, ids[t], dp[t], renorm=False, scale=2.5)
+            s = R.scores(row, np.ones(E, bool), False)
+            tol = rnd * np.abs(ref) + 2.5 * s * np.abs(dp[t]).sum() * (2.0 ** -49 + 2.0 ** -44 * (1 - s.max())) + step
+            assert (np.abs(got[t] - ref) <= tol).all(), (t, np.abs(got[t] - ref).max(), ref[ids[t]])
