@@ -91,18 +91,20 @@ __global__ void __launch_bounds__(256) grad_scale_kernel(const GradChunk* __rest
     for (int i = threadIdx.x; i < n_partial; i += 256) s += partial[i];
     const double norm = __builtin_sqrt(block_sum(s));
     if (blockIdx.x == 0 && threadIdx.x == 0) *norm_out = norm;
-    // An Inf or NaN among the gradients leaves them as they are.
+    // An Inf or NaN among the gradients leaves them as they are, to the bit: a
+    // conversion would make signaling NaNs quiet.
     const double coef = norm > max_norm && norm < __builtin_inf() ? max_norm / norm : 1.0;
+    const bool same = coef == 1.0;
     for (int64_t k0 = blockIdx.x; k0 < n_chunks; k0 += gridDim.x) {
         const GradChunk c = plan[n_chunks - 1 - k0];
-        if (coef == 1.0 && c.in == c.out) continue;
+        if (same && c.in == c.out) continue;
         const uint32_t per = c.bf16 ? 8 : 4, body = (c.n - c.head) / per, tail = c.head + body * per;
         auto one = [&](uint32_t i) {
             const float g = (float)((double)grad_at(c, i) * coef);
             if (c.bf16)
-                ((uint16_t*)c.out)[i] = (uint16_t)bf16_hw(g);
+                ((uint16_t*)c.out)[i] = same ? ((const uint16_t*)c.in)[i] : (uint16_t)bf16_hw(g);
             else
-                ((float*)c.out)[i] = g;
+                ((uint32_t*)c.out)[i] = same ? ((const uint32_t*)c.in)[i] : __float_as_uint(g);
         };
         if (threadIdx.x < c.head) one(threadIdx.x);
         if (c.out_vec) {
@@ -110,6 +112,7 @@ __global__ void __launch_bounds__(256) grad_scale_kernel(const GradChunk* __rest
             const u32x4* v = reinterpret_cast<const u32x4*>((const uint8_t*)c.in + skip);
             u32x4* o = reinterpret_cast<u32x4*>((uint8_t*)c.out + skip);
             auto scale = [&](u32x4 q) {
+                if (same) return q;
 #pragma unroll
                 for (int j = 0; j < 4; j++) {
                     if (c.bf16) {

@@ -155,3 +155,21 @@ def test_refusals(gpu):
         m.GradSet([g], [g.to(torch.bfloat16)])
     with pytest.raises(m.Nvfp4Error):
         m.clip_grad_norm(m.GradSet([g]), -1.0)
+
+
+@pytest.mark.parametrize("max_norm", [1e-3, float("inf")])
+def test_nonfinite_gradients_are_copied_to_the_bit(gpu, max_norm):
+    """Outputs apart from the inputs, aligned with them and not: signaling and quiet NaNs keep every bit."""
+    import torch
+    m, dev = gpu
+    rng = np.random.default_rng(17)
+    for kind, bits, nans in ((torch.float32, torch.int32, (0x7F800001, -0x7FFFFF, 0x7FC12345, -1, 0x7F800000)),
+                             (torch.bfloat16, torch.int16, (0x7F81, -0x7F, 0x7FD5, -1, 0x7F80))):
+        for shift in (0, 1):
+            g = torch.randn(5000, device=dev).to(kind)[3:]
+            at = torch.from_numpy(rng.choice(4997, 400, replace=False)).to(dev)
+            g.view(bits)[at] = torch.tensor(nans, dtype=bits, device=dev).repeat(80)
+            g.view(bits)[0] = nans[0]
+            out = torch.zeros(5001, device=dev, dtype=kind)[3 + shift:][:4997]
+            assert not np.isfinite(float(m.clip_grad_norm(m.GradSet([g], [out]), max_norm)))
+            assert torch.equal(out.view(bits), g.view(bits))
