@@ -101,10 +101,10 @@ namespace {
 // The builtin would make the compiler wait for every load in flight before
 // each LDS read, since it cannot tell the buffers apart; here the waits are
 // written out (`arrive`).  The load has no output register, and its address
-// register is read when it issues.  m0, which the compiler does not list as
-// clobbered, has no other user in these kernels.
+// register is read when it issues.  The LDS address is an operand in m0, so the
+// compiler knows what m0 holds; the load must not follow that move directly.
 __device__ __forceinline__ void dma16(const uint8_t* base, uint32_t off, uint32_t lds) {
-    asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, %1" ::"v"(off), "s"(base), "s"(lds) : "memory");
+    asm volatile("s_nop 0\n\tglobal_load_lds_dwordx4 %0, %1" ::"v"(off), "s"(base), "{m0}"(lds) : "memory");
 }
 __device__ __forceinline__ uint32_t lds_addr(const void* p) {
     return (uint32_t)(uintptr_t)(const __attribute__((address_space(3))) void*)p;
