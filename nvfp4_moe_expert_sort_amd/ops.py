@@ -27,13 +27,18 @@ def _elsewhere(t, stream):
 
 
 @contextlib.contextmanager
-def _there(t, stream):
+def _there(stream, t, *others):
     """`t`'s device and `stream` (default: that device's current one) made current, so that outputs are allocated
-    where they are used."""
+    where they are used.  The call's tensors count as in use on a stream that is named: their memory, which belongs to
+    another stream, is not handed out again before the call's work is done, even if the caller drops them."""
     if stream is not None and stream.device != t.device:
         raise ValueError(f"the stream is on {stream.device}, the tensors on {t.device}")
     with torch.cuda.device(t.device), torch.cuda.stream(stream):
         yield
+    if stream is not None:
+        for each in (t, *others):
+            if each is not None:
+                each.record_stream(stream)
 
 
 def _raw_stream(t):
@@ -67,7 +72,7 @@ def _select_config(*fields):
 def router_logits(x, w_router, out=None, stream=None):
     """nvfp4moe_router_logits: x [T,H] BF16, w_router [E,H] BF16 -> logits [T,E] f32 (router_topk's)."""
     if _elsewhere(x, stream):
-        with _there(x, stream):
+        with _there(stream, x, w_router, out):
             return router_logits(x, w_router, out)
     T, H = x.shape
     E = w_router.shape[0]
@@ -100,7 +105,7 @@ def router_select(logits, k: int, bias=None, score: int = SCORE_SOFTMAX, renorma
     kind, ld = _logits("router_select", logits, bias)
     T, E = logits.shape
     if _elsewhere(logits, stream):
-        with _there(logits, stream):
+        with _there(stream, logits, bias, *(out or ())):
             return router_select(logits, k, bias, score, renormalize, scale, n_groups, top_groups, group_score, out)
     if out is None:
         ids = torch.empty((T, max(k, 0)), dtype=torch.int32, device=logits.device)
@@ -126,7 +131,7 @@ def router_select_backward(logits, ids, dprobs, bias=None, score: int = SCORE_SO
     _need("router_select_backward", ids, "ids", (torch.int32,), (T, k), logits.device)
     _need("router_select_backward", dprobs, "dprobs", (torch.float32,), (T, k), logits.device)
     if _elsewhere(logits, stream):
-        with _there(logits, stream):
+        with _there(stream, logits, ids, dprobs, bias, out):
             return router_select_backward(logits, ids, dprobs, bias, score, renormalize, scale, out)
     if out is None:
         out = torch.empty((T, E), dtype=logits.dtype, device=logits.device)
@@ -147,7 +152,7 @@ def mxfp4_quantize(x, scale_round: int = MXFP4_SCALE_FLOOR, out=None, stream=Non
     rows, cols = x.shape
     _need("mxfp4_quantize", x, "x", _BF16, (rows, cols), x.device, contiguous=False)
     if _elsewhere(x, stream):
-        with _there(x, stream):
+        with _there(stream, x, *(out or ())):
             return mxfp4_quantize(x, scale_round, out)
     if out is None:
         codes = torch.empty((rows, cols // 2), dtype=torch.uint8, device=x.device)
@@ -170,7 +175,7 @@ def mxfp4_dequantize(codes, scales, out=None, stream=None):
     _need("mxfp4_dequantize", codes, "codes", (torch.uint8,), (rows, half), codes.device)
     _need("mxfp4_dequantize", scales, "scales", (torch.uint8,), (rows, cols // 32), codes.device)
     if _elsewhere(codes, stream):
-        with _there(codes, stream):
+        with _there(stream, codes, scales, out):
             return mxfp4_dequantize(codes, scales, out)
     if out is None:
         out = torch.empty((rows, cols), dtype=torch.bfloat16, device=codes.device)
@@ -198,7 +203,7 @@ class Mxfp4Weights:
         """nvfp4moe_mxfp4_quantize: BF16 w [n_mats, rows, cols] -> these buffers, in place."""
         _need("Mxfp4Weights.quantize_from", w, "w", _BF16, self.shape, self.codes.device)
         if _elsewhere(w, stream):
-            with _there(w, stream):
+            with _there(stream, w, self.codes, self.scales):
                 return self.quantize_from(w, scale_round)
         _check(lib().nvfp4moe_mxfp4_quantize(w.data_ptr(), self.shape[2], self.Wq, scale_round, _raw_stream(w)),
                "nvfp4moe_mxfp4_quantize")
@@ -207,7 +212,7 @@ class Mxfp4Weights:
     def dequantize(self, stream=None):
         """nvfp4moe_mxfp4_dequantize: the values, [n_mats, rows, cols] bfloat16."""
         if _elsewhere(self.codes, stream):
-            with _there(self.codes, stream):
+            with _there(stream, self.codes, self.scales):
                 return self.dequantize()
         out = torch.empty(self.shape, dtype=torch.bfloat16, device=self.codes.device)
         _check(lib().nvfp4moe_mxfp4_dequantize(self.Wq, out.data_ptr(), self.shape[2], _raw_stream(out)),
@@ -234,7 +239,7 @@ def _mxfp4_product(where, x, offsets, W, scale_round, workspace, out, stream):
     if offsets is not None:
         _need(where, offsets, "offsets", (torch.int32,), (E + 1,), device)
     if _elsewhere(x, stream):
-        with _there(x, stream):
+        with _there(stream, x, offsets, W.codes, W.scales, workspace, out):
             return _mxfp4_product(where, x, offsets, W, scale_round, workspace, out, None)
     if out is None:
         out = torch.empty((M, N), dtype=x.dtype, device=device)
@@ -298,11 +303,8 @@ def clip_grad_norm(grads: GradSet, max_norm: float, stream=None):
     """nvfp4moe_clip_grad_norm: the global norm (float64 [1], on the GPU); the set's outputs hold the gradients scaled
     to at most max_norm (unchanged if the norm is not finite).  max_norm = inf takes the norm only."""
     if _elsewhere(grads.plan, stream):
-        with _there(grads.plan, stream):
-            norm = clip_grad_norm(grads, max_norm)
-        if stream is not None and grads.n_chunks:
-            grads.plan.record_stream(stream)
-        return norm
+        with _there(stream, grads.plan, *grads.grads, *grads.out):
+            return clip_grad_norm(grads, max_norm)
     words = lib().nvfp4moe_clip_workspace_bytes() // 8
     buf = torch.empty((1 + words,), dtype=torch.float64, device=grads.device)  # the norm, then the partial sums
     at = buf.data_ptr()
