@@ -328,27 +328,89 @@ __global__ void __launch_bounds__(256, 2) mx_gemm_wide_kernel(MxGemmParams P) {
 // across its column groups.
 constexpr int kSmallRing = 3, kSmallMT = 2, kSmallBM = 16 * kSmallMT;
 
+namespace {
+
+struct MxPass {
+    int32_t mat;
+    int64_t row0;
+    int32_t rows;  // up to kSmallBM
+};
+
+// Pass blockIdx.y of a grouped product, of all experts' passes of kSmallBM rows
+// in expert order; false past the last.  Offsets count as in build_tiles:
+// clamped to [0, M], and the largest up to an expert is where it ends.  Every
+// wavefront finds it for itself, each lane with E / 64 consecutive experts.
+__device__ __forceinline__ bool mx_pass(const MxGemmParams& P, MxPass& T) {
+    constexpr int kPer = kMaxExperts / 64;
+    const int lane = threadIdx.x & 63, per = (P.E + 63) / 64, e0 = lane * per;
+    const int32_t M = (int32_t)P.M, pass = (int32_t)blockIdx.y;
+    int32_t end[kPer], top = 0;
+    if (lane == 0) top = max(0, min(P.offsets[0], M));
+#pragma unroll
+    for (int i = 0; i < kPer; i++) {
+        if (i >= per) break;
+        end[i] = top = max(top, e0 + i < P.E ? min(P.offsets[e0 + i + 1], M) : 0);
+    }
+    int32_t before = lane == 0 ? max(0, min(P.offsets[0], M)) : 0;  // where the lane's first expert begins
+#pragma unroll
+    for (int o = 1; o < 64; o <<= 1) {
+        const int32_t u = __shfl_up(top, o, kWave);
+        if (lane >= o) top = max(top, u);
+    }
+    const int32_t left = __shfl_up(top, 1, kWave);
+    if (lane > 0) before = left;
+    int32_t sum = 0;  // passes of the lane's experts, then of all up to them
+    int32_t begin = before;
+#pragma unroll
+    for (int i = 0; i < kPer; i++) {
+        if (i >= per) break;
+        end[i] = max(end[i], begin);
+        sum += (end[i] - begin + kSmallBM - 1) / kSmallBM;
+        begin = end[i];
+    }
+    const int32_t own = sum;
+#pragma unroll
+    for (int o = 1; o < 64; o <<= 1) {
+        const int32_t u = __shfl_up(sum, o, kWave);
+        if (lane >= o) sum += u;
+    }
+    int32_t at = pass - (sum - own);  // among the lane's passes, if it is one
+    const uint64_t owner = __ballot(at >= 0 && at < own);
+    if (owner == 0) return false;
+    int32_t mat = 0, row0 = 0, rows = 0;
+    begin = before;
+#pragma unroll
+    for (int i = 0; i < kPer; i++) {
+        if (i >= per) break;
+        const int32_t n = (end[i] - begin + kSmallBM - 1) / kSmallBM;
+        if (at >= 0 && at < n) {
+            mat = e0 + i;
+            row0 = begin + at * kSmallBM;
+            rows = min(end[i] - row0, kSmallBM);
+        }
+        at -= n;
+        begin = end[i];
+    }
+    const int src = __builtin_ctzll(owner);
+    T.mat = __builtin_amdgcn_readlane(mat, src);
+    T.row0 = __builtin_amdgcn_readlane(row0, src);
+    T.rows = __builtin_amdgcn_readlane(rows, src);
+    return true;
+}
+
+}  // namespace
+
 __global__ void __launch_bounds__(256, 4) mx_gemm_small_kernel(MxGemmParams P) {
     // codes [kSmallBM][lds_codes], then scale words [kSmallBM][lds_scales]
     extern __shared__ __attribute__((aligned(16))) uint8_t smem[];
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), q = lane >> 4, r = lane & 15;
-    int64_t row0 = 0, row1 = P.M;
-    if (P.offsets) {
-        // as build_tiles: clamped to [0, M], the largest of offsets 0..e
-        const int e = blockIdx.y;
-        int32_t lo = 0;
-        for (int i = lane; i <= e; i += 64) lo = max(lo, min(P.offsets[i], (int32_t)P.M));
-        const int32_t hi = min(P.offsets[e + 1], (int32_t)P.M);
-#pragma unroll
-        for (int o = 32; o > 0; o >>= 1) lo = max(lo, __shfl_xor(lo, o, kWave));
-        row0 = __builtin_amdgcn_readfirstlane(lo);
-        row1 = hi;
-        if (row0 >= row1) return;
-    }
+    MxPass T{0, 0, (int32_t)P.M};
+    if (P.offsets && !mx_pass(P, T)) return;
+    const uint32_t rows = (uint32_t)T.rows;
     const int32_t chunks = P.chunks, quads = P.quads;
     const int32_t col_groups = (P.N + 63) / 64;
     const int32_t mine = (col_groups - blockIdx.x + gridDim.x - 1) / gridDim.x;  // this workgroup's
-    const int64_t mat_tile = (int64_t)blockIdx.y * P.row_tiles;
+    const int64_t mat_tile = (int64_t)T.mat * P.row_tiles;
     const uint32_t lane16 = lane * 16, lane4 = lane * 4;
     const uint32_t groups = (uint32_t)chunks * 16;  // 8-column groups of a row, padded to whole chunks
     uint8_t* sc = smem + kSmallBM * P.lds_codes;
@@ -376,66 +438,62 @@ __global__ void __launch_bounds__(256, 4) mx_gemm_small_kernel(MxGemmParams P) {
             }
         }
     };
-    for (int64_t at = row0; at < row1; at += kSmallBM) {
-        const uint32_t rows = (uint32_t)min<int64_t>(kSmallBM, row1 - at);
-        lg = lj = 0;
-        column_group(0);
+    lg = lj = 0;
+    column_group(0);
 #pragma unroll
-        for (int s = 0; s < kSmallRing; s++) load(s);
-        for (uint32_t i0 = threadIdx.x; i0 < rows * groups; i0 += 4 * 256) {
-            u32x4 v[4];
-            uint32_t row[4], col[4];
+    for (int s = 0; s < kSmallRing; s++) load(s);
+    for (uint32_t i0 = threadIdx.x; i0 < rows * groups; i0 += 4 * 256) {
+        u32x4 v[4];
+        uint32_t row[4], col[4];
 #pragma unroll
-            for (int u = 0; u < 4; u++) {
-                const uint32_t i = i0 + u * 256;
-                row[u] = __umulhi(i, P.groups_magic);
-                col[u] = (i - row[u] * groups) * 8;
-                v[u] = u32x4{0u, 0u, 0u, 0u};
-                if (i < rows * groups && col[u] < P.cols)
-                    v[u] = *reinterpret_cast<const u32x4*>(P.x + (at + row[u]) * P.ldx + col[u]);
-            }
-#pragma unroll
-            for (int u = 0; u < 4; u++) {
-                const uint32_t byte = mx_scale_byte(mx_block_max(v[u]), P.up);
-                if (i0 + u * 256 >= rows * groups) continue;
-                *reinterpret_cast<uint32_t*>(smem + row[u] * P.lds_codes + col[u] / 2) = mx_encode8(v[u], byte);
-                const uint32_t b = col[u] / 32, c = b >> 2;
-                if ((threadIdx.x & 3) == 0) sc[row[u] * P.lds_scales + (c >> 2) * 16 + (b & 3) * 4 + (c & 3)] = (uint8_t)byte;
-            }
+        for (int u = 0; u < 4; u++) {
+            const uint32_t i = i0 + u * 256;
+            row[u] = __umulhi(i, P.groups_magic);
+            col[u] = (i - row[u] * groups) * 8;
+            v[u] = u32x4{0u, 0u, 0u, 0u};
+            if (i < rows * groups && col[u] < P.cols)
+                v[u] = *reinterpret_cast<const u32x4*>(P.x + (T.row0 + row[u]) * P.ldx + col[u]);
         }
-        __syncthreads();
-        const bool two = rows > 16;
-        f32x4 acc[kSmallMT] = {};
-        int32_t g = 0, j = 0;  // the product cursor
-        while (j < mine) {
 #pragma unroll
-            for (int s = 0; s < kSmallRing; s++) {
-                if (j >= mine) break;
+        for (int u = 0; u < 4; u++) {
+            const uint32_t byte = mx_scale_byte(mx_block_max(v[u]), P.up);
+            if (i0 + u * 256 >= rows * groups) continue;
+            *reinterpret_cast<uint32_t*>(smem + row[u] * P.lds_codes + col[u] / 2) = mx_encode8(v[u], byte);
+            const uint32_t b = col[u] / 32, c = b >> 2;
+            if ((threadIdx.x & 3) == 0) sc[row[u] * P.lds_scales + (c >> 2) * 16 + (b & 3) * 4 + (c & 3)] = (uint8_t)byte;
+        }
+    }
+    __syncthreads();
+    const bool two = rows > 16;
+    f32x4 acc[kSmallMT] = {};
+    int32_t g = 0, j = 0;  // the product cursor
+    while (j < mine) {
 #pragma unroll
-                for (int i = 0; i < kSmallMT; i++) {
-                    if (i > 0 && !two) break;
-                    const uint32_t as = *reinterpret_cast<const uint32_t*>(sc + (i * 16 + r) * P.lds_scales + g * 16 + q * 4);
+        for (int s = 0; s < kSmallRing; s++) {
+            if (j >= mine) break;
 #pragma unroll
-                    for (int cc = 0; cc < 4; cc++)
-                        if (g * 4 + cc < chunks) {
-                            const u32x4 a = *reinterpret_cast<const u32x4*>(smem + (i * 16 + r) * P.lds_codes +
-                                                                            (g * 4 + cc) * 64 + q * 16);
-                            acc[i] = mx_mfma_sel(cc, w[s][cc], a, acc[i], ws[s], as);
-                        }
-                }
-                load(s);
-                if (++g == quads) {
-                    const int32_t n = ((int32_t)blockIdx.x + j * (int32_t)gridDim.x) * 64 + wave * 16 + q * 4;
-                    for (int i = 0; i < kSmallMT; i++) {
-                        if (i * 16 + r < (int)rows) mx_store4(P, at + i * 16 + r, n, acc[i]);
-                        acc[i] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+            for (int i = 0; i < kSmallMT; i++) {
+                if (i > 0 && !two) break;
+                const uint32_t as = *reinterpret_cast<const uint32_t*>(sc + (i * 16 + r) * P.lds_scales + g * 16 + q * 4);
+#pragma unroll
+                for (int cc = 0; cc < 4; cc++)
+                    if (g * 4 + cc < chunks) {
+                        const u32x4 a = *reinterpret_cast<const u32x4*>(smem + (i * 16 + r) * P.lds_codes +
+                                                                        (g * 4 + cc) * 64 + q * 16);
+                        acc[i] = mx_mfma_sel(cc, w[s][cc], a, acc[i], ws[s], as);
                     }
-                    g = 0;
-                    j++;
+            }
+            load(s);
+            if (++g == quads) {
+                const int32_t n = ((int32_t)blockIdx.x + j * (int32_t)gridDim.x) * 64 + wave * 16 + q * 4;
+                for (int i = 0; i < kSmallMT; i++) {
+                    if (i * 16 + r < (int)rows) mx_store4(P, T.row0 + i * 16 + r, n, acc[i]);
+                    acc[i] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
                 }
+                g = 0;
+                j++;
             }
         }
-        if (at + kSmallBM < row1) __syncthreads();  // the next rows go into the same LDS
     }
 }
 
@@ -465,7 +523,10 @@ hipError_t launch_mx_gemm_small(MxGemmParams P, int64_t E, hipStream_t stream) {
     if (share > col_groups) share = col_groups;
     const int64_t each = (col_groups + share - 1) / share;  // evenly
     share = (col_groups + each - 1) / each;
-    hipLaunchKernelGGL(mx_gemm_small_kernel, dim3((unsigned)share, (unsigned)E), dim3(256),
+    // A pass of kSmallBM rows is a workgroup row: at most one an expert that is not full.
+    const int64_t passes = P.offsets ? P.M / kSmallBM + used : 1;
+    P.E = (int32_t)E;
+    hipLaunchKernelGGL(mx_gemm_small_kernel, dim3((unsigned)share, (unsigned)passes), dim3(256),
                        kSmallBM * (P.lds_codes + P.lds_scales), stream, P);
     return hipGetLastError();
 }

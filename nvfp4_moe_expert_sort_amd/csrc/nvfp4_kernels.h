@@ -184,6 +184,7 @@ struct MxGemmParams {
     uint32_t cols;
     bool up;
     const int32_t* offsets;  // [E + 1] of a grouped product, or null
+    int32_t E;               // set by the launcher
     int32_t lds_codes, lds_scales;  // bytes per row in LDS; set by the launcher
     uint32_t groups_magic;   // ceil(2^32 / 8-column groups of a row); set by the launcher
 };

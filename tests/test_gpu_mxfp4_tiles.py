@@ -191,3 +191,73 @@ def test_graphs_over_one_workspace_rebuild_the_table(gpu):
                 alone = torch.zeros(E + 1, dtype=torch.int32, device=dev)
                 alone[e + 1:] = 1
                 assert torch.equal(m.mxfp4_grouped_linear(x[hi - 1:hi], alone, w)[0], a[hi - 1])
+
+
+@pytest.mark.parametrize("E,rows,N,K", [(1, 16, 40, 96), (4, 64, 72, 160), (64, 1024, 33, 96), (65, 1040, 80, 256),
+                                        (128, 2048, 200, 320), (700, 9000, 48, 32), (1024, 16384, 16, 64)])
+@pytest.mark.parametrize("kind", ["skewed", "an eighth", "last", "first", "hostile"])
+def test_grouped_few_rows_on_average(gpu, E, rows, N, K, kind):
+    """The few-row kernel, whose rule knows the average only: experts of many passes of 32 rows beside empty ones.  Every
+    expert of more than 16 rows is compared bit for bit with its dense product in tiles, all rows with FP64."""
+    import torch
+    m, dev = gpu
+    rng = np.random.default_rng(E * 7 + rows)
+    counts = np.zeros(E, np.int64)
+    if kind in ("skewed", "hostile"):
+        p = np.exp(rng.standard_normal(E) * 2)
+        counts = rng.multinomial(rows, p / p.sum())
+    elif kind == "an eighth":
+        counts = rng.multinomial(rows - rows // 8, np.full(E, 1 / E))
+        counts[E // 2] += rows // 8
+    else:
+        counts[-1 if kind == "last" else 0] = rows
+    given = np.concatenate([[0], np.cumsum(counts)])
+    if kind == "hostile":
+        given[1::3] -= rng.integers(0, 2 * rows, len(given[1::3]))
+        given[0] = rng.integers(-5, 5)
+        given[-1] += rng.integers(-3, 1 << 20)
+    o = np.maximum.accumulate(np.clip(given, 0, rows))
+    assert rows <= 16 * E and rows * K <= 32768 * E
+    bits, xb = _bits(rng, (E, N, K), 0.1), _bits(rng, (rows, K))
+    w, wv = _weights(m, dev, bits)
+    x = to_dev(xb, dev)
+    out = torch.full((rows + 2, N), 77, dtype=torch.int16, device=dev)
+    m.mxfp4_grouped_linear(x, to_dev(given.astype(np.int32), dev), w, out=out[1:-1])
+    y = to_host(out[1:-1])
+    assert (out[0] == 77).all() and (out[-1] == 77).all() and (y[:o[0]] == 77).all() and (y[o[-1]:] == 77).all()
+    xv = R.mxfp4_values(*R.mxfp4_quantize(xb, False))
+    for e in np.flatnonzero(np.diff(o)):
+        a, b = o[e], o[e + 1]
+        _check_product(R.bf16_values(y[a:b]), xv[a:b], wv[e])
+        if b - a > 16:
+            one = m.Mxfp4Weights(1, N, K, dev).quantize_from(to_dev(bits[e:e + 1], dev))
+            assert np.array_equal(to_host(m.mxfp4_linear(x[a:b], one)), y[a:b]), e
+
+
+def test_grouped_rows_on_one_expert_cost_no_more(gpu):
+    """2048 rows of 128 experts, evenly and all on one: the second call reads one expert's weights in place of all.  (With
+    one workgroup row an expert it took 23 times as long as the first.)"""
+    import torch
+    m, dev = gpu
+    E, rows, N, K = 128, 2048, 1536, 2048
+    w = m.Mxfp4Weights(E, N, K, dev).quantize_from(torch.randn(E, N, K, device=dev).to(torch.bfloat16))
+    x = torch.randn(rows, K, device=dev).to(torch.bfloat16)
+    ws = m.mxfp4_alloc_workspace(rows, K, E, dev)
+    out = torch.empty(rows, N, dtype=torch.bfloat16, device=dev)
+    even = torch.arange(0, rows + 1, rows // E, dtype=torch.int32, device=dev)
+    one = torch.zeros(E + 1, dtype=torch.int32, device=dev)
+    one[E // 2 + 1:] = rows
+
+    def ms(off):
+        best = float("inf")
+        for _ in range(5):
+            a, b = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+            a.record()
+            for _ in range(10):
+                m.mxfp4_grouped_linear(x, off, w, workspace=ws, out=out)
+            b.record()
+            b.synchronize()
+            best = min(best, a.elapsed_time(b))
+        return best
+
+    assert ms(one) < 3 * ms(even)
