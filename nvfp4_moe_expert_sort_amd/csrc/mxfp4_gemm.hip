@@ -9,8 +9,9 @@
 //   mx_gemm_wide_kernel    tiles of up to 128 rows x 256 or 64 columns:
 //                          activations shared through LDS by direct loads, each
 //                          wave's weights straight from memory into registers
-//   mx_gemm_small_kernel   up to about 32 rows a matrix: 16 columns per wave,
-//                          activations quantized into LDS by the workgroup
+//   mx_gemm_small_kernel   few rows a matrix on average (8, or 16 of one matrix):
+//                          16 columns per wave, up to 32 rows quantized into
+//                          LDS by the workgroup
 #include <type_traits>
 
 #include "mxfp4.h"
@@ -317,15 +318,16 @@ __global__ void __launch_bounds__(256, 2) mx_gemm_wide_kernel(MxGemmParams P) {
         wide_tile<2, NT>(P, T, S);
 }
 
-// Few rows: workgroup (x, y) takes every gridDim.x-th group of 64 columns of
-// matrix y, 16 per wave, and its rows kSmallMT * 16 at a time.  It quantizes the
-// rows itself, into LDS, while its first weights (12 KiB a wave) are on their way:
+// Few rows: workgroup (x, y) takes every gridDim.x-th group of 64 columns, 16 per
+// wave, for pass y of the product: up to kSmallBM rows of one matrix, so that an
+// expert with many rows keeps as many workgroups busy.  It quantizes the rows
+// itself, into LDS, while its first weights (12 KiB a wave) are on their way:
 // no launch, table or round trip through memory comes before them.  Bound by
 // reading the weights: 512 rows over 128 experts of 1536 x 2048 take 36 us for
 // 214 MB (6 TB/s, part of it from the last-level cache; 43 us and 5.0 TB/s from
-// memory); 7 x 4096 x 2048 takes 6.1 us, a launch and one chain of loads.  After
-// the first it streams: each wave keeps a ring of kSmallRing quads of weights in flight
-// across its column groups.
+// memory), 19 us if one expert has them all; 7 x 4096 x 2048 takes 6.1 us, a
+// launch and one chain of loads.  After the first it streams: each wave keeps a
+// ring of kSmallRing quads of weights in flight across its column groups.
 constexpr int kSmallRing = 3, kSmallMT = 2, kSmallBM = 16 * kSmallMT;
 
 namespace {
@@ -497,19 +499,25 @@ __global__ void __launch_bounds__(256, 4) mx_gemm_small_kernel(MxGemmParams P) {
     }
 }
 
-// The small kernel is for up to 16 rows a matrix on average (a rule on what the
-// host knows; a matrix with more takes them kSmallBM at a time) of up to
-// kSmallElements elements together, which each of its workgroups quantizes, in
-// rows that fit LDS.  Against the tile kernel, quantizer included: 8 rows of
-// 4096 for one matrix of 4096 columns 8.8 against 11.0 us, 16 rows of 768 for
-// each of 128 x 2048 columns 22.7 against 25.6, 16 rows of 2048 for each of
-// 128 x 1536 columns 52 against 48 (8 rows: 47 each).
-constexpr int64_t kSmallRows = 16, kSmallElements = 32768;
+// The small kernel is for few rows a matrix on average (a rule on what the host
+// knows), of up to kSmallElements elements together, which each of its
+// workgroups quantizes, in rows that fit LDS.  Against the tile kernel, quantizer
+// included: one matrix, 8 rows of 4096 to 4096 columns 8.8 against 11.0 us.
+// Grouped, rows spread evenly and (in brackets) by a popularity of e^(N(0, 1/4)):
+//   128 x 1536 x 2048,  4 rows  36.7 (35.9) against 38.9 (37.9)
+//                       8 rows  39.4 (41.1) against 40.1 (39.7)
+//                      12 rows  42.2 (47.1) against 40.4 (40.9)
+//   128 x 2048 x 768,   8 rows  22.0 (22.8) against 25.3 (24.8)
+//                      14 rows  23.6 (28.6) against 25.6 (26.5)
+//   60 x 1536 x 2048,   6 rows  20.0 (21.5) against 22.4 (22.4)
+//                      12 rows  21.6 (27.1) against 22.5 (23.1)
+// Routing is uneven, so grouped products take it up to 8 rows.
+constexpr int64_t kSmallRows = 16, kSmallGroupedRows = 8, kSmallElements = 32768;
 constexpr int32_t kSmallCols = 4096;
 constexpr int64_t kSmallBlocks = 1024;  // workgroups of the small kernel
 constexpr int64_t kWideBlocks = 144;    // tiles that make 256 columns worth it
 bool mx_small(int64_t rows, int64_t E, int64_t K) {
-    return rows <= kSmallRows * E && rows * K <= kSmallElements * E && K <= kSmallCols;
+    return rows <= (E > 1 ? kSmallGroupedRows : kSmallRows) * E && rows * K <= kSmallElements * E && K <= kSmallCols;
 }
 
 hipError_t launch_mx_gemm_small(MxGemmParams P, int64_t E, hipStream_t stream) {
