@@ -179,7 +179,6 @@ int mx_product(const uint16_t* x, int64_t M, int64_t ldx, const int32_t* offsets
 
 struct Range {
     uintptr_t lo, hi;
-    int32_t tensor;
     bool write;
 };
 
@@ -362,8 +361,8 @@ int nvfp4moe_grad_plan(const nvfp4moe_grad* grads, int32_t n_grads, void* plan_h
         const nvfp4moe_grad& g = grads[i];
         if (g.n == 0) continue;
         const size_t len = (size_t)g.n * (g.type == NVFP4MOE_BF16 ? 2 : 4);
-        ranges.push_back({(uintptr_t)g.out, (uintptr_t)g.out + len, i, true});
-        if (g.in != g.out) ranges.push_back({(uintptr_t)g.in, (uintptr_t)g.in + len, i, false});
+        ranges.push_back({(uintptr_t)g.out, (uintptr_t)g.out + len, true});
+        if (g.in != g.out) ranges.push_back({(uintptr_t)g.in, (uintptr_t)g.in + len, false});
     }
     std::sort(ranges.begin(), ranges.end(), [](const Range& a, const Range& b) { return a.lo < b.lo; });
     uintptr_t end_any = 0, end_write = 0;
