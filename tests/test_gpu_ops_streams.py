@@ -16,7 +16,7 @@ def gpu():
 
 
 def _calls(m, dev):
-    """{name: (inputs, call of them on a stream)}"""
+    """{name: (inputs, what makes of them a call on a stream)}"""
     import torch
     g = torch.Generator(device=dev).manual_seed(1)
 
@@ -37,19 +37,23 @@ def _calls(m, dev):
 
     W1, W2 = m.Mxfp4Weights(1, 512, 512, dev).quantize_from(w[:1]), m.Mxfp4Weights(2, 512, 512, dev).quantize_from(w)
     ws = m.mxfp4_alloc_workspace(4096, 512, 2, dev)
+    def clip(g):  # (the set is made before the call: its plan's copy makes the host wait)
+        grads = m.GradSet([g])
+        return lambda s: m.clip_grad_norm(grads, 1.0, stream=s)
+
     return {
-        "router_logits": ((x, wr), lambda s, x, wr: m.router_logits(x, wr, stream=s)),
-        "router_select": ((logits, bias), lambda s, l, b: m.router_select(l, 8, bias=b, stream=s)),
-        "router_select_backward": ((logits, ids, dp), lambda s, l, i, d: m.router_select_backward(l, i, d, stream=s)),
-        "mxfp4_quantize": ((x,), lambda s, x: m.mxfp4_quantize(x, stream=s)),
-        "mxfp4_dequantize": ((codes, scales), lambda s, c, sc: m.mxfp4_dequantize(c, sc, stream=s)),
-        "quantize_from": ((w,), lambda s, w: m.Mxfp4Weights(2, 512, 512, dev).quantize_from(w, stream=s).codes),
-        "dequantize": ((W2.codes, W2.scales), lambda s, c, sc: weights(c, sc, 2).dequantize(stream=s)),
-        "mxfp4_linear": ((x, W1.codes, W1.scales, ws),
-                         lambda s, x, c, sc, ws: m.mxfp4_linear(x, weights(c, sc, 1), workspace=ws, stream=s)),
-        "mxfp4_grouped_linear": ((x, off, W2.codes, W2.scales),
-                                 lambda s, x, o, c, sc: m.mxfp4_grouped_linear(x, o, weights(c, sc, 2), stream=s)),
-        "clip_grad_norm": ((logits,), lambda s, g: m.clip_grad_norm(m.GradSet([g]), 1.0, stream=s)),
+        "router_logits": ((x, wr), lambda x, wr: lambda s: m.router_logits(x, wr, stream=s)),
+        "router_select": ((logits, bias), lambda l, b: lambda s: m.router_select(l, 8, bias=b, stream=s)),
+        "router_select_backward": ((logits, ids, dp), lambda l, i, d: lambda s: m.router_select_backward(l, i, d, stream=s)),
+        "mxfp4_quantize": ((x,), lambda x: lambda s: m.mxfp4_quantize(x, stream=s)),
+        "mxfp4_dequantize": ((codes, scales), lambda c, sc: lambda s: m.mxfp4_dequantize(c, sc, stream=s)),
+        "quantize_from": ((w,), lambda w: lambda s: m.Mxfp4Weights(2, 512, 512, dev).quantize_from(w, stream=s).codes),
+        "dequantize": ((W2.codes, W2.scales), lambda c, sc: lambda s: weights(c, sc, 2).dequantize(stream=s)),
+        "mxfp4_linear": ((x, W1.codes, W1.scales, ws), lambda x, c, sc, ws: lambda s: m.mxfp4_linear(
+            x, weights(c, sc, 1), workspace=ws, stream=s)),
+        "mxfp4_grouped_linear": ((x, off, W2.codes, W2.scales), lambda x, o, c, sc: lambda s: m.mxfp4_grouped_linear(
+            x, o, weights(c, sc, 2), stream=s)),
+        "clip_grad_norm": ((logits,), clip),
     }
 
 
@@ -59,20 +63,25 @@ def _calls(m, dev):
 def test_memory_of_dropped_tensors_waits_for_the_stream(gpu, name):
     import torch
     m, dev = gpu
-    inputs, call = _calls(m, dev)[name]
-    want = call(None, *[t.clone() for t in inputs])
+    inputs, make = _calls(m, dev)[name]
+    want = make(*[t.clone() for t in inputs])(None)
     side = torch.cuda.Stream(dev)
+    sizes = [t.numel() * t.element_size() for t in inputs]
+    # What is allocated below comes from the caches: an allocation of the driver's may wait for the GPU.
+    make(*[t.clone() for t in inputs])(side)
+    warm = [torch.empty(n, dtype=torch.uint8, device=dev) for n in sizes for _ in range(4)]
+    torch.cuda.synchronize()
     mine = [t.clone() for t in inputs]
+    call = make(*mine)
     torch.cuda.synchronize()
     with torch.cuda.stream(side):
-        torch.cuda._sleep(400_000_000)  # some tenths of a second of the clock
-    got = call(side, *mine)
-    assert not side.query()  # the call's work still waits
+        torch.cuda._sleep(1_000_000_000)  # about half a second
+    got = call(side)
     taken = {t.data_ptr() for t in mine}
-    sizes = [t.numel() * t.element_size() for t in mine]
-    mine = None
+    mine = call = warm = None
     new = [torch.empty(n, dtype=torch.uint8, device=dev) for n in sizes for _ in range(3)]
-    assert not side.query() and not taken & {t.data_ptr() for t in new}
+    assert not side.query()  # the call's work still waits, and its memory with it
+    assert not taken & {t.data_ptr() for t in new}
     side.synchronize()
     for a, b in zip(got if isinstance(got, tuple) else (got,), want if isinstance(want, tuple) else (want,)):
         assert torch.equal(a, b)
