@@ -416,9 +416,10 @@ typedef struct {
  *   - probs: scale * s (renormalize 0), or scale * s / (sum of s over the
  *     token's available selected experts), computed so that the sum does not
  *     vanish however negative the logits are.
- * s and v are formed in FP64, so the choice does not depend on FP32 rounding;
- * with a bias (or TOP2) values closer than about 2^-40 relative may count as
- * equal.
+ * s and v are formed in FP64, so the choice does not depend on FP32 rounding.
+ * With a bias (or TOP2) values that differ by less than about 2^-40 of the
+ * scores and biases they are made of may count as equal or change places, and a
+ * score below FP64's normal range may count as 0.
  *   ids [T, K] int32, probs [T, K] FP32: caller-owned outputs, which may not
  *   overlap the inputs
  * Requirements: T < 2^31 (more than some 2^26 tokens take several launches);
@@ -485,7 +486,8 @@ typedef struct {
 NVFP4MOE_API int nvfp4moe_mxfp4_bytes(const nvfp4moe_mxfp4_tensor* q, size_t* codes_bytes, size_t* scales_bytes);
 
 /* x [n_mats*rows, cols] BF16 (rows ld elements apart) -> q's planes, and back
- * (exactly: every MXFP4 value is a BF16 number; out's rows are ld apart).
+ * (exactly, as far as BF16 reaches: values of 2^128 and more, which RU makes of
+ * the largest magnitudes, become infinite; out's rows are ld apart).
  * Requirements: x / out 16-byte aligned, ld >= cols and a multiple of 8, codes
  * 16-byte aligned (scales 4-byte in the GEMM layout), n_mats*rows*cols < 2^34.
  * Zero rows or matrices are a no-op; outputs may not overlap inputs.  No
@@ -499,7 +501,7 @@ NVFP4MOE_API int nvfp4moe_mxfp4_dequantize(const nvfp4moe_mxfp4_tensor* q, uint1
  * matrix [N, K] and FP32 accumulation.  M >= 0, K % 32 == 0, K < 2^24, any N
  * (fewer than 2^24 tiles of 128 rows x 256 columns).
  * Requirements: x 16-byte aligned, ldx >= K and a multiple of 8; out aligned to
- * 2 bytes, ld_out >= N (8-byte stores where out, ld_out and N allow them); no
+ * 2 bytes, ld_out >= N (stores of up to 16 bytes where out, ld_out and N allow); no
  * element of out shares memory with x, Wq or the workspace (x is still read
  * while out is written);
  * workspace 256-byte aligned, nvfp4moe_mxfp4_workspace_bytes(M, K, 1) bytes.
@@ -534,7 +536,7 @@ NVFP4MOE_API int nvfp4moe_mxfp4_grouped_linear(const uint16_t* x, int64_t R, int
  * The tensors are given once, as a plan: nvfp4moe_grad_plan writes a table of
  * n_chunks entries for n_grads tensors (host array) into host memory, which
  * the caller copies to the device and may use as long as the tensors stay
- * where they are.  in and out of a tensor are the same address (in place) or
+ * where they are; tensors that were allocated anew need a new one.  in and out of a tensor are the same address (in place) or
  * disjoint; no output may overlap another tensor (NVFP4_E_ARG).  Tensors of 0
  * elements are allowed.  Each is contiguous and aligned to its element. */
 typedef struct {

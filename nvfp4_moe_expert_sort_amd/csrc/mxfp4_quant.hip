@@ -12,7 +12,7 @@
 //                          the products with the row-tile table beside them
 //   mx_quant_tiles_kernel  the weights' tile layout: a wave takes 16 rows x 512
 //                          columns and stores whole 1 KiB tiles
-//   mx_dequant_kernel      either layout back to BF16 (exact)
+//   mx_dequant_kernel      either layout back to BF16 (exact below 2^128)
 #include "mxfp4.h"
 #include "nvfp4_kernels.h"
 

@@ -15,7 +15,8 @@
 // bits (complemented for v >= 0, so that the lower id is the larger key).
 // Without a bias v is an FP32 number whose low 29 bits are zero, and the
 // order is exact; with one, values are told apart down to about 2^-41 relative
-// (42 bits of key, scores within 2^-45).
+// (42 bits of key), and where s and b cancel down to the 2^-45 of s that the
+// scores are within.
 //
 // LT lanes (16, or 64 for more than 256 experts or 16 slots) share a token, so
 // a wavefront takes 4 tokens or one, each lane NV experts.  The lane sorts its
@@ -491,8 +492,8 @@ __global__ void __launch_bounds__(kSelWaves * 64, 4) router_select_kernel(Select
 // softmax's terms too: dp_k - sum_j dp_j w_j is a small difference where one
 // expert has nearly all the weight.  Each value is rounded to FP32 once, and a
 // BF16 one from there (half a step of BF16 and 2^-24 more).  T = 4096, E = 256, FP32, renormalised: 4.4 us for 4.3 MB (a launch and
-// one chain of loads); T = 32749, E = 128, BF16, softmax over all: 7.2 us for
-// 18.9 MB, of which the copy rate allows 3.6.
+// one chain of loads); T = 32749, E = 128, BF16, softmax over all: 9.0 us for
+// 18.9 MB, of which the copy rate allows 3.6 (with FP32 terms 7.2).
 template <int LT, int NV, typename L>
 __global__ void __launch_bounds__(kSelWaves * 64) router_select_backward_kernel(SelectParams P) {
     constexpr int kTok = kWave / LT;

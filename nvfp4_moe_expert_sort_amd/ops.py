@@ -275,7 +275,9 @@ def mxfp4_grouped_linear(x, offsets, W: Mxfp4Weights, scale_round: int = MXFP4_S
 
 class GradSet:
     """The tensors that clip_grad_norm works on: FP32 or BF16, contiguous, on one GPU.  `out` (default: in place)
-    receives the clipped ones.  Holds the tensors and their plan on the GPU; make a new one if they move."""
+    receives the clipped ones.  Holds the tensors and their plan on the GPU; make a new one if they move.  Making one
+    copies the plan to the GPU and waits for the copy: once, before the steps, for gradients that stay where they are,
+    and outside a graph's capture."""
 
     def __init__(self, grads, out=None):
         self.grads = list(grads)
