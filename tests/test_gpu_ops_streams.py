@@ -109,3 +109,18 @@ def test_a_named_stream_under_capture(gpu):
         assert torch.equal(ids, a) and torch.equal(probs, b) and torch.equal(y, m.mxfp4_linear(x, w))
     del g, l, x, w, ids, probs, y
     assert float(torch.ones(1 << 20, device=dev).sum()) == 1 << 20
+
+
+def test_empty_tensors_on_a_named_stream(gpu):
+    import torch
+    m, dev = gpu
+    side = torch.cuda.Stream(dev)
+    l, x = torch.empty(0, 16, device=dev), torch.empty(0, 64, dtype=torch.bfloat16, device=dev)
+    ids, probs = m.router_select(l, 4, stream=side)
+    assert m.router_select_backward(l, ids, probs, stream=side).shape == (0, 16)
+    w = m.Mxfp4Weights(1, 40, 64, dev).quantize_from(torch.zeros(1, 40, 64, dtype=torch.bfloat16, device=dev))
+    assert m.mxfp4_linear(x, w, stream=side).shape == (0, 40)
+    assert m.mxfp4_dequantize(*m.mxfp4_quantize(x, stream=side), stream=side).shape == (0, 64)
+    norm = m.clip_grad_norm(m.GradSet([torch.empty(0, device=dev)]), 1.0, stream=side)
+    side.synchronize()
+    assert float(norm) == 0.0
