@@ -449,6 +449,64 @@ NVFP4MOE_API int nvfp4moe_router_select_backward(const nvfp4moe_select_config* c
                                                  const float* bias, const int32_t* ids, const float* dprobs, void* dlogits,
                                                  int64_t ld_out, void* stream);
 
+/* The balance loss of a router, and how many tokens each expert got: what
+ * keeps the selection above from collapsing onto few experts in training (the
+ * counts are also what its bias is updated from).
+ * The rows form S sequences: sequence s holds rows [seq_offsets[s],
+ * seq_offsets[s+1]) (device int32 [S+1], not decreasing), or, where
+ * seq_offsets is NULL, S is 1 and the one sequence holds all T rows.  Rows
+ * before the first offset and from the last one on belong to none.  With T_s
+ * rows in sequence s and T' in all of them:
+ *   counts_se = slots (t in s, k) with ids_tk == e (ids outside [0, E) count
+ *     nowhere)
+ *   f_se = E counts_se / (K T_s): 1 where the load is even
+ *   p_te = softmax over the row's usable logits, or sigmoid(l_te) divided by
+ *     their sum over the row; usable as in nvfp4moe_router_select, 0 where not
+ *     and in a row that is masked whole
+ *   loss = coef / T' sum_s sum_{t in s} sum_e f_se p_te
+ * which is coef where load or probabilities are even.  A sequence without rows
+ * adds nothing. */
+typedef struct {
+    int32_t n_experts;   /* E: 1..1024 */
+    int32_t top_k;       /* K: slots per token, 1..32 */
+    int32_t score;       /* NVFP4MOE_SCORE_* */
+    int32_t logits_type; /* NVFP4MOE_F32 or NVFP4MOE_BF16 */
+    float coef;          /* finite */
+} nvfp4moe_balance_config;
+
+/* logits [T, E] (rows ld elements apart), ids [T, K] int32 -> loss (device
+ * float), counts [S, E] int32, every element written.  The probabilities are
+ * summed in FP32 over at most 256 tokens and in FP64 from there, in one order:
+ * the same bits in every run.
+ * Requirements: 0 <= T < 2^31, 1 <= S <= 65536, ld >= E; logits aligned to
+ * their element, the others to 4 bytes; workspace 256-byte aligned,
+ * nvfp4moe_balance_workspace_bytes(T, E, S) bytes (0 for sizes out of range),
+ * not shared by calls that may run at the same time.  Offsets outside [0, T]
+ * are taken as the nearer end; with decreasing ones the results are undefined
+ * (no access leaves the buffers).  Outputs may not overlap inputs.  No
+ * synchronisation. */
+NVFP4MOE_API size_t nvfp4moe_balance_workspace_bytes(int64_t T, int32_t n_experts, int32_t n_sequences);
+NVFP4MOE_API int nvfp4moe_router_balance_loss(const nvfp4moe_balance_config* cfg, const void* logits, int64_t ld, int64_t T,
+                                              const int32_t* ids, const int32_t* seq_offsets, int32_t n_sequences,
+                                              float* loss, int32_t* counts, void* workspace, size_t workspace_bytes,
+                                              void* stream);
+
+/* Its gradient with respect to the logits, the counts taken as constants:
+ *   dlogits_te = add_te + dloss coef / T' p_te (f_se - sum_j f_sj p_tj) [x (1 - sigmoid(l_te))]
+ * with cfg, logits and sequences the forward's, counts its output, dloss the
+ * gradient of the loss (device float; NULL: 1) and add [T, E] of the logits'
+ * type (rows ld_add apart) or NULL for 0: nvfp4moe_router_select_backward's
+ * dlogits, so that one pass gives the router's whole gradient.  Every element
+ * of dlogits (logits' type, rows ld_out apart) is written, rows of no sequence
+ * and unusable logits with add alone.  Formed in FP64 from FP32 exponentials
+ * and rounded at the end (a BF16 value by way of FP32).
+ * dlogits may be add (the same address and stride, else NVFP4_E_ARG) and may
+ * not overlap anything else.  Requirements as for the loss; no workspace. */
+NVFP4MOE_API int nvfp4moe_router_balance_backward(const nvfp4moe_balance_config* cfg, const void* logits, int64_t ld,
+                                                  int64_t T, const int32_t* counts, const int32_t* seq_offsets,
+                                                  int32_t n_sequences, const float* dloss, const void* add,
+                                                  int64_t ld_add, void* dlogits, int64_t ld_out, void* stream);
+
 /* MXFP4, the OCP microscaled 4-bit format: E2M1 elements with one E8M0 (power
  * of two) scale per block of 32 along the row and no outer scale.  Its
  * products run on the scaled FP4 matrix instruction, which takes these
@@ -523,6 +581,60 @@ NVFP4MOE_API int nvfp4moe_mxfp4_linear(const uint16_t* x, int64_t M, int64_t ldx
 NVFP4MOE_API int nvfp4moe_mxfp4_grouped_linear(const uint16_t* x, int64_t R, int64_t ldx, const int32_t* offsets,
                                                const nvfp4moe_mxfp4_tensor* Wq, uint16_t* out, int64_t ld_out,
                                                int32_t scale_round, void* workspace, size_t workspace_bytes, void* stream);
+
+/* Low-rank adapters of many requests beside a shared projection (host struct,
+ * device pointers): what is served per request, or trained, on top of weights
+ * that stay quantized.  Adapter a is A[a] [rank, in_features] and B[a]
+ * [out_features, rank], both BF16 and contiguous, and the factor scale[a]
+ * (FP32 [n], or NULL for 1).  Adapters of a lower rank are padded with zeros.
+ * n 1..1024; rank 8..128, in_features and out_features 8..2^24 - 1, all three
+ * multiples of 8; A and B 16-byte aligned. */
+typedef struct {
+    const uint16_t* A;
+    const uint16_t* B;
+    const float* scale;
+    int32_t n;
+    int32_t rank;
+    int32_t in_features;
+    int32_t out_features;
+} nvfp4moe_adapters;
+
+/* For each of M rows, with a = ids[r] (device int32 [M], in any order: the
+ * request's adapter, or for an expert's projection the row's expert):
+ *   v_r   = A[a] x_r
+ *   out_r = bf16(base_r + scale[a] B[a] v_r)
+ * with base the shared projection's output (nvfp4moe_mxfp4_linear's, say) or
+ * NULL for 0.  Rows whose id lies outside [0, n) have no adapter: out_r is
+ * base_r to the bit (or 0), v_r is 0.  Sums are FP32, rounded once at the end;
+ * v enters the second product as two BF16 values (within 2^-16 of it).  A
+ * row's bits depend on that row alone: not on the batch, nor on its place in it.
+ * x [M, in_features], base and out [M, out_features] BF16, rows ldx, ld_base
+ * and ld_out apart (multiples of 8, pointers 16-byte aligned); out may be base
+ * (in place, the same stride, else NVFP4_E_ARG) and may not overlap anything else.  v (FP32
+ * [M, rank], 16-byte aligned, may be NULL) is what the gradients need of the
+ * forward pass.  M < 2^26; M == 0 is a no-op.
+ * Workspace: nvfp4moe_adapter_workspace_bytes(ad, M, backward) bytes (0 for
+ * sizes out of range; ad's pointers are not read), 256-byte aligned, not shared
+ * by calls that may run at the same time.  No synchronisation. */
+NVFP4MOE_API size_t nvfp4moe_adapter_workspace_bytes(const nvfp4moe_adapters* ad, int64_t M, int32_t backward);
+NVFP4MOE_API int nvfp4moe_adapter_linear(const nvfp4moe_adapters* ad, const uint16_t* x, int64_t M, int64_t ldx,
+                                         const int32_t* ids, const uint16_t* base, int64_t ld_base, uint16_t* out,
+                                         int64_t ld_out, float* v, void* workspace, size_t workspace_bytes, void* stream);
+
+/* The gradients, from dy [M, out_features] BF16 (of out) and the forward's v:
+ *   dx_r  = bf16(base_r + A[a]^T w_r),  w_r = scale[a] B[a]^T dy_r
+ *   dA[a] = sum over its rows of w_r x_r^T               (FP32 [n, rank, in_features])
+ *   dB[a] = scale[a] sum over its rows of dy_r v_r^T     (FP32 [n, out_features, rank])
+ * with base [M, in_features] BF16 the gradient through the shared projection,
+ * or NULL for 0 (rows without an adapter: dx_r is base_r or 0).  Every element
+ * of dA and dB is written, those of adapters without rows with zeros; the same
+ * inputs give the same bits in every run.  w and v enter the sums in full (three
+ * BF16 values each).  dx may be base (the same stride); outputs may not overlap
+ * anything else.  dA and dB 16-byte aligned, the rest as for the forward. */
+NVFP4MOE_API int nvfp4moe_adapter_backward(const nvfp4moe_adapters* ad, const uint16_t* x, int64_t M, int64_t ldx,
+                                           const int32_t* ids, const float* v, const uint16_t* dy, int64_t ld_dy,
+                                           const uint16_t* base, int64_t ld_base, uint16_t* dx, int64_t ld_dx, float* dA,
+                                           float* dB, void* workspace, size_t workspace_bytes, void* stream);
 
 /* Clipping of gradients by their global norm, the end of a training step whose
  * weight gradients nvfp4moe_moe_expert_backward gives.

@@ -43,7 +43,9 @@ EXPORTS = ["nvfp4_status_str", "nvfp4_quantize", "nvfp4moe_weight_bytes", "nvfp4
            "nvfp4moe_router_select_backward", "nvfp4moe_mxfp4_bytes", "nvfp4moe_mxfp4_quantize",
            "nvfp4moe_mxfp4_dequantize", "nvfp4moe_mxfp4_workspace_bytes", "nvfp4moe_mxfp4_linear",
            "nvfp4moe_mxfp4_grouped_linear", "nvfp4moe_grad_plan_bytes", "nvfp4moe_grad_plan",
-           "nvfp4moe_clip_workspace_bytes", "nvfp4moe_clip_grad_norm"]
+           "nvfp4moe_clip_workspace_bytes", "nvfp4moe_clip_grad_norm", "nvfp4moe_balance_workspace_bytes",
+           "nvfp4moe_router_balance_loss", "nvfp4moe_router_balance_backward", "nvfp4moe_adapter_workspace_bytes",
+           "nvfp4moe_adapter_linear", "nvfp4moe_adapter_backward"]
 
 
 class Nvfp4Error(RuntimeError):
@@ -76,6 +78,16 @@ class SelectConfig(ctypes.Structure):
                 ("top_groups", ctypes.c_int32), ("group_score", ctypes.c_int32), ("logits_type", ctypes.c_int32)]
 
 
+class BalanceConfig(ctypes.Structure):
+    _fields_ = [("n_experts", ctypes.c_int32), ("top_k", ctypes.c_int32), ("score", ctypes.c_int32),
+                ("logits_type", ctypes.c_int32), ("coef", ctypes.c_float)]
+
+
+class Adapters(ctypes.Structure):
+    _fields_ = [("A", ctypes.c_void_p), ("B", ctypes.c_void_p), ("scale", ctypes.c_void_p), ("n", ctypes.c_int32),
+                ("rank", ctypes.c_int32), ("in_features", ctypes.c_int32), ("out_features", ctypes.c_int32)]
+
+
 class Mxfp4Tensor(ctypes.Structure):
     _fields_ = [("codes", ctypes.c_void_p), ("scales", ctypes.c_void_p), ("n_mats", ctypes.c_int32),
                 ("rows", ctypes.c_int32), ("cols", ctypes.c_int32), ("layout", ctypes.c_int32)]
@@ -99,6 +111,7 @@ def lib():
     vp, i32, i64, sz = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_size_t
     cfgp, qtp = ctypes.POINTER(Config), ctypes.POINTER(QTensor)
     selp, mxp, gradp = ctypes.POINTER(SelectConfig), ctypes.POINTER(Mxfp4Tensor), ctypes.POINTER(Grad)
+    balp, adp = ctypes.POINTER(BalanceConfig), ctypes.POINTER(Adapters)
     szp, i64p = ctypes.POINTER(sz), ctypes.POINTER(i64)
     sig = {
         "nvfp4_status_str": (ctypes.c_char_p, [ctypes.c_int]),
@@ -136,6 +149,13 @@ def lib():
         "nvfp4moe_mxfp4_workspace_bytes": (sz, [i64, i64, i64]),
         "nvfp4moe_mxfp4_linear": (ctypes.c_int, [vp, i64, i64, mxp, vp, i64, i32, vp, sz, vp]),
         "nvfp4moe_mxfp4_grouped_linear": (ctypes.c_int, [vp, i64, i64, vp, mxp, vp, i64, i32, vp, sz, vp]),
+        "nvfp4moe_balance_workspace_bytes": (sz, [i64, i32, i32]),
+        "nvfp4moe_router_balance_loss": (ctypes.c_int, [balp, vp, i64, i64, vp, vp, i32, vp, vp, vp, sz, vp]),
+        "nvfp4moe_router_balance_backward": (ctypes.c_int, [balp, vp, i64, i64, vp, vp, i32, vp, vp, i64, vp, i64, vp]),
+        "nvfp4moe_adapter_workspace_bytes": (sz, [adp, i64, i32]),
+        "nvfp4moe_adapter_linear": (ctypes.c_int, [adp, vp, i64, i64, vp, vp, i64, vp, i64, vp, vp, sz, vp]),
+        "nvfp4moe_adapter_backward": (ctypes.c_int, [adp, vp, i64, i64, vp, vp, vp, i64, vp, i64, vp, i64, vp, vp, vp, sz,
+                                                     vp]),
         "nvfp4moe_grad_plan_bytes": (ctypes.c_int, [gradp, i32, szp, i64p]),
         "nvfp4moe_grad_plan": (ctypes.c_int, [gradp, i32, vp, sz]),
         "nvfp4moe_clip_workspace_bytes": (sz, []),
@@ -438,11 +458,12 @@ def selftest_batch_invariance(cfg: Config, weights: QuantWeights, seed: int, n_p
     return st, dict(n_compared=rep[0], n_mismatched=rep[1], first_bad_probe=rep[2], first_bad_batch=rep[3])
 
 
-# --- expert selection, MXFP4 products, gradient clipping: ops.py, loaded (with torch) on first use -----
+# --- expert selection, balance loss, MXFP4 products, adapters, gradient clipping: ops.py, loaded (with torch) on first use -----
 
 _OPS = ("router_logits", "router_select", "router_select_backward", "mxfp4_quantize", "mxfp4_dequantize", "Mxfp4Weights",
         "mxfp4_workspace_bytes", "mxfp4_alloc_workspace", "mxfp4_linear", "mxfp4_grouped_linear", "GradSet",
-        "clip_grad_norm")
+        "clip_grad_norm", "router_balance_loss", "router_balance_backward", "adapter_workspace_bytes",
+        "adapter_alloc_workspace", "adapter_linear", "adapter_backward")
 
 
 def __getattr__(name):

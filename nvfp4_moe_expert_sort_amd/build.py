@@ -10,7 +10,7 @@ CSRC = os.path.join(HERE, "csrc")
 BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "lib", "libnvfp4moe.so")
 SOURCES = ["quant.hip", "route.hip", "gemm.hip", "gemm_w4a16.hip", "producer.hip", "backward.hip", "combine.hip",
-           "router.hip", "select.hip", "mxfp4_quant.hip", "mxfp4_gemm.hip", "grad_clip.hip", "api.hip", "api_ops.hip",
+           "router.hip", "select.hip", "balance.hip", "mxfp4_quant.hip", "mxfp4_gemm.hip", "adapter.hip", "grad_clip.hip", "api.hip", "api_ops.hip",
            "selftest.hip"]
 
 # -ffp-contract=off and no fast-math: the quantizer's binary32 divisions and

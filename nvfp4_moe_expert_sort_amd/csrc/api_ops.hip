@@ -1,6 +1,7 @@
 // api_ops.hip -- host side of the entry points beside the expert forward:
-// router logits, expert selection and its gradient, the MXFP4 quantizer and
-// products, and gradient clipping.  Argument checks (before any launch),
+// router logits, expert selection and its gradient, the balance loss and its
+// gradient, the MXFP4 quantizer and products, low-rank adapters and their
+// gradients, and gradient clipping.  Argument checks (before any launch),
 // workspace carving and launches; include/nvfp4moe.h documents each.
 #include <hip/hip_runtime.h>
 
@@ -54,6 +55,44 @@ int select_params(const nvfp4moe_select_config* c, const void* logits, int64_t l
     P->top_groups = c->top_groups;
     P->group_magic = ((1u << 22) + (uint32_t)size - 1) / (uint32_t)size;
     return NVFP4_OK;
+}
+
+int balance_params(const nvfp4moe_balance_config* c, const void* logits, int64_t ld, int64_t T, const int32_t* offsets,
+                   int32_t S, BalanceParams* P) {
+    if (!c) return NVFP4_E_NULL;
+    if (c->score != NVFP4MOE_SCORE_SOFTMAX && c->score != NVFP4MOE_SCORE_SIGMOID) return NVFP4_E_ARG;
+    if (c->logits_type != NVFP4MOE_F32 && c->logits_type != NVFP4MOE_BF16) return NVFP4_E_ARG;
+    if (!std::isfinite(c->coef)) return NVFP4_E_ARG;
+    if (c->n_experts < 1 || c->n_experts > kMaxExperts || c->top_k < 1 || c->top_k > kMaxTopK) return NVFP4_E_SHAPE;
+    if (S < 1 || S > kMaxSequences || (!offsets && S != 1)) return NVFP4_E_SHAPE;
+    if (T < 0 || T >= ((int64_t)1 << 31) || ld < c->n_experts) return NVFP4_E_SHAPE;
+    const size_t elem = c->logits_type == NVFP4MOE_BF16 ? 2 : 4;
+    if (!aligned(logits, elem) || !aligned(offsets, 4)) return NVFP4_E_ALIGN;
+    *P = BalanceParams{};
+    P->logits = logits;
+    P->ld = ld;
+    P->T = T;
+    P->E = c->n_experts;
+    P->K = c->top_k;
+    P->S = S;
+    P->offsets = offsets;
+    P->coef = c->coef;
+    P->sigmoid = c->score == NVFP4MOE_SCORE_SIGMOID;
+    P->vec = ld % 4 == 0 && aligned(logits, 4 * elem);
+    return NVFP4_OK;
+}
+// Workspace of the loss: the chunks' sums and counts, the shares of the loss, a counter.
+struct BalanceWork {
+    size_t csum, part, done, total;
+};
+bool balance_work(int64_t T, int64_t E, int64_t S, BalanceWork* w) {
+    if (T < 0 || T >= ((int64_t)1 << 31) || E < 1 || E > kMaxExperts || S < 1 || S > kMaxSequences) return false;
+    const int64_t chunk = balance_chunk(T), slots = (T + chunk - 1) / chunk + S;
+    w->csum = up(slots * E * 4, kAlign);
+    w->part = 2 * w->csum;
+    w->done = w->part + up(S * ((E + 63) / 64) * 8, kAlign);
+    w->total = w->done + kAlign;
+    return true;
 }
 
 struct MxShape {
@@ -177,6 +216,53 @@ int mx_product(const uint16_t* x, int64_t M, int64_t ldx, const int32_t* offsets
     return hip_status(launch_mx_gemm(p, tiles, s));
 }
 
+// Sizes and pointers of a set of adapters.
+int adapter_shape(const nvfp4moe_adapters* ad, int64_t M) {
+    if (!ad) return NVFP4_E_NULL;
+    if (ad->n < 1 || ad->n > kMaxExperts || ad->rank < 8 || ad->rank > kMaxRank || ad->rank % 8 != 0) return NVFP4_E_SHAPE;
+    for (const int32_t w : {ad->in_features, ad->out_features})
+        if (w < 8 || w % 8 != 0 || w >= (1 << 24)) return NVFP4_E_SHAPE;
+    if (M < 0 || M >= ((int64_t)1 << 26)) return NVFP4_E_SHAPE;
+    return NVFP4_OK;
+}
+int adapter_planes(const nvfp4moe_adapters* ad) {
+    if (!ad->A || !ad->B) return NVFP4_E_NULL;
+    if (!aligned(ad->A, 16) || !aligned(ad->B, 16) || !aligned(ad->scale, 4)) return NVFP4_E_ALIGN;
+    return NVFP4_OK;
+}
+// Workspace: the plan (rows by adapter, its tables) and, for the gradients, the
+// transposed adapters, w and partial sums.
+struct AdapterWork {
+    size_t order, tiles, chunks, info, at, bt, w, slots, total;
+    int64_t n_tiles, n_chunks;
+    int32_t chunk;
+};
+AdapterWork adapter_work(const nvfp4moe_adapters* ad, int64_t M, bool backward) {
+    AdapterWork w{};
+    const int64_t n = ad->n, R = ad->rank, K = ad->in_features, N = ad->out_features, tile = adapter_tile(ad->rank);
+    w.n_tiles = M / tile + std::min(M, n + 1);
+    w.order = kAlign;
+    w.tiles = w.order + up(M * 4, kAlign);
+    w.total = w.tiles + up(w.n_tiles * 16, kAlign);
+    if (!backward) return w;
+    w.chunk = adapter_chunk(M, K, N);
+    w.n_chunks = M / w.chunk + std::min(M, n);
+    w.chunks = w.total;
+    w.info = w.chunks + up(w.n_chunks * 16, kAlign);
+    w.at = w.info + up(n * 8, kAlign);
+    w.bt = w.at + up(n * R * K * 2, kAlign);
+    w.w = w.bt + up(n * R * N * 2, kAlign);
+    w.slots = w.w + up(M * R * 4, kAlign);
+    // chunks of adapters that have more than one: each such adapter has more
+    // than `chunk` rows, so at most twice its rows / chunk of them
+    w.total = w.slots + up((2 * M / w.chunk) * R * (K + N) * 4, kAlign);
+    return w;
+}
+int adapter_rows(const uint16_t* p, int64_t ld, int64_t cols) {
+    if (ld < cols) return NVFP4_E_SHAPE;
+    return aligned(p, 16) && ld % 8 == 0 ? NVFP4_OK : NVFP4_E_ALIGN;
+}
+
 struct Range {
     uintptr_t lo, hi;
     bool write;
@@ -249,6 +335,59 @@ int nvfp4moe_router_select_backward(const nvfp4moe_select_config* cfg, const voi
     P.ld_out = ld_out;
     P.vec_out = ld_out % 4 == 0 && aligned(dlogits, 4 * elem);
     return hip_status(launch_router_select_backward(P, cfg->logits_type == NVFP4MOE_BF16, (hipStream_t)stream));
+}
+
+size_t nvfp4moe_balance_workspace_bytes(int64_t T, int32_t n_experts, int32_t n_sequences) {
+    BalanceWork w;
+    return balance_work(T, n_experts, n_sequences, &w) ? w.total : 0;
+}
+
+int nvfp4moe_router_balance_loss(const nvfp4moe_balance_config* cfg, const void* logits, int64_t ld, int64_t T,
+                                 const int32_t* ids, const int32_t* seq_offsets, int32_t n_sequences, float* loss,
+                                 int32_t* counts, void* workspace, size_t workspace_bytes, void* stream) {
+    BalanceParams P;
+    const int st = balance_params(cfg, logits, ld, T, seq_offsets, n_sequences, &P);
+    if (st != NVFP4_OK) return st;
+    BalanceWork w;
+    if (!balance_work(T, P.E, P.S, &w)) return NVFP4_E_SHAPE;
+    if (!loss || !counts || !workspace || (T > 0 && (!logits || !ids))) return NVFP4_E_NULL;
+    if (workspace_bytes < w.total) return NVFP4_E_WORKSPACE;
+    if (!aligned(ids, 4) || !aligned(loss, 4) || !aligned(counts, 4) || !aligned(workspace, kAlign)) return NVFP4_E_ALIGN;
+    uint8_t* ws = (uint8_t*)workspace;
+    P.ids = ids;
+    P.chunk = balance_chunk(T);
+    P.psum = (float*)ws;
+    P.csum = (int32_t*)(ws + w.csum);
+    P.part = (double*)(ws + w.part);
+    P.done = (uint32_t*)(ws + w.done);
+    P.loss = loss;
+    P.counts = counts;
+    return hip_status(launch_balance(P, cfg->logits_type == NVFP4MOE_BF16, (hipStream_t)stream));
+}
+
+int nvfp4moe_router_balance_backward(const nvfp4moe_balance_config* cfg, const void* logits, int64_t ld, int64_t T,
+                                     const int32_t* counts, const int32_t* seq_offsets, int32_t n_sequences,
+                                     const float* dloss, const void* add, int64_t ld_add, void* dlogits, int64_t ld_out,
+                                     void* stream) {
+    BalanceParams P;
+    const int st = balance_params(cfg, logits, ld, T, seq_offsets, n_sequences, &P);
+    if (st != NVFP4_OK) return st;
+    if (ld_out < P.E || (add && ld_add < P.E)) return NVFP4_E_SHAPE;
+    if (T == 0) return NVFP4_OK;
+    if (!logits || !counts || !dlogits) return NVFP4_E_NULL;
+    const size_t elem = cfg->logits_type == NVFP4MOE_BF16 ? 2 : 4;
+    if (add == dlogits && ld_add != ld_out) return NVFP4_E_ARG;
+    if (!aligned(counts, 4) || !aligned(dloss, 4) || !aligned(add, elem) || !aligned(dlogits, elem)) return NVFP4_E_ALIGN;
+    P.counts_in = counts;
+    P.dloss = dloss;
+    P.add = add;
+    P.ld_add = ld_add;
+    P.dlogits = dlogits;
+    P.ld_out = ld_out;
+    P.vec_add = ld_add % 4 == 0 && aligned(add, 4 * elem);
+    P.vec_out = ld_out % 4 == 0 && aligned(dlogits, 4 * elem);
+    P.vec_counts = P.E % 4 == 0 && aligned(counts, 16);
+    return hip_status(launch_balance(P, cfg->logits_type == NVFP4MOE_BF16, (hipStream_t)stream));
 }
 
 int nvfp4moe_mxfp4_bytes(const nvfp4moe_mxfp4_tensor* q, size_t* codes_bytes, size_t* scales_bytes) {
@@ -329,6 +468,135 @@ int nvfp4moe_mxfp4_grouped_linear(const uint16_t* x, int64_t R, int64_t ldx, con
                                   const nvfp4moe_mxfp4_tensor* Wq, uint16_t* out, int64_t ld_out, int32_t scale_round,
                                   void* workspace, size_t workspace_bytes, void* stream) {
     return mx_product(x, R, ldx, offsets, true, Wq, out, ld_out, scale_round, workspace, workspace_bytes, stream);
+}
+
+size_t nvfp4moe_adapter_workspace_bytes(const nvfp4moe_adapters* ad, int64_t M, int32_t backward) {
+    return adapter_shape(ad, M) == NVFP4_OK ? adapter_work(ad, M, backward != 0).total : 0;
+}
+
+int nvfp4moe_adapter_linear(const nvfp4moe_adapters* ad, const uint16_t* x, int64_t M, int64_t ldx, const int32_t* ids,
+                            const uint16_t* base, int64_t ld_base, uint16_t* out, int64_t ld_out, float* v,
+                            void* workspace, size_t workspace_bytes, void* stream) {
+    int st = adapter_shape(ad, M);
+    if (st != NVFP4_OK) return st;
+    const int32_t K = ad->in_features, N = ad->out_features;
+    if (M == 0) return NVFP4_OK;
+    if (!x || !ids || !out || !workspace) return NVFP4_E_NULL;
+    if ((st = adapter_planes(ad)) != NVFP4_OK || (st = adapter_rows(x, ldx, K)) != NVFP4_OK ||
+        (st = adapter_rows(out, ld_out, N)) != NVFP4_OK || (base && (st = adapter_rows(base, ld_base, N)) != NVFP4_OK))
+        return st;
+    if (base == out && ld_base != ld_out) return NVFP4_E_ARG;
+    const AdapterWork w = adapter_work(ad, M, false);
+    if (workspace_bytes < w.total) return NVFP4_E_WORKSPACE;
+    if (!aligned(ids, 4) || !aligned(v, 16) || !aligned(workspace, kAlign)) return NVFP4_E_ALIGN;
+    uint8_t* ws = (uint8_t*)workspace;
+    AdapterPlan plan{};
+    plan.ids = ids;
+    plan.M = M;
+    plan.n = ad->n;
+    plan.tile = adapter_tile(ad->rank);
+    plan.rest = base != out || v;
+    plan.n_tables = (int32_t*)ws;
+    plan.order = (int32_t*)(ws + w.order);
+    plan.tiles = (int4*)(ws + w.tiles);
+    if (launch_adapter_plan(plan, (hipStream_t)stream) != hipSuccess) return NVFP4_E_HIP;
+    AdapterParams p{};
+    p.x = x;
+    p.ldx = ldx;
+    p.A = ad->A;
+    p.B = ad->B;
+    p.scale = ad->scale;
+    p.R = ad->rank;
+    p.K = K;
+    p.N = N;
+    p.base = base;
+    p.ld_base = ld_base;
+    p.out = out;
+    p.ld_out = ld_out;
+    p.v = v;
+    p.order = plan.order;
+    p.tiles = plan.tiles;
+    p.n_tiles = plan.n_tables;
+    return hip_status(launch_adapter(p, w.n_tiles, (hipStream_t)stream));
+}
+
+int nvfp4moe_adapter_backward(const nvfp4moe_adapters* ad, const uint16_t* x, int64_t M, int64_t ldx, const int32_t* ids,
+                              const float* v, const uint16_t* dy, int64_t ld_dy, const uint16_t* base, int64_t ld_base,
+                              uint16_t* dx, int64_t ld_dx, float* dA, float* dB, void* workspace, size_t workspace_bytes,
+                              void* stream) {
+    int st = adapter_shape(ad, M);
+    if (st != NVFP4_OK) return st;
+    const int32_t K = ad->in_features, N = ad->out_features;
+    if (!dA || !dB || !workspace || (M > 0 && (!x || !ids || !v || !dy || !dx))) return NVFP4_E_NULL;
+    if ((st = adapter_planes(ad)) != NVFP4_OK || (st = adapter_rows(x, ldx, K)) != NVFP4_OK ||
+        (st = adapter_rows(dy, ld_dy, N)) != NVFP4_OK || (st = adapter_rows(dx, ld_dx, K)) != NVFP4_OK ||
+        (base && (st = adapter_rows(base, ld_base, K)) != NVFP4_OK))
+        return st;
+    if (base && base == dx && ld_base != ld_dx) return NVFP4_E_ARG;
+    const AdapterWork w = adapter_work(ad, M, true);
+    if (workspace_bytes < w.total) return NVFP4_E_WORKSPACE;
+    if (!aligned(ids, 4) || !aligned(v, 4) || !aligned(dA, 16) || !aligned(dB, 16) || !aligned(workspace, kAlign))
+        return NVFP4_E_ALIGN;
+    uint8_t* ws = (uint8_t*)workspace;
+    hipStream_t s = (hipStream_t)stream;
+    AdapterPlan plan{};
+    plan.ids = ids;
+    plan.M = M;
+    plan.n = ad->n;
+    plan.tile = adapter_tile(ad->rank);
+    plan.chunk = w.chunk;
+    plan.rest = base != dx;
+    plan.n_tables = (int32_t*)ws;
+    plan.order = (int32_t*)(ws + w.order);
+    plan.tiles = (int4*)(ws + w.tiles);
+    plan.chunks = (int4*)(ws + w.chunks);
+    plan.info = (int2*)(ws + w.info);
+    if (launch_adapter_plan(plan, s) != hipSuccess) return NVFP4_E_HIP;
+    AdapterGrad g{};
+    g.A = ad->A;
+    g.B = ad->B;
+    g.scale = ad->scale;
+    g.n = ad->n;
+    g.R = ad->rank;
+    g.K = K;
+    g.N = N;
+    g.At = (uint16_t*)(ws + w.at);
+    g.Bt = (uint16_t*)(ws + w.bt);
+    g.x = x;
+    g.dy = dy;
+    g.ldx = ldx;
+    g.ld_dy = ld_dy;
+    g.v = v;
+    g.w = (float*)(ws + w.w);
+    g.order = plan.order;
+    g.chunks = plan.chunks;
+    g.n_tables = plan.n_tables;
+    g.info = plan.info;
+    g.slots = (float*)(ws + w.slots);
+    g.dA = dA;
+    g.dB = dB;
+    if (M > 0) {
+        if (launch_adapter_transpose(g, s) != hipSuccess) return NVFP4_E_HIP;
+        AdapterParams p{};
+        p.x = dy;
+        p.ldx = ld_dy;
+        p.A = g.Bt;
+        p.B = g.At;
+        p.scale = ad->scale;
+        p.R = ad->rank;
+        p.K = N;
+        p.N = K;
+        p.base = base;
+        p.ld_base = ld_base;
+        p.out = dx;
+        p.ld_out = ld_dx;
+        p.v = (float*)(ws + w.w);
+        p.order = plan.order;
+        p.tiles = plan.tiles;
+        p.n_tiles = plan.n_tables;
+        if (launch_adapter(p, w.n_tiles, s) != hipSuccess) return NVFP4_E_HIP;
+    }
+    return hip_status(launch_adapter_wgrad(g, w.n_chunks, s));
 }
 
 int nvfp4moe_grad_plan_bytes(const nvfp4moe_grad* grads, int32_t n_grads, size_t* bytes, int64_t* n_chunks) {

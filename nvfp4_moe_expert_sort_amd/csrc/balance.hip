@@ -1,0 +1,324 @@
+// balance.hip -- the router's balance loss, the experts' token counts, and the
+// loss's gradient (include/nvfp4moe.h, nvfp4moe_router_balance_loss).
+//
+// With n_se the slots of sequence s that name expert e, p_t the token's
+// probabilities over all experts and T' the tokens of all sequences:
+//   loss = coef E / (K T') sum_s 1 / T_s sum_e n_se sum_{t in s} p_te
+//   d/dl_te = coef E / (K T' T_s) p_te (n_se - sum_j n_sj p_tj)  [(1 - sigma_te)]
+// The counts are constants of the gradient.
+#include <algorithm>
+
+#include "nvfp4_device.h"
+#include "nvfp4_kernels.h"
+#include "router_lanes.h"
+
+namespace nvfp4 {
+
+namespace {
+
+constexpr int kBalThreads = 256;
+
+// e^d for d <= 0 within a few 2^-24 wherever it is a normal number: the part
+// of d log2 e that its rounding to FP32 drops is put back to first order.
+__device__ __forceinline__ float exp_neg(float d) {
+    d = max32(d, -150.0f);
+    const float t = d * 1.44269502f;
+    float r = __builtin_fmaf(d, 1.44269502f, -t);
+    r = __builtin_fmaf(d, 1.92596299e-8f, r);
+    const float e = __builtin_amdgcn_exp2f(t);
+    return __builtin_fmaf(e, r * 0.693147182f, e);
+}
+
+// Terms w_e >= 0 of the token's probabilities, p_e = w_e / sum w, from its
+// clean logits; for sigmoid scores other = 1 - sigma.  Both are shifted so
+// that the sum cannot vanish: by the largest logit, or for sigmoid scores by
+// m = min(largest, 0), sigma(l) e^-m = e^(l - m) / (1 + e^l).
+template <int LT, int NV>
+__device__ __forceinline__ void score_terms(const float (&l)[NV], bool sigmoid, float (&w)[NV], float (&other)[NV]) {
+    float mx = l[0];
+#pragma unroll
+    for (int i = 1; i < NV; i++) mx = max32(mx, l[i]);
+    mx = max32(tok_max<LT>(mx), -kFltMax);
+    if (sigmoid) {
+        mx = min32(mx, 0.0f);
+#pragma unroll
+        for (int i = 0; i < NV; i++) {
+            const bool neg = l[i] < 0.0f;
+            const float t = exp_neg(-fabsf(l[i])), inv = __builtin_amdgcn_rcpf(1.0f + t);
+            w[i] = l[i] > -__builtin_inff() ? (neg ? exp_neg(l[i] - mx) * inv : inv) : 0.0f;
+            other[i] = neg ? inv : t * inv;
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < NV; i++) {
+            w[i] = l[i] > -__builtin_inff() ? exp_neg(l[i] - mx) : 0.0f;
+            other[i] = 1.0f;
+        }
+    }
+}
+
+// First row of sequence s (of S; s == S: the end of the last), within [0, T].
+__device__ __forceinline__ int64_t seq_start(const BalanceParams& P, int32_t s) {
+    if (!P.offsets) return s == 0 ? 0 : P.T;
+    return min(max((int64_t)P.offsets[s], (int64_t)0), P.T);
+}
+// The sequence that holds row t, -1 before the first and S behind the last:
+// how many of the S + 1 offsets are <= t, less one.  All threads call it.
+__device__ __forceinline__ int32_t find_sequence(const BalanceParams& P, int64_t t, int32_t* lds) {
+    if (!P.offsets) return 0;
+    int32_t n = 0;
+    for (int32_t i = threadIdx.x; i <= P.S; i += kBalThreads) n += seq_start(P, i) <= t ? 1 : 0;
+#pragma unroll
+    for (int o = 32; o > 0; o >>= 1) n += __shfl_xor(n, o, kWave);
+    __syncthreads();
+    if ((threadIdx.x & 63) == 0) lds[threadIdx.x >> 6] = n;
+    __syncthreads();
+    return lds[0] + lds[1] + lds[2] + lds[3] - 1;
+}
+
+template <int LT, int NV, typename L>
+__device__ __forceinline__ void load_row(const L* row, const BalanceParams& P, int lane, float (&l)[NV]) {
+#pragma unroll
+    for (int i = 0; i < NV / 4; i++) {
+        float v[4];
+        load4(row, (i * LT + lane) * 4, P.E, P.vec, v);
+#pragma unroll
+        for (int j = 0; j < 4; j++) l[4 * i + j] = clean(v[j]);
+    }
+}
+
+}  // namespace
+
+// A workgroup takes P.chunk rows.  For each sequence in them it adds up the
+// probabilities (a lane its own experts over its tokens, then the token slots
+// in LDS) and the counts; chunk b's part of sequence s goes to slot b + s: a
+// walk along the rows raises b or s at every step, so no two parts share one.
+template <int LT, int NV, typename L>
+__global__ void __launch_bounds__(kBalThreads) balance_chunk_kernel(BalanceParams P) {
+    constexpr int kTok = kBalThreads / LT;
+    __shared__ float part[kTok][LT * NV];
+    __shared__ int32_t hist[LT * NV];
+    __shared__ int32_t found[4];
+    const int lane = threadIdx.x & (LT - 1), slot = threadIdx.x / LT;
+    const int64_t first = (int64_t)blockIdx.x * P.chunk, past = min(P.T, first + P.chunk);
+    if (blockIdx.x == 0 && threadIdx.x == 0) *P.done = 0;
+    for (int32_t s = max(find_sequence(P, first, found), 0); s < P.S; s++) {
+        const int64_t s0 = seq_start(P, s), lo = max(s0, first), hi = min(seq_start(P, s + 1), past);
+        if (s0 >= past) break;
+        if (lo >= hi) continue;
+        for (int e = threadIdx.x; e < P.E; e += kBalThreads) hist[e] = 0;
+        __syncthreads();
+        for (int64_t i = lo * P.K + threadIdx.x; i < hi * P.K; i += kBalThreads) {
+            const int32_t e = P.ids[i];
+            if (e >= 0 && e < P.E) atomicAdd(&hist[e], 1);
+        }
+        float acc[NV];
+#pragma unroll
+        for (int i = 0; i < NV; i++) acc[i] = 0.0f;
+        for (int64_t t0 = lo; t0 < hi; t0 += kTok) {
+            const bool live = t0 + slot < hi;
+            float l[NV], w[NV], other[NV];
+            load_row<LT, NV, L>((const L*)P.logits + min(t0 + slot, hi - 1) * P.ld, P, lane, l);
+            score_terms<LT, NV>(l, P.sigmoid, w, other);
+            float sum = 0.0f;
+#pragma unroll
+            for (int i = 0; i < NV; i++) sum += w[i];
+            sum = tok_sum<LT>(sum);
+            const float inv = live && sum > 0.0f ? 1.0f / sum : 0.0f;
+#pragma unroll
+            for (int i = 0; i < NV; i++) acc[i] = __builtin_fmaf(w[i], inv, acc[i]);
+        }
+#pragma unroll
+        for (int i = 0; i < NV; i++) part[slot][((i >> 2) * LT + lane) * 4 + (i & 3)] = acc[i];
+        __syncthreads();
+        const int64_t at = ((int64_t)blockIdx.x + s) * P.E;
+        for (int e = threadIdx.x; e < P.E; e += kBalThreads) {
+            float sum = 0.0f;
+            for (int k = 0; k < kTok; k++) sum += part[k][e];
+            P.psum[at + e] = sum;
+            P.csum[at + e] = hist[e];
+        }
+        __syncthreads();
+    }
+}
+
+// Adds the slots of one sequence and 64 experts in FP64, in one order; the
+// workgroup that is last to finish adds up the workgroups' shares of the loss.
+__global__ void __launch_bounds__(kBalThreads) balance_join_kernel(BalanceParams P) {
+    __shared__ double sums[4][64];
+    __shared__ int32_t cnts[4][64];
+    __shared__ bool last;
+    const int groups = (P.E + 63) / 64, col = threadIdx.x & 63, stripe = threadIdx.x >> 6;
+    const int32_t s = blockIdx.x / groups;
+    const int e = (blockIdx.x % groups) * 64 + col;
+    const int64_t lo = seq_start(P, s), hi = seq_start(P, s + 1);
+    double sum = 0.0;
+    int32_t n = 0;
+    if (hi > lo && e < P.E) {
+        for (int64_t b = lo / P.chunk + stripe; b <= (hi - 1) / P.chunk; b += 4) {
+            sum += (double)P.psum[(b + s) * P.E + e];
+            n += P.csum[(b + s) * P.E + e];
+        }
+    }
+    sums[stripe][col] = sum;
+    cnts[stripe][col] = n;
+    __syncthreads();
+    if (stripe == 0) {
+        sum = (sums[0][col] + sums[1][col]) + (sums[2][col] + sums[3][col]);
+        n = (cnts[0][col] + cnts[1][col]) + (cnts[2][col] + cnts[3][col]);
+        if (e < P.E) P.counts[(int64_t)s * P.E + e] = n;
+        double v = hi > lo ? sum * (double)n / (double)(hi - lo) : 0.0;
+#pragma unroll
+        for (int o = 32; o > 0; o >>= 1) v += __shfl_xor(v, o, kWave);
+        if (col == 0) {
+            P.part[blockIdx.x] = v;
+            __threadfence();
+            last = atomicAdd(P.done, 1u) == gridDim.x - 1;
+        }
+    }
+    __syncthreads();
+    if (!last) return;
+    __threadfence();
+    double total = 0.0;
+    for (uint32_t i = threadIdx.x; i < gridDim.x; i += kBalThreads) total += P.part[i];
+#pragma unroll
+    for (int o = 32; o > 0; o >>= 1) total += __shfl_xor(total, o, kWave);
+    if (col == 0) sums[0][stripe] = total;
+    __syncthreads();
+    if (threadIdx.x == 0) {
+        const double tokens = (double)max(seq_start(P, P.S) - seq_start(P, 0), (int64_t)1);
+        total = (sums[0][0] + sums[0][1]) + (sums[0][2] + sums[0][3]);
+        *P.loss = (float)(total * (double)P.coef * (double)P.E / ((double)P.K * tokens));
+    }
+}
+
+// One token per LT lanes.  With w the terms of p, D their sum and G = sum w n:
+//   d_e = c w_e (n_e D - G) / D^2
+// where D, G and the difference are FP64: for a token whose top expert has
+// nearly all the probability, n_e - sum n p is small against its terms, and
+// here only the relative errors of the w remain (some 2^-23 each).
+template <int LT, int NV, typename L>
+__global__ void __launch_bounds__(kBalThreads) balance_backward_kernel(BalanceParams P) {
+    constexpr int kTok = kBalThreads / LT;
+    __shared__ int32_t found[4];
+    const int lane = threadIdx.x & (LT - 1), slot = threadIdx.x / LT;
+    const double tokens = (double)max(seq_start(P, P.S) - seq_start(P, 0), (int64_t)1);
+    const double c0 = (double)(P.dloss ? *P.dloss : 1.0f) * (double)P.coef * (double)P.E / ((double)P.K * tokens);
+    for (int64_t tile = blockIdx.x; tile * kTok < P.T; tile += gridDim.x) {
+        const int64_t t = tile * kTok + slot, tr = min(t, P.T - 1);
+        float l[NV], w[NV], other[NV], add[NV];
+        load_row<LT, NV, L>((const L*)P.logits + tr * P.ld, P, lane, l);
+#pragma unroll
+        for (int i = 0; i < NV / 4; i++) {
+            float v[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+            if (P.add) load4((const L*)P.add + tr * P.ld_add, (i * LT + lane) * 4, P.E, P.vec_add, v);
+#pragma unroll
+            for (int j = 0; j < 4; j++) add[4 * i + j] = v[j];
+        }
+        int32_t s = max(find_sequence(P, tile * kTok, found), 0);
+        while (s < P.S && seq_start(P, s + 1) <= tr) s++;
+        double c = 0.0;  // rows of no sequence get no gradient
+        if (s < P.S) {
+            const int64_t lo = seq_start(P, s), hi = seq_start(P, s + 1);
+            if (tr >= lo && hi > lo) c = c0 / (double)(hi - lo);
+        }
+        const int32_t* counts = P.counts_in + (int64_t)min(s, P.S - 1) * P.E;
+        float n[NV];
+#pragma unroll
+        for (int i = 0; i < NV / 4; i++) {
+            const int e0 = (i * LT + lane) * 4;
+            if (P.vec_counts && e0 + 4 <= P.E) {
+                const int4 q = *reinterpret_cast<const int4*>(counts + e0);
+                n[4 * i] = __int_as_float(q.x), n[4 * i + 1] = __int_as_float(q.y);
+                n[4 * i + 2] = __int_as_float(q.z), n[4 * i + 3] = __int_as_float(q.w);
+            } else {
+#pragma unroll
+                for (int j = 0; j < 4; j++) n[4 * i + j] = __int_as_float(e0 + j < P.E ? counts[e0 + j] : 0);
+            }
+        }
+        score_terms<LT, NV>(l, P.sigmoid, w, other);
+        double D = 0.0, G = 0.0;
+#pragma unroll
+        for (int i = 0; i < NV; i++) {
+            D += (double)w[i];
+            G = __builtin_fma((double)w[i], (double)__float_as_int(n[i]), G);
+        }
+        D = tok_sum<LT>(D);
+        G = tok_sum<LT>(G);
+        c = D > 0.0 ? c / (D * D) : 0.0;
+        if (t >= P.T) continue;
+        L* out = (L*)P.dlogits + t * P.ld_out;
+#pragma unroll
+        for (int i = 0; i < NV / 4; i++) {
+            const int e0 = (i * LT + lane) * 4;
+            if (e0 >= P.E) continue;
+            float v[4];
+#pragma unroll
+            for (int j = 0; j < 4; j++) {
+                const int k = 4 * i + j;
+                const double d = c * (double)(w[k] * other[k]) * __builtin_fma((double)__float_as_int(n[k]), D, -G);
+                v[j] = (float)(d + (double)add[k]);
+            }
+            if constexpr (sizeof(L) == 4) {
+                if (P.vec_out && e0 + 4 <= P.E)
+                    *reinterpret_cast<float4*>(out + e0) = float4{v[0], v[1], v[2], v[3]};
+                else
+                    for (int j = 0; j < 4; j++)
+                        if (e0 + j < P.E) out[e0 + j] = v[j];
+            } else {
+                if (P.vec_out && e0 + 4 <= P.E)
+                    *reinterpret_cast<u32x2*>(out + e0) =
+                        u32x2{bf16_hw(v[0]) | (bf16_hw(v[1]) << 16), bf16_hw(v[2]) | (bf16_hw(v[3]) << 16)};
+                else
+                    for (int j = 0; j < 4; j++)
+                        if (e0 + j < P.E) out[e0 + j] = (uint16_t)bf16_hw(v[j]);
+            }
+        }
+    }
+}
+
+namespace {
+
+template <int LT, int NV, typename L>
+hipError_t loss_run(const BalanceParams& P, hipStream_t s) {
+    const int64_t chunks = std::max<int64_t>(1, (P.T + P.chunk - 1) / P.chunk);
+    hipLaunchKernelGGL((balance_chunk_kernel<LT, NV, L>), dim3((unsigned)chunks), dim3(kBalThreads), 0, s, P);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+    hipLaunchKernelGGL(balance_join_kernel, dim3((unsigned)(P.S * ((P.E + 63) / 64))), dim3(kBalThreads), 0, s, P);
+    return hipGetLastError();
+}
+template <int LT, int NV, typename L>
+hipError_t balance_backward_run(const BalanceParams& P, hipStream_t s) {
+    constexpr int kTok = kBalThreads / LT;
+    const int64_t tiles = (P.T + kTok - 1) / kTok;
+    hipLaunchKernelGGL((balance_backward_kernel<LT, NV, L>), dim3((unsigned)std::min<int64_t>(tiles, 65536)),
+                       dim3(kBalThreads), 0, s, P);
+    return hipGetLastError();
+}
+// 16 lanes a token hold up to 256 experts, 64 lanes up to 1024.
+template <typename L>
+hipError_t balance_type(const BalanceParams& P, hipStream_t s) {
+    const bool back = P.dlogits != nullptr;
+    if (P.E <= 64) return back ? balance_backward_run<16, 4, L>(P, s) : loss_run<16, 4, L>(P, s);
+    if (P.E <= 128) return back ? balance_backward_run<16, 8, L>(P, s) : loss_run<16, 8, L>(P, s);
+    if (P.E <= 256) return back ? balance_backward_run<16, 16, L>(P, s) : loss_run<16, 16, L>(P, s);
+    if (P.E <= 512) return back ? balance_backward_run<64, 8, L>(P, s) : loss_run<64, 8, L>(P, s);
+    return back ? balance_backward_run<64, 16, L>(P, s) : loss_run<64, 16, L>(P, s);
+}
+
+}  // namespace
+
+// Rows of a workgroup of the loss: few enough that 256 CUs have one each, at
+// most 256 (a lane then adds 16 tokens in FP32 before FP64 takes over).
+int32_t balance_chunk(int64_t T) {
+    int32_t chunk = 16;
+    while (chunk < 256 && (T + chunk - 1) / chunk > 256) chunk *= 2;
+    return chunk;
+}
+
+hipError_t launch_balance(const BalanceParams& P, bool bf16, hipStream_t stream) {
+    return bf16 ? balance_type<uint16_t>(P, stream) : balance_type<float>(P, stream);
+}
+
+}  // namespace nvfp4

@@ -131,6 +131,92 @@ struct SelectParams {
 hipError_t launch_router_select(SelectParams P, bool bf16, hipStream_t stream);
 hipError_t launch_router_select_backward(const SelectParams& P, bool bf16, hipStream_t stream);
 
+// The balance loss, the experts' counts and the loss's gradient (balance.hip).
+constexpr int32_t kMaxSequences = 65536;
+struct BalanceParams {
+    const void* logits;  // FP32 or BF16 [T, E], rows ld apart
+    int64_t ld, T;
+    int32_t E, K, S;
+    const int32_t* offsets;  // [S + 1], or null: one sequence of all rows
+    float coef;
+    bool sigmoid, vec;
+    const int32_t* ids;  // loss: [T, K]
+    int32_t chunk;       // rows of a workgroup
+    float* psum;         // [chunks + S][E] sums of probabilities, and counts
+    int32_t* csum;
+    double* part;        // workgroups' shares of the loss
+    uint32_t* done;
+    float* loss;
+    int32_t* counts;     // [S, E]
+    const int32_t* counts_in;  // gradient
+    const float* dloss;        // or null: 1
+    const void* add;           // [T, E] of the logits' type, or null
+    int64_t ld_add;
+    void* dlogits;
+    int64_t ld_out;
+    bool vec_add, vec_out, vec_counts;
+};
+int32_t balance_chunk(int64_t T);
+hipError_t launch_balance(const BalanceParams& P, bool bf16, hipStream_t stream);
+
+// Low-rank adapters and their gradients (adapter.hip).
+constexpr int kMaxRank = 128;
+struct AdapterPlan {  // rows grouped by adapter
+    const int32_t* ids;  // [M]
+    int64_t M, rows;     // rows per workgroup; set by the launcher
+    int32_t n, tile;
+    int32_t chunk;       // rows of a chunk of the gradients, 0: forward
+    bool rest;           // tiles for the rows without an adapter too
+    int32_t* n_tables;   // [2]: row tiles, chunks
+    int32_t* order;      // [M]
+    int4* tiles;         // {adapter or -1, first position in order, rows, 0}
+    int4* chunks;        // {adapter, first position, rows, partial sum or -1: the adapter's only one}
+    int2* info;          // [n] {chunks, first partial sum}
+};
+hipError_t launch_adapter_plan(AdapterPlan P, hipStream_t stream);
+struct AdapterParams {
+    const uint16_t* x;
+    int64_t ldx;
+    const uint16_t* A;   // [n][R][K]
+    const uint16_t* B;   // [n][N][R]
+    const float* scale;  // [n] or null
+    int32_t R, K, N;
+    const uint16_t* base;  // or null
+    int64_t ld_base;
+    uint16_t* out;
+    int64_t ld_out;
+    float* v;            // [M][R] or null
+    const int32_t* order;
+    const int4* tiles;
+    const int32_t* n_tiles;
+    int32_t slabs;       // set by the launcher
+};
+int adapter_tile(int32_t R);  // rows of a row tile
+hipError_t launch_adapter(AdapterParams P, int64_t tiles_bound, hipStream_t stream);
+struct AdapterGrad {
+    const uint16_t* A;
+    const uint16_t* B;
+    const float* scale;
+    int32_t n, R, K, N;
+    uint16_t* At;        // [n][K][R]
+    uint16_t* Bt;        // [n][R][N]
+    const uint16_t* x;
+    const uint16_t* dy;
+    int64_t ldx, ld_dy;
+    const float* v;      // [M][R] A x, and B^T dy
+    const float* w;
+    const int32_t* order;
+    const int4* chunks;
+    const int32_t* n_tables;
+    const int2* info;
+    float* slots;        // partial sums, R (K + N) each
+    float* dA;
+    float* dB;
+};
+int32_t adapter_chunk(int64_t M, int64_t K, int64_t N);
+hipError_t launch_adapter_transpose(const AdapterGrad& P, hipStream_t stream);
+hipError_t launch_adapter_wgrad(const AdapterGrad& P, int64_t chunks_bound, hipStream_t stream);
+
 // MXFP4 quantizers (mxfp4_quant.hip) and products (mxfp4_gemm.hip).
 constexpr int kMxUnroll = 4;  // 8-element groups per thread
 struct MxRowsParams {

@@ -1,4 +1,4 @@
-"""Expert selection, MXFP4 products and gradient clipping: the binding of these entry points (``include/nvfp4moe.h``
+"""Expert selection, the balance loss, MXFP4 products, low-rank adapters and gradient clipping: the binding of these entry points (``include/nvfp4moe.h``
 documents each) for PyTorch tensors.
 
 At decode sizes a call takes a few microseconds on the GPU, so the binding's own time counts: arguments are checked
@@ -12,8 +12,8 @@ import functools
 
 import torch
 
-from . import (BF16, F32, GROUP_MAX, LAYOUT_GEMM, LAYOUT_LOGICAL, MXFP4_SCALE_FLOOR, SCORE_SOFTMAX, Grad, Mxfp4Tensor,
-               Nvfp4Error, SelectConfig, _check, lib)
+from . import (BF16, F32, GROUP_MAX, LAYOUT_GEMM, LAYOUT_LOGICAL, MXFP4_SCALE_FLOOR, SCORE_SOFTMAX, Adapters, BalanceConfig,
+               Grad, Mxfp4Tensor, Nvfp4Error, SelectConfig, _check, lib)
 
 _BF16 = (torch.bfloat16, torch.int16, torch.uint16)  # storage of BF16 bits
 _TYPES = {torch.float32: F32, torch.bfloat16: BF16}
@@ -146,6 +146,84 @@ def router_select_backward(logits, ids, dprobs, bias=None, score: int = SCORE_SO
     return out
 
 
+@functools.lru_cache(256)
+def _balance_config(*fields):
+    """A pointer to the BalanceConfig of these values."""
+    return ctypes.pointer(BalanceConfig(*fields))
+
+
+def _sequences(where, offsets, device):
+    """Number of sequences and the address of their offsets (None: one sequence of all rows)."""
+    if offsets is None:
+        return 1, None
+    if offsets.dim() != 1 or offsets.numel() < 2:
+        raise ValueError(f"{where}: offsets must have one entry more than there are sequences, got {tuple(offsets.shape)}")
+    _need(where, offsets, "offsets", (torch.int32,), offsets.shape, device)
+    return offsets.numel() - 1, offsets.data_ptr()
+
+
+@functools.lru_cache(256)
+def _balance_workspace_bytes(T, E, S):
+    n = lib().nvfp4moe_balance_workspace_bytes(T, E, S)
+    if n == 0:
+        raise Nvfp4Error(2, "nvfp4moe_balance_workspace_bytes")
+    return n
+
+
+def router_balance_loss(logits, ids, coef: float, score: int = SCORE_SOFTMAX, offsets=None, stream=None):
+    """nvfp4moe_router_balance_loss: logits [T,E] f32 or bf16 (rows may be strided), ids [T,k] int32 (router_select's),
+    offsets [S+1] int32 on the GPU (default: one sequence of all rows) -> (loss [1] float32, counts [S,E] int32)."""
+    where = "router_balance_loss"
+    kind, ld = _logits(where, logits, None)
+    T, E = logits.shape
+    if ids.dim() != 2:
+        raise ValueError(f"{where}: ids must be a matrix, got {tuple(ids.shape)}")
+    k = ids.shape[1]
+    _need(where, ids, "ids", (torch.int32,), (T, k), logits.device)
+    S, off = _sequences(where, offsets, logits.device)
+    if _elsewhere(logits, stream):
+        with _there(stream, logits, ids, offsets):
+            return router_balance_loss(logits, ids, coef, score, offsets)
+    loss = torch.empty((1,), dtype=torch.float32, device=logits.device)
+    counts = torch.empty((S, E), dtype=torch.int32, device=logits.device)
+    n = _balance_workspace_bytes(T, E, S)
+    ws = torch.empty((n,), dtype=torch.uint8, device=logits.device)
+    st = lib().nvfp4moe_router_balance_loss(_balance_config(E, k, score, kind, coef), logits.data_ptr(), ld, T,
+                                            ids.data_ptr(), off, S, loss.data_ptr(), counts.data_ptr(), ws.data_ptr(), n,
+                                            _raw_stream(logits))
+    _check(st, "nvfp4moe_router_balance_loss")
+    return loss, counts
+
+
+def router_balance_backward(logits, counts, k: int, coef: float, score: int = SCORE_SOFTMAX, offsets=None, dloss=None,
+                            add=None, out=None, stream=None):
+    """nvfp4moe_router_balance_backward: router_balance_loss's logits, counts and offsets, k slots a token, dloss
+    float32 [1] on the GPU (default 1), add [T,E] of the logits' type (router_select_backward's dlogits, which `out`
+    may be) -> dlogits [T,E] of the logits' type."""
+    where = "router_balance_backward"
+    kind, ld = _logits(where, logits, None)
+    T, E = logits.shape
+    S, off = _sequences(where, offsets, logits.device)
+    _need(where, counts, "counts", (torch.int32,), (S, E), logits.device)
+    if dloss is not None:
+        _need(where, dloss, "dloss", (torch.float32,), (1,), logits.device)
+    if add is not None:
+        _need(where, add, "add", (logits.dtype,), (T, E), logits.device, contiguous=False)
+    if _elsewhere(logits, stream):
+        with _there(stream, logits, counts, offsets, dloss, add, out):
+            return router_balance_backward(logits, counts, k, coef, score, offsets, dloss, add, out)
+    if out is None:
+        out = torch.empty((T, E), dtype=logits.dtype, device=logits.device)
+    else:
+        _need(where, out, "out", (logits.dtype,), (T, E), logits.device, contiguous=False)
+    st = lib().nvfp4moe_router_balance_backward(
+        _balance_config(E, k, score, kind, coef), logits.data_ptr(), ld, T, counts.data_ptr(), off, S,
+        None if dloss is None else dloss.data_ptr(), None if add is None else add.data_ptr(),
+        0 if add is None else _ld(where, add, "add"), out.data_ptr(), _ld(where, out, "out"), _raw_stream(logits))
+    _check(st, "nvfp4moe_router_balance_backward")
+    return out
+
+
 def mxfp4_quantize(x, scale_round: int = MXFP4_SCALE_FLOOR, out=None, stream=None):
     """nvfp4moe_mxfp4_quantize, logical layout: x [rows, cols] BF16 (rows may be strided) -> (codes [rows, cols/2]
     uint8, scales [rows, cols/32] uint8)."""
@@ -271,6 +349,103 @@ def mxfp4_grouped_linear(x, offsets, W: Mxfp4Weights, scale_round: int = MXFP4_S
     """nvfp4moe_mxfp4_grouped_linear: x [R,K] BF16 with expert e's rows in [offsets[e], offsets[e+1]) (int32, on the
     GPU), W of E matrices [N,K] -> out [R,N] BF16; rows outside the offsets are not written."""
     return _mxfp4_product("nvfp4moe_mxfp4_grouped_linear", x, offsets, W, scale_round, workspace, out, stream)
+
+
+def adapter_workspace_bytes(M: int, K: int, N: int, rank: int, n: int, backward: bool = False) -> int:
+    size = lib().nvfp4moe_adapter_workspace_bytes(Adapters(None, None, None, n, rank, K, N), M, 1 if backward else 0)
+    if size == 0:
+        raise Nvfp4Error(2, "nvfp4moe_adapter_workspace_bytes")
+    return size
+
+
+def adapter_alloc_workspace(M: int, K: int, N: int, rank: int, n: int, backward: bool = False, device="cuda"):
+    return torch.empty((adapter_workspace_bytes(M, K, N, rank, n, backward),), dtype=torch.uint8, device=device)
+
+
+def _adapters(where, x, ids, A, B, scale):
+    """Checks a set of adapters and the rows they apply to; the set, and its sizes (M, K, N, rank, n)."""
+    if A.dim() != 3 or B.dim() != 3 or x.dim() != 2:
+        raise ValueError(f"{where}: needs x [M, K], A [n, rank, K] and B [n, N, rank], got {tuple(x.shape)}, "
+                         f"{tuple(A.shape)} and {tuple(B.shape)}")
+    n, rank, K = A.shape
+    M, N = x.shape[0], B.shape[1]
+    _need(where, x, "x", _BF16, (M, K), x.device, contiguous=False)
+    _need(where, ids, "ids", (torch.int32,), (M,), x.device)
+    _need(where, A, "A", _BF16, (n, rank, K), x.device)
+    _need(where, B, "B", _BF16, (n, N, rank), x.device)
+    if scale is not None:
+        _need(where, scale, "scale", (torch.float32,), (n,), x.device)
+    return Adapters(A.data_ptr(), B.data_ptr(), None if scale is None else scale.data_ptr(), n, rank, K, N), (M, K, N, rank, n)
+
+
+def _rows(where, t, name, shape, device):
+    """Address and row stride of a BF16 matrix, or of none."""
+    if t is None:
+        return None, 0
+    _need(where, t, name, _BF16, shape, device, contiguous=False)
+    return t.data_ptr(), _ld(where, t, name)
+
+
+def adapter_linear(x, ids, A, B, base=None, scale=None, out=None, v=None, workspace=None, stream=None):
+    """nvfp4moe_adapter_linear: x [M,K] BF16, ids [M] int32 (each row's adapter, outside [0,n) none), A [n,rank,K] and
+    B [n,N,rank] BF16, scale [n] float32 (default 1), base [M,N] BF16 (the shared projection's output, default 0) ->
+    base + scale (x A^T) B^T [M,N] BF16.  `out` may be base; `v` [M,rank] float32 receives x A^T, which
+    adapter_backward takes.  Rows of x, base and out may be strided; `workspace` (adapter_alloc_workspace) may be shared
+    by calls that follow each other on one stream."""
+    where = "adapter_linear"
+    ad, (M, K, N, rank, n) = _adapters(where, x, ids, A, B, scale)
+    dev = x.device
+    base_at, ld_base = _rows(where, base, "base", (M, N), dev)
+    if _elsewhere(x, stream):
+        with _there(stream, x, ids, A, B, base, scale, out, v, workspace):
+            return adapter_linear(x, ids, A, B, base, scale, out, v, workspace)
+    if out is None:
+        out = torch.empty((M, N), dtype=x.dtype, device=dev)
+    out_at, ld_out = _rows(where, out, "out", (M, N), dev)
+    if v is not None:
+        _need(where, v, "v", (torch.float32,), (M, rank), dev)
+    if workspace is None:
+        workspace = adapter_alloc_workspace(M, K, N, rank, n, False, dev)
+    else:
+        _need(where, workspace, "workspace", (torch.uint8,), (workspace.numel(),), dev)
+    st = lib().nvfp4moe_adapter_linear(ad, x.data_ptr(), M, _ld(where, x, "x"), ids.data_ptr(), base_at, ld_base, out_at,
+                                       ld_out, None if v is None else v.data_ptr(), workspace.data_ptr(),
+                                       workspace.numel(), _raw_stream(x))
+    _check(st, "nvfp4moe_adapter_linear")
+    return out
+
+
+def adapter_backward(x, ids, A, B, v, dy, base=None, scale=None, out=None, workspace=None, stream=None):
+    """nvfp4moe_adapter_backward: adapter_linear's x, ids, A, B, scale and v, the gradient dy [M,N] BF16 of its output,
+    base [M,K] BF16 (the gradient through the shared projection, default 0) -> (dx [M,K] BF16, dA [n,rank,K] float32,
+    dB [n,N,rank] float32).  `out` may hold the three, preallocated; dx may be base."""
+    where = "adapter_backward"
+    ad, (M, K, N, rank, n) = _adapters(where, x, ids, A, B, scale)
+    dev = x.device
+    _need(where, v, "v", (torch.float32,), (M, rank), dev)
+    dy_at, ld_dy = _rows(where, dy, "dy", (M, N), dev)
+    base_at, ld_base = _rows(where, base, "base", (M, K), dev)
+    if _elsewhere(x, stream):
+        with _there(stream, x, ids, A, B, v, dy, base, scale, workspace, *(out or ())):
+            return adapter_backward(x, ids, A, B, v, dy, base, scale, out, workspace)
+    if out is None:
+        dx = torch.empty((M, K), dtype=x.dtype, device=dev)
+        dA = torch.empty((n, rank, K), dtype=torch.float32, device=dev)
+        dB = torch.empty((n, N, rank), dtype=torch.float32, device=dev)
+    else:
+        dx, dA, dB = out
+        _need(where, dA, "out dA", (torch.float32,), (n, rank, K), dev)
+        _need(where, dB, "out dB", (torch.float32,), (n, N, rank), dev)
+    dx_at, ld_dx = _rows(where, dx, "out dx", (M, K), dev)
+    if workspace is None:
+        workspace = adapter_alloc_workspace(M, K, N, rank, n, True, dev)
+    else:
+        _need(where, workspace, "workspace", (torch.uint8,), (workspace.numel(),), dev)
+    st = lib().nvfp4moe_adapter_backward(ad, x.data_ptr(), M, _ld(where, x, "x"), ids.data_ptr(), v.data_ptr(), dy_at, ld_dy,
+                                         base_at, ld_base, dx_at, ld_dx, dA.data_ptr(), dB.data_ptr(),
+                                         workspace.data_ptr(), workspace.numel(), _raw_stream(x))
+    _check(st, "nvfp4moe_adapter_backward")
+    return dx, dA, dB
 
 
 class GradSet:
