@@ -19,6 +19,7 @@ typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 typedef float f32x4 __attribute__((ext_vector_type(4)));
 
 constexpr int kAdWaves = 8;          // wavefronts that share the first product's K
+constexpr int kPlanThreads = 1024;
 constexpr int kBins = kMaxExperts + 1;  // adapters, and the rows without one
 
 __device__ __forceinline__ f32x4 mfma16(u32x4 a, u32x4 b, f32x4 c) {
@@ -35,9 +36,9 @@ __device__ __forceinline__ uint32_t bf16_piece(float& rest) {
     return b;
 }
 
-// Sum over the block's earlier entries of a[0..n), in place; 256 threads, every one calls it.
+// Sum over the workgroup's earlier entries of a[0..n), in place; every thread calls it.
 __device__ __forceinline__ void block_scan(int32_t* a, int n, int32_t* lds) {
-    const int per = (n + 255) / 256, lo = min((int)threadIdx.x * per, n), hi = min(lo + per, n);
+    const int per = (n + kPlanThreads - 1) / kPlanThreads, lo = min((int)threadIdx.x * per, n), hi = min(lo + per, n);
     int32_t sum = 0;
     for (int i = lo; i < hi; i++) sum += a[i];
     int32_t incl = sum;
@@ -69,118 +70,142 @@ __device__ __forceinline__ int find_bin(const int32_t* start, int n, int32_t i) 
     return lo;
 }
 
-__device__ __forceinline__ int row_bin(const AdapterPlan& P, int64_t r) {
-    const int32_t a = P.ids[r];
-    return a >= 0 && a < P.n ? a : P.n;
-}
+__device__ __forceinline__ int bin_of(const AdapterPlan& P, int32_t id) { return id >= 0 && id < P.n ? id : P.n; }
 
-// Counts the lanes' bins (those of live lanes) in LDS.  Neighbouring rows mostly
-// share an adapter: one lane then adds for all.
-__device__ __forceinline__ void count_bins(int32_t* hist, int b, bool live) {
-    const uint64_t m = __ballot(live);
-    if (!m) return;
-    const int lead = __builtin_ctzll(m), lead_bin = __builtin_amdgcn_readlane(b, lead);
-    if (__ballot(live && b == lead_bin) == m) {
-        if ((int)(threadIdx.x & 63) == lead) atomicAdd(&hist[lead_bin], __popcll(m));
-    } else if (live) {
-        atomicAdd(&hist[b], 1);
+// Counts the bins of the lanes' four consecutive rows in LDS, of which the
+// first `live` exist.  Neighbouring rows mostly share an adapter: one lane then
+// adds for all.
+__device__ __forceinline__ void count4(int32_t* hist, const AdapterPlan& P, int4 id, int64_t live) {
+    if (live <= 0) return;
+    const int b0 = bin_of(P, id.x), b1 = bin_of(P, id.y), b2 = bin_of(P, id.z), b3 = bin_of(P, id.w);
+    const bool same = live >= 4 && b0 == b1 && b0 == b2 && b0 == b3;
+    if (__ballot(same && b0 == __builtin_amdgcn_readfirstlane(b0)) == ~0ull) {
+        if ((threadIdx.x & 63) == 0) atomicAdd(&hist[b0], 256);
+    } else if (same) {
+        atomicAdd(&hist[b0], 4);
+    } else {
+        atomicAdd(&hist[b0], 1);
+        if (live > 1) atomicAdd(&hist[b1], 1);
+        if (live > 2) atomicAdd(&hist[b2], 1);
+        if (live > 3) atomicAdd(&hist[b3], 1);
     }
 }
 
 }  // namespace
 
 // Rows grouped by adapter, each adapter's in their order, rows without one
-// behind them; the row tiles and, for the gradients, the row chunks.  Every
-// workgroup counts all rows (and those before its own) for itself, which saves
-// a launch that only counts; its wavefronts place consecutive rows.
-__global__ void __launch_bounds__(256) adapter_plan_kernel(AdapterPlan P) {
-    __shared__ int32_t total[kBins + 1], start[kBins + 1], before[kBins], wave_base[4][kBins], scan[4];
+// behind them; the row tiles and, for the gradients, the row chunks, which the
+// last workgroup writes.  Every workgroup counts all rows for itself (16 K rows
+// of ids in flight at once), which saves a launch that only counts.
+__global__ void __launch_bounds__(kPlanThreads) adapter_plan_kernel(AdapterPlan P) {
+    constexpr int kWaves = kPlanThreads / 64, kAhead = 4;
+    __shared__ int32_t total[kBins + 1], start[kBins + 1], before[kBins], scan[kWaves];
+    __shared__ uint16_t counts[kWaves][kBins];
+    __shared__ int32_t tile0[kBins], chunk0[kBins], slot0[kBins];
     const int bins = P.n + 1, wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
-    const int64_t first = (int64_t)blockIdx.x * P.rows, share = P.rows / 4;  // rows of the workgroup, of a wavefront
-    for (int i = threadIdx.x; i <= bins; i += 256) total[i] = 0;
-    for (int i = threadIdx.x; i < bins; i += 256) before[i] = wave_base[0][i] = wave_base[1][i] = wave_base[2][i] = wave_base[3][i] = 0;
+    const bool tables = blockIdx.x == gridDim.x - 1;
+    const int64_t first = tables ? 0 : (int64_t)blockIdx.x * P.rows;  // a multiple of 256: a wavefront's rows lie on one side
+    for (int i = threadIdx.x; i <= bins; i += kPlanThreads) total[i] = 0;
+    for (int i = threadIdx.x; i < bins; i += kPlanThreads) before[i] = 0;
     __syncthreads();
-    for (int64_t r0 = 0; r0 < P.M; r0 += 256) {
-        const int64_t r = r0 + threadIdx.x;
-        const bool live = r < P.M;
-        const int b = live ? row_bin(P, r) : 0;
-        count_bins(total, b, live);
-        if (r0 < first) count_bins(before, b, live && r < first);
-    }
-    for (int64_t k = lane; k < share; k += 64) {
-        const int64_t r = first + wave * share + k;
-        const bool live = r < P.M;
-        count_bins(wave_base[wave], live ? row_bin(P, r) : 0, live);
-    }
-    __syncthreads();
-    for (int i = threadIdx.x; i < bins; i += 256) {  // where the wavefront's rows of the bin start among the bin's
-        int32_t run = before[i];
-        for (int w = 0; w < 4; w++) {
-            const int32_t n = wave_base[w][i];
-            wave_base[w][i] = run;
-            run += n;
+    for (int64_t r0 = 0; r0 < P.M; r0 += 4 * kPlanThreads * kAhead) {
+        int4 id[kAhead];
+#pragma unroll
+        for (int k = 0; k < kAhead; k++) {
+            const int64_t r = r0 + 4 * ((int64_t)k * kPlanThreads + threadIdx.x);
+            id[k] = make_int4(-1, -1, -1, -1);
+            if (P.vec && r + 4 <= P.M) {
+                id[k] = *reinterpret_cast<const int4*>(P.ids + r);
+            } else {
+                if (r < P.M) id[k].x = P.ids[r];
+                if (r + 1 < P.M) id[k].y = P.ids[r + 1];
+                if (r + 2 < P.M) id[k].z = P.ids[r + 2];
+                if (r + 3 < P.M) id[k].w = P.ids[r + 3];
+            }
+        }
+#pragma unroll
+        for (int k = 0; k < kAhead; k++) {
+            const int64_t r = r0 + 4 * ((int64_t)k * kPlanThreads + threadIdx.x);
+            count4(r < first ? before : total, P, id[k], P.M - r);
         }
     }
-    for (int i = threadIdx.x; i <= bins; i += 256) start[i] = total[i];
+    __syncthreads();
+    for (int i = threadIdx.x; i <= bins; i += kPlanThreads) {
+        if (i < bins) total[i] += before[i];
+        start[i] = total[i];
+    }
     __syncthreads();
     block_scan(start, bins + 1, scan);
-    // Place the wavefront's rows, 64 at a time: a row's rank is the number of
-    // lanes before it in the same bin.
-    for (int64_t k = 0; k < share && first + wave * share + k < P.M; k += 64) {
-        const int64_t r = first + wave * share + k + lane;
-        const bool live = r < P.M;
-        const int b = live ? row_bin(P, r) : -1;
-        uint64_t left = __ballot(live);
-        while (left) {
-            const int lead = __builtin_ctzll(left);
-            const int lead_bin = __builtin_amdgcn_readlane(b, lead);
-            const uint64_t same = __ballot(live && b == lead_bin);
-            const int32_t base = start[lead_bin] + wave_base[wave][lead_bin];
-            if (live && b == lead_bin) P.order[base + __popcll(same & ((1ull << lane) - 1))] = (int32_t)r;
-            if (lane == lead) wave_base[wave][lead_bin] += __popcll(same);
-            left &= ~same;
+    if (!tables) {
+        // 1024 rows at a time, one a thread.  Lanes of one bin find each other
+        // by a ballot for each bit of it; a row's place is the bin's next one,
+        // plus the bin's rows in earlier wavefronts and earlier lanes.
+        for (int i = threadIdx.x; i < bins; i += kPlanThreads) start[i] += before[i];
+        for (int64_t k = 0; k < P.rows && first + k < P.M; k += kPlanThreads) {
+            const int64_t r = first + k + threadIdx.x;
+            const bool live = r < P.M;
+            const int b = live ? bin_of(P, P.ids[r]) : 0;
+            uint64_t same = __ballot(live);
+            for (int bit = 0; (P.n >> bit) != 0; bit++) {
+                const bool on = (b >> bit) & 1;
+                const uint64_t m = __ballot(on);
+                same &= on ? m : ~m;
+            }
+            uint16_t* mine = counts[wave];
+            for (int i = lane; i < bins; i += 64) mine[i] = 0;
+            asm volatile("" ::: "memory");  // (a wavefront's LDS stores take effect in order)
+            const int rank = __popcll(same & ((1ull << lane) - 1));
+            if (live && rank == 0) mine[b] = (uint16_t)__popcll(same);
+            __syncthreads();
+            for (int i = threadIdx.x; i < bins; i += kPlanThreads) {
+                uint32_t run = 0;
+                for (int w = 0; w < kWaves; w++) {
+                    const uint32_t n = counts[w][i];
+                    counts[w][i] = (uint16_t)run;
+                    run += n;
+                }
+                before[i] = run;
+            }
+            __syncthreads();
+            if (live) P.order[start[b] + mine[b] + rank] = (int32_t)r;
+            __syncthreads();
+            for (int i = threadIdx.x; i < bins; i += kPlanThreads) start[i] += before[i];
         }
+        return;
     }
-    if (blockIdx.x != 0) return;
-    __syncthreads();
-    // The tables, by workgroup 0.  wave_base is free now: starts of a bin's
-    // tiles, chunks and partial sums in them.
-    int32_t *tile0 = wave_base[0], *chunk0 = wave_base[1], *slot0 = wave_base[2];
-    for (int i = threadIdx.x; i < bins; i += 256) {
+    for (int i = threadIdx.x; i < bins; i += kPlanThreads) {
         const int32_t chunks = i < P.n && P.chunk ? (total[i] + P.chunk - 1) / P.chunk : 0;
         tile0[i] = i < P.n || P.rest ? (total[i] + P.tile - 1) / P.tile : 0;
         chunk0[i] = chunks;
         slot0[i] = chunks > 1 ? chunks : 0;
     }
     __syncthreads();
-    int32_t n_tiles = 0, n_chunks = 0;
-    if (threadIdx.x == 0) {
-        n_tiles = tile0[bins - 1];
-        n_chunks = chunk0[bins - 1];
-    }
+    const int32_t last_tiles = tile0[bins - 1];  // (the rows without an adapter have no chunks)
     __syncthreads();
     block_scan(tile0, bins, scan);
-    block_scan(chunk0, bins, scan);
-    block_scan(slot0, bins, scan);
-    if (threadIdx.x == 0) {
-        total[bins] = n_tiles + tile0[bins - 1];
-        scan[0] = n_chunks + chunk0[bins - 1];
-        P.n_tables[0] = total[bins];
-        P.n_tables[1] = scan[0];
+    const int32_t n_tiles = tile0[bins - 1] + last_tiles;
+    int32_t n_chunks = 0;
+    if (P.chunk) {
+        block_scan(chunk0, bins, scan);
+        block_scan(slot0, bins, scan);
+        n_chunks = chunk0[bins - 1];
     }
-    __syncthreads();
-    for (int32_t i = threadIdx.x; i < total[bins]; i += 256) {
+    if (threadIdx.x == 0) {
+        P.n_tables[0] = n_tiles;
+        P.n_tables[1] = n_chunks;
+    }
+    for (int32_t i = threadIdx.x; i < n_tiles; i += kPlanThreads) {
         const int b = find_bin(tile0, bins, i);
         const int32_t at = (i - tile0[b]) * P.tile;
         P.tiles[i] = make_int4(b < P.n ? b : -1, start[b] + at, min(total[b] - at, P.tile), 0);
     }
     if (!P.chunk) return;
-    for (int32_t i = threadIdx.x; i < scan[0]; i += 256) {
+    for (int32_t i = threadIdx.x; i < n_chunks; i += kPlanThreads) {
         const int b = find_bin(chunk0, bins, i);
         const int32_t k = i - chunk0[b], at = k * P.chunk;
         P.chunks[i] = make_int4(b, start[b] + at, min(total[b] - at, P.chunk), total[b] > P.chunk ? slot0[b] + k : -1);
     }
-    for (int i = threadIdx.x; i < P.n; i += 256)
+    for (int i = threadIdx.x; i < P.n; i += kPlanThreads)
         P.info[i] = make_int2((total[i] + P.chunk - 1) / P.chunk, slot0[i]);
 }
 
@@ -481,12 +506,13 @@ __global__ void __launch_bounds__(256) adapter_join_kernel(AdapterGrad P) {
 // The row tile for a rank: RB * MB * 8 KiB of LDS join the wavefronts' sums.
 int adapter_tile(int32_t R) { return R <= 64 ? 32 : 16; }
 
-// A workgroup of the plan places 1024 rows, and more where that would take more
-// than 256 workgroups: each of them counts all rows.
+// A workgroup of the plan places 1024 rows, or as many as keep their number to
+// 256: each of them counts all rows.
 hipError_t launch_adapter_plan(AdapterPlan P, hipStream_t stream) {
-    P.rows = std::max<int64_t>(1024, (P.M + 65535) / 65536 * 256);
-    const int64_t blocks = std::max<int64_t>(1, (P.M + P.rows - 1) / P.rows);
-    hipLaunchKernelGGL(adapter_plan_kernel, dim3((unsigned)blocks), dim3(256), 0, stream, P);
+    P.rows = std::max<int64_t>(1, (P.M + 256 * kPlanThreads - 1) / (256 * kPlanThreads)) * kPlanThreads;
+    P.vec = (uintptr_t)P.ids % 16 == 0;
+    const int64_t blocks = (P.M + P.rows - 1) / P.rows + 1;
+    hipLaunchKernelGGL(adapter_plan_kernel, dim3((unsigned)blocks), dim3(kPlanThreads), 0, stream, P);
     return hipGetLastError();
 }
 

@@ -163,7 +163,9 @@ hipError_t launch_balance(const BalanceParams& P, bool bf16, hipStream_t stream)
 constexpr int kMaxRank = 128;
 struct AdapterPlan {  // rows grouped by adapter
     const int32_t* ids;  // [M]
-    int64_t M, rows;     // rows per workgroup; set by the launcher
+    int64_t M;
+    int64_t rows;        // rows per workgroup, and whether ids allow four-element loads; set by the launcher
+    bool vec;
     int32_t n, tile;
     int32_t chunk;       // rows of a chunk of the gradients, 0: forward
     bool rest;           // tiles for the rows without an adapter too
