@@ -7,6 +7,7 @@
 // operation with B^T and A^T in the places of A and B, so one kernel serves
 // both, on transposed copies of the adapters.
 #include <algorithm>
+#include <type_traits>
 
 #include "nvfp4_device.h"
 #include "nvfp4_kernels.h"
@@ -25,6 +26,9 @@ constexpr int kBins = kMaxExperts + 1;  // adapters, and the rows without one
 __device__ __forceinline__ f32x4 mfma16(u32x4 a, u32x4 b, f32x4 c) {
     return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, a), __builtin_bit_cast(bf16x8, b), c, 0, 0, 0);
 }
+// Keeps the loads before it ahead of what follows (the scheduler would move
+// them down to where their values are needed, to save registers).
+__device__ __forceinline__ void issue() { __builtin_amdgcn_sched_barrier(0); }
 __device__ __forceinline__ u32x4 load16(const uint16_t* p) { return *reinterpret_cast<const u32x4*>(p); }
 
 // v as the sum of BF16 values of falling size, each the rounding of what the
@@ -34,6 +38,15 @@ __device__ __forceinline__ uint32_t bf16_piece(float& rest) {
     const float r = rest - bf16_to_f32(b);
     rest = fabsf(r) < __builtin_inff() ? r : 0.0f;
     return b;
+}
+
+// Element c (of 8) of each of 8 rows.
+__device__ __forceinline__ u32x4 column8(const u32x4 (&z)[8], int c) {
+    u32x4 f;
+#pragma unroll
+    for (int e = 0; e < 4; e++)
+        f[e] = __builtin_amdgcn_perm(z[2 * e + 1][c / 2], z[2 * e][c / 2], (c & 1) ? 0x07060302u : 0x05040100u);
+    return f;
 }
 
 // Sum over the workgroup's earlier entries of a[0..n), in place; every thread calls it.
@@ -101,7 +114,7 @@ __global__ void __launch_bounds__(kPlanThreads) adapter_plan_kernel(AdapterPlan 
     constexpr int kWaves = kPlanThreads / 64, kAhead = 4;
     __shared__ int32_t total[kBins + 1], start[kBins + 1], before[kBins], scan[kWaves];
     __shared__ uint16_t counts[kWaves][kBins];
-    __shared__ int32_t tile0[kBins], chunk0[kBins], slot0[kBins];
+    __shared__ int32_t tile0[kBins], chunk0[kBins], slot0[kBins];  // (a tile is a step of the gradients)
     const int bins = P.n + 1, wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
     const bool tables = blockIdx.x == gridDim.x - 1;
     const int64_t first = tables ? 0 : (int64_t)blockIdx.x * P.rows;  // a multiple of 256: a wavefront's rows lie on one side
@@ -197,189 +210,346 @@ __global__ void __launch_bounds__(kPlanThreads) adapter_plan_kernel(AdapterPlan 
     for (int32_t i = threadIdx.x; i < n_tiles; i += kPlanThreads) {
         const int b = find_bin(tile0, bins, i);
         const int32_t at = (i - tile0[b]) * P.tile;
-        P.tiles[i] = make_int4(b < P.n ? b : -1, start[b] + at, min(total[b] - at, P.tile), 0);
+        P.tiles[i] = make_int4(b < P.n ? b : -1, start[b] + at, min(total[b] - at, P.tile), i);
     }
     if (!P.chunk) return;
     for (int32_t i = threadIdx.x; i < n_chunks; i += kPlanThreads) {
         const int b = find_bin(chunk0, bins, i);
         const int32_t k = i - chunk0[b], at = k * P.chunk;
         P.chunks[i] = make_int4(b, start[b] + at, min(total[b] - at, P.chunk), total[b] > P.chunk ? slot0[b] + k : -1);
+        P.chunk_step[i] = tile0[b] + at / P.tile;
     }
     for (int i = threadIdx.x; i < P.n; i += kPlanThreads)
         P.info[i] = make_int2((total[i] + P.chunk - 1) / P.chunk, slot0[i]);
 }
 
 // One workgroup: up to 16 MB rows of one adapter, and a share of the columns.
+//
 // The first product V = A x^T over K is split over the wavefronts (chunks of
 // 64 columns in turn) and joined in LDS in one fixed order, whatever the tile:
 // a row's bits do not depend on the rows beside it.  V, an FP32 sum, is passed
 // on as two BF16 values (2^-16 of it may be lost, against the 2^-8 of the output's
 // one rounding): 32 of the second product's inputs are then 16 ranks twice,
 // which costs no instruction at rank 16.
+//
+// A matrix operand has its rows on neighbouring lanes; read like that, memory
+// gives 16 bytes of 16 lines at a time.  So each wavefront reads its operands
+// in whole lines and turns them over in a piece of LDS of its own (16-byte
+// units, exclusive-ored with the row so that operand reads meet no bank twice),
+// the loads two steps ahead in registers; base and out are accessed in runs of
+// 16 lanes a row, with the second product's columns dealt out so that a lane
+// holds neighbouring ones.
+//
 // RB: ranks in blocks of 16; MB: rows in blocks of 16.
-template <int RB, int MB>
-__global__ void __launch_bounds__(kAdWaves * 64) adapter_kernel(AdapterParams P) {
-    constexpr int kR = 16 * RB, kPitch = 2 * kR + 8;
-    __shared__ __attribute__((aligned(16))) f32x4 red[kAdWaves][RB * MB][64];
+// kGrad: V and the forward's v also go, as three BF16 values, to the operands
+// of the weights' gradients.
+template <int RB, int MB, bool kGrad, bool kBase>
+__global__ void __launch_bounds__(kAdWaves * 64, 2) adapter_kernel(AdapterParams P) {
+    constexpr int kR = 16 * RB, kPieces = kGrad ? 3 : 2, kPitch = kPieces * kR + 8;
+    constexpr int kRound = RB * MB < 8 ? RB * MB : 8;  // blocks of V joined at a time
+    constexpr int kA = RB < 4 ? RB : 4;                // rank blocks turned over at a time
+    constexpr int kAhead = RB < 8 ? 2 : 1;             // steps of the first product whose loads are in registers
+    constexpr int NB = RB < 4 ? 8 : 4, kCols = 16 * NB;  // neighbouring columns of a lane; columns of a step
+    constexpr int kB = (RB + 1) / 2, kBLoads = NB * RB / 2;  // operands a column; 16-byte loads of B a lane and step
+    constexpr int kUnits1 = (MB + kA) * 128, kUnits2 = kBLoads * 64, kUnits = kUnits1 > kUnits2 ? kUnits1 : kUnits2;
+    constexpr int kRed = kRound * kAdWaves * 64;
+    // Units of 16 bytes: the wavefronts' pieces, and in between their sums.
+    __shared__ __attribute__((aligned(16))) u32x4 lds[kAdWaves * kUnits > kRed ? kAdWaves * kUnits : kRed];
     __shared__ __attribute__((aligned(16))) uint16_t vs[16 * MB][kPitch];
-    __shared__ int32_t rows[16 * MB];
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, i = lane & 15, q = lane >> 4;
-    const int32_t tile = blockIdx.x / P.slabs, slab = blockIdx.x % P.slabs;
-    if (tile >= *P.n_tiles) return;
-    const int4 t = P.tiles[tile];
+    const int lane = threadIdx.x & 63, i = lane & 15, q = lane >> 4;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    u32x4* own = lds + wave * kUnits;
+    // Consecutive tiles, which mostly share an adapter, on one XCD.
+    const uint32_t items = (uint32_t)*P.n_tiles * P.slabs, per = (items + 7) / 8, item = (blockIdx.x & 7) * per + (blockIdx.x >> 3);
+    if ((blockIdx.x >> 3) >= per || item >= items) return;
+    const int32_t slab = item % P.slabs;
+    const int4 t = P.tiles[item / P.slabs];
     const int a = t.x, count = t.z;
-    if (threadIdx.x < 16 * MB) rows[threadIdx.x] = P.order[t.y + min((int)threadIdx.x, count - 1)];
-    __syncthreads();
+    // Rows past `count` repeat the last one: its values, stored again.
+    auto row_of = [&](int m) { return (int64_t)P.order[t.y + min(m, count - 1)]; };
     if (a < 0) {  // rows without an adapter
         const int pieces = P.N / 8;
         for (int64_t k = slab * (kAdWaves * 64) + threadIdx.x; k < (int64_t)count * pieces; k += P.slabs * (kAdWaves * 64)) {
-            const int64_t r = rows[k / pieces], c = k % pieces * 8;
+            const int64_t r = row_of(k / pieces), c = k % pieces * 8;
             const u32x4 z = {0, 0, 0, 0};
-            *reinterpret_cast<u32x4*>(P.out + r * P.ld_out + c) = P.base ? load16(P.base + r * P.ld_base + c) : z;
+            *reinterpret_cast<u32x4*>(P.out + r * P.ld_out + c) = kBase ? load16(P.base + r * P.ld_base + c) : z;
         }
-        if (P.v && slab == 0)
-            for (int k = threadIdx.x; k < count * P.R; k += kAdWaves * 64) P.v[(int64_t)rows[k / P.R] * P.R + k % P.R] = 0.0f;
+        if (!kGrad && P.v && slab == 0)
+            for (int k = threadIdx.x; k < count * P.R; k += kAdWaves * 64) P.v[row_of(k / P.R) * P.R + k % P.R] = 0.0f;
         return;
     }
-    int64_t row[MB];
-#pragma unroll
-    for (int m = 0; m < MB; m++) row[m] = rows[16 * m + i];
 
+    // The first product: 64 columns a step, of 8 rows a load.  (Ranks past R
+    // take other ones' values, which the join makes zeros.)
+    const int sub = lane >> 3, piece = lane & 7;  // row in a load, unit in a row
+    const uint16_t* xr[2 * MB];
+#pragma unroll
+    for (int k = 0; k < 2 * MB; k++) xr[k] = P.x + row_of(8 * k + sub) * P.ldx + 8 * piece;
+    const uint16_t* ar = P.A + ((int64_t)a * P.R + sub) * P.K + 8 * piece;
+    u32x4 xf[kAhead][2 * MB], af[kAhead][2 * RB];
     f32x4 acc[RB][MB];
 #pragma unroll
     for (int r = 0; r < RB; r++)
 #pragma unroll
         for (int m = 0; m < MB; m++) acc[r][m] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-    const uint16_t* A = P.A + (int64_t)a * P.R * P.K;
-    for (int k0 = wave * 64; k0 < P.K; k0 += kAdWaves * 64) {
+    auto load1 = [&](int s, int c) {
 #pragma unroll
-        for (int h = 0; h < 2; h++) {
-            const int k = k0 + 32 * h + 8 * q;
-            u32x4 af[RB], xf[MB];
+        for (int k = 0; k < 2 * MB; k++) xf[s][k] = load16(xr[k] + c * 64);
 #pragma unroll
-            for (int m = 0; m < MB; m++) xf[m] = u32x4{0, 0, 0, 0};
+        for (int k = 0; k < 2 * RB; k++) af[s][k] = load16(ar + (int64_t)min(8 * k, P.R - 8) * P.K + c * 64);
+        issue();
+    };
+    auto mul1 = [&](int s, auto next) {
+        u32x4* put = own + sub * 8 + (piece ^ sub);
 #pragma unroll
-            for (int r = 0; r < RB; r++) af[r] = u32x4{0, 0, 0, 0};
-            if (k < P.K) {
+        for (int k = 0; k < 2 * MB; k++) put[64 * k] = xf[s][k];
 #pragma unroll
-                for (int m = 0; m < MB; m++) xf[m] = load16(P.x + row[m] * P.ldx + k);
+        for (int r0 = 0; r0 < RB; r0 += kA) {
 #pragma unroll
-                for (int r = 0; r < RB; r++)
-                    if (16 * r + i < P.R) af[r] = load16(A + (int64_t)(16 * r + i) * P.K + k);
+            for (int k = 0; k < 2 * kA; k++) put[64 * (2 * MB + k)] = af[s][2 * r0 + k];
+            if (r0 + kA == RB) {
+                issue();
+                next();
             }
 #pragma unroll
-            for (int r = 0; r < RB; r++)
+            for (int h = 0; h < 2; h++) {
+                const u32x4* at = own + i * 8 + ((4 * h + q) ^ (i & 7));
+                u32x4 x[MB];
 #pragma unroll
-                for (int m = 0; m < MB; m++) acc[r][m] = mfma16(af[r], xf[m], acc[r][m]);
+                for (int m = 0; m < MB; m++) x[m] = at[128 * m];
+#pragma unroll
+                for (int r = 0; r < kA; r++) {
+                    const u32x4 w = at[128 * (MB + r)];
+#pragma unroll
+                    for (int m = 0; m < MB; m++) acc[r0 + r][m] = mfma16(w, x[m], acc[r0 + r][m]);
+                }
+            }
+        }
+    };
+    auto nothing = [] {};
+    {
+        const int whole = P.K / 64;
+        int c = wave;
+        if constexpr (kAhead == 2) {
+            if (c < whole) load1(0, c);
+            if (c + kAdWaves < whole) {
+                load1(1, c + kAdWaves);
+                for (; c + 3 * kAdWaves < whole; c += 2 * kAdWaves) {
+                    mul1(0, [&] { load1(0, c + 2 * kAdWaves); });
+                    mul1(1, [&] { load1(1, c + 3 * kAdWaves); });
+                }
+                if (c + 2 * kAdWaves < whole) {
+                    mul1(0, [&] { load1(0, c + 2 * kAdWaves); });
+                    mul1(1, nothing);
+                    mul1(0, nothing);
+                    c += 3 * kAdWaves;
+                } else {
+                    mul1(0, nothing);
+                    mul1(1, nothing);
+                    c += 2 * kAdWaves;
+                }
+            } else if (c < whole) {
+                mul1(0, nothing);
+                c += kAdWaves;
+            }
+        } else if (c < whole) {
+            load1(0, c);
+            for (; c + kAdWaves < whole; c += kAdWaves) mul1(0, [&] { load1(0, c + kAdWaves); });
+            mul1(0, nothing);
+            c += kAdWaves;
+        }
+        if (c == whole && c * 64 < P.K) {  // the rest of K
+            const bool in = c * 64 + 8 * piece < P.K;
+            const int k0 = in ? c * 64 : -8 * piece;  // (the row's start)
+            const u32x4 z = {0, 0, 0, 0};
+#pragma unroll
+            for (int k = 0; k < 2 * MB; k++) {
+                xf[0][k] = load16(xr[k] + k0);
+                if (!in) xf[0][k] = z;
+            }
+#pragma unroll
+            for (int k = 0; k < 2 * RB; k++) {
+                af[0][k] = load16(ar + (int64_t)min(8 * k, P.R - 8) * P.K + k0);
+                if (!in) af[0][k] = z;
+            }
+            mul1(0, nothing);
         }
     }
-#pragma unroll
-    for (int r = 0; r < RB; r++)
-#pragma unroll
-        for (int m = 0; m < MB; m++) red[wave][r * MB + m][lane] = acc[r][m];
-    __syncthreads();
-    for (int j = wave; j < RB * MB; j += kAdWaves) {
-        const int m = j % MB, r = j / MB * 16 + 4 * q;  // the lane's ranks r .. r + 3 of row i
-        f32x4 s = red[0][j][lane];
-#pragma unroll
-        for (int w = 1; w < kAdWaves; w++) s += red[w][j][lane];
-        if (r >= P.R) s = f32x4{0.0f, 0.0f, 0.0f, 0.0f};  // (0 times an infinite x)
-        if (P.v && slab == 0 && r < P.R && 16 * m + i < count)
-            *reinterpret_cast<f32x4*>(P.v + (int64_t)rows[16 * m + i] * P.R + r) = s;
-        const float scale = P.scale ? P.scale[a] : 1.0f;
-        uint32_t hi[4], lo[4];
-#pragma unroll
-        for (int e = 0; e < 4; e++) {
-            float v = s[e] * scale;
-            hi[e] = bf16_piece(v);
-            lo[e] = bf16_hw(v);
-        }
-        *reinterpret_cast<u32x2*>(&vs[16 * m + i][r]) = u32x2{hi[0] | (hi[1] << 16), hi[2] | (hi[3] << 16)};
-        *reinterpret_cast<u32x2*>(&vs[16 * m + i][kR + r]) = u32x2{lo[0] | (lo[1] << 16), lo[2] | (lo[3] << 16)};
-    }
-    __syncthreads();
 
-    // The second product: 64 columns a step.  Row n of its first operand is
-    // column c0 + 16 (n / 4) + 4 b + n % 4, so that the four products b leave
-    // the lane 16 consecutive columns of its row.
+    // The second product, kCols columns a step: lane i has columns NB i .. + NB - 1
+    // of rows 4 q .. + 3 of each block; product b takes columns NB n + b.
+    typedef uint32_t vec __attribute__((ext_vector_type(NB / 2)));
+    uint32_t out_row[MB][4];
+#pragma unroll
+    for (int m = 0; m < MB; m++)
+#pragma unroll
+        for (int e = 0; e < 4; e++) out_row[m][e] = (uint32_t)row_of(16 * m + 4 * q + e);
+    const uint16_t* B = P.B + (int64_t)a * P.N * P.R;
+    const int units_b = kCols * P.R / 8;  // of B in a step: consecutive
+    vec old[MB][4];
+    u32x4 bf[kBLoads];
+    auto load2 = [&](int n0, int units) {  // `units` of B, at most units_b, and columns from n0 on exist
+        if (kBase) {
+            const int n = min(n0 + NB * i, P.N - NB);
+#pragma unroll
+            for (int m = 0; m < MB; m++)
+#pragma unroll
+                for (int e = 0; e < 4; e++) old[m][e] = *reinterpret_cast<const vec*>(P.base + out_row[m][e] * P.ld_base + n);
+        }
+#pragma unroll
+        for (int k = 0; k < kBLoads; k++) bf[k] = load16(B + (int64_t)n0 * P.R + min(64 * k + lane, units - 1) * 8);
+        issue();
+    };
+    const int c_step = P.slabs * kAdWaves * kCols;
+    int n0 = (slab * kAdWaves + wave) * kCols;
+    if (n0 < P.N) load2(n0, min(units_b, (P.N - n0) * (P.R / 8)));
+
+    const float scale = P.scale ? P.scale[a] : 1.0f;
+    f32x4* red = reinterpret_cast<f32x4*>(lds);
+#pragma unroll
+    for (int j0 = 0; j0 < RB * MB; j0 += kRound) {
+        __syncthreads();
+#pragma unroll
+        for (int r = 0; r < RB; r++)
+#pragma unroll
+            for (int m = 0; m < MB; m++)
+                if (r * MB + m >= j0 && r * MB + m < j0 + kRound) red[(wave * kRound + r * MB + m - j0) * 64 + lane] = acc[r][m];
+        __syncthreads();
+        if (wave < kRound) {
+            const int j = j0 + wave, m = j % MB, r = j / MB * 16 + 4 * q;  // the lane's ranks r .. r + 3 of row i
+            f32x4 s = red[wave * 64 + lane];
+#pragma unroll
+            for (int w = 1; w < kAdWaves; w++) s += red[(w * kRound + wave) * 64 + lane];
+            if (r >= P.R) s = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+            if (!kGrad && P.v && slab == 0 && r < P.R && 16 * m + i < count)
+                *reinterpret_cast<f32x4*>(P.v + row_of(16 * m + i) * P.R + r) = s;
+            uint32_t part[kPieces][4];
+#pragma unroll
+            for (int e = 0; e < 4; e++) {
+                float v = s[e] * scale;
+#pragma unroll
+                for (int p = 0; p < kPieces; p++) part[p][e] = bf16_piece(v);
+            }
+#pragma unroll
+            for (int p = 0; p < kPieces; p++)
+                *reinterpret_cast<u32x2*>(&vs[16 * m + i][p * kR + r]) =
+                    u32x2{part[p][0] | (part[p][1] << 16), part[p][2] | (part[p][3] << 16)};
+        }
+    }
+    __syncthreads();
+    if constexpr (kGrad) {
+        // Operands of the weights' gradients (adapter_wgrad_kernel): lane l of
+        // block (rank block, piece) holds rank l % 16 of rows 8 (l / 16) .. + 7.
+        if (slab == 0) {
+            const int64_t at = (int64_t)t.w * (RB * 3 * 64);
+            for (int k = threadIdx.x; k < RB * 64; k += kAdWaves * 64) {
+                const int rb = k / 64, l = k % 64, rank = rb * 16 + (l & 15), m0 = (l >> 4) * 8;
+                u32x4 w[3], v[3];
+#pragma unroll
+                for (int e = 0; e < 4; e++) {
+                    float f[2];
+                    uint32_t keep = 0;  // (rows past `count` count nothing)
+#pragma unroll
+                    for (int o = 0; o < 2; o++) {
+                        const int m = m0 + 2 * e + o;
+                        f[o] = 0.0f;
+                        if (m < count && rank < P.R) f[o] = P.v_in[row_of(m) * P.R + rank];
+                        if (m < count) keep |= 0xFFFFu << (16 * o);
+                    }
+#pragma unroll
+                    for (int p = 0; p < 3; p++) {
+                        w[p][e] = (vs[m0 + 2 * e][p * kR + rank] | ((uint32_t)vs[m0 + 2 * e + 1][p * kR + rank] << 16)) & keep;
+                        const uint32_t lo = bf16_piece(f[0]);
+                        v[p][e] = lo | (bf16_piece(f[1]) << 16);
+                    }
+                }
+#pragma unroll
+                for (int p = 0; p < 3; p++) {
+                    P.w_pack[at + (rb * 3 + p) * 64 + l] = w[p];
+                    P.v_pack[at + (rb * 3 + p) * 64 + l] = v[p];
+                }
+            }
+        }
+    }
+
     u32x4 vf[MB][RB];
 #pragma unroll
     for (int m = 0; m < MB; m++)
 #pragma unroll
         for (int j = 0; j < RB; j++) vf[m][j] = *reinterpret_cast<const u32x4*>(&vs[16 * m + i][32 * j + 8 * q]);
-    const uint16_t* B = P.B + (int64_t)a * P.N * P.R;
-    for (int c0 = (slab * kAdWaves + wave) * 64; c0 < P.N; c0 += P.slabs * kAdWaves * 64) {
-        const int n0 = c0 + 16 * q;
-        u32x4 old[MB][2];
+    // Unit p of B's piece lies at p ^ ((p / 16) ^ (p / 64)) % 16: reads of one
+    // product are 16 NB rows apart, and these differ in that term.
+    const int r8 = P.R / 8;
+    auto step2 = [&](int n0, auto whole) {
+#pragma unroll
+        for (int k = 0; k < kBLoads; k++) own[64 * k + (lane ^ (lane >> 4) ^ ((4 * k ^ k) & 15))] = bf[k];
+        vec keep[MB][4];
 #pragma unroll
         for (int m = 0; m < MB; m++)
 #pragma unroll
-            for (int h = 0; h < 2; h++) {
-                old[m][h] = u32x4{0, 0, 0, 0};
-                if (P.base && n0 + 8 * h < P.N && 16 * m + i < count) old[m][h] = load16(P.base + row[m] * P.ld_base + n0 + 8 * h);
+            for (int e = 0; e < 4; e++) keep[m][e] = old[m][e];
+        const int next = n0 + c_step;
+        issue();
+        if (next < P.N) load2(next, min(units_b, (P.N - next) * r8));
+        f32x4 y[MB][NB];
+#pragma unroll
+        for (int b = 0; b < NB; b++) {
+#pragma unroll
+            for (int m = 0; m < MB; m++) y[m][b] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+            u32x4 w[kB];
+#pragma unroll
+            for (int j = 0; j < kB; j++) {
+                const int p = (NB * i + b) * r8 + min(RB == 1 ? q & 1 : 4 * j + q, r8 - 1);
+                w[j] = own[p ^ (((p >> 4) ^ (p >> 6)) & 15)];
             }
-        f32x4 y[MB][4];
 #pragma unroll
-        for (int b = 0; b < 4; b++) {
-            const int n = min(c0 + 16 * (i >> 2) + 4 * b + (i & 3), P.N - 1);
-            u32x4 bf[(RB + 1) / 2];
+            for (int j = RB - 1; j >= 0; j--)
 #pragma unroll
-            for (int j = 0; j < (RB + 1) / 2; j++) {
-                const int r = RB == 1 ? 8 * (q & 1) : 32 * j + 8 * q;
-                bf[j] = u32x4{0, 0, 0, 0};
-                if (r < P.R) bf[j] = load16(B + (int64_t)n * P.R + r);
-            }
-#pragma unroll
-            for (int m = 0; m < MB; m++) {
-                y[m][b] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll
-                for (int j = RB - 1; j >= 0; j--) y[m][b] = mfma16(bf[RB == 1 ? 0 : j % (RB / 2 > 0 ? RB / 2 : 1)], vf[m][j], y[m][b]);
-            }
+                for (int m = 0; m < MB; m++) y[m][b] = mfma16(vf[m][j], w[j % kB], y[m][b]);
         }
+        const int n = n0 + NB * i;
+        if (!whole.value && n >= P.N) return;
 #pragma unroll
-        for (int m = 0; m < MB; m++) {
-            if (16 * m + i >= count) continue;
+        for (int m = 0; m < MB; m++)
 #pragma unroll
-            for (int h = 0; h < 2; h++) {
-                if (n0 + 8 * h >= P.N) continue;
-                u32x4 o;
+            for (int e = 0; e < 4; e++) {
+                vec o;
 #pragma unroll
-                for (int e = 0; e < 4; e++) {
-                    const f32x4 d = y[m][2 * h + e / 2];
-                    const float lo = d[2 * (e & 1)] + __uint_as_float(old[m][h][e] << 16);
-                    const float hi = d[2 * (e & 1) + 1] + __uint_as_float(old[m][h][e] & 0xFFFF0000u);
-                    o[e] = bf16_hw(lo) | (bf16_hw(hi) << 16);
+                for (int k = 0; k < NB / 2; k++) {
+                    float lo = y[m][2 * k][e], hi = y[m][2 * k + 1][e];
+                    if (kBase) {
+                        lo += __uint_as_float(keep[m][e][k] << 16);
+                        hi += __uint_as_float(keep[m][e][k] & 0xFFFF0000u);
+                    }
+                    o[k] = bf16_hw(lo) | (bf16_hw(hi) << 16);
                 }
-                *reinterpret_cast<u32x4*>(P.out + row[m] * P.ld_out + n0 + 8 * h) = o;
+                *reinterpret_cast<vec*>(P.out + out_row[m][e] * P.ld_out + n) = o;
             }
-        }
-    }
+    };
+    for (; n0 + kCols <= P.N; n0 += c_step) step2(n0, std::true_type{});
+    if (n0 < P.N) step2(n0, std::false_type{});
 }
 
-// The adapters that have rows, transposed: At [n][K][R] and Bt [n][R][N].
+// The adapters that have rows, transposed: At [n][K][R] and Bt [n][R][N].  A
+// thread turns 8 x 8 elements over in registers, one byte permutation each two.
 __global__ void __launch_bounds__(256) adapter_transpose_kernel(AdapterGrad P) {
-    __shared__ uint16_t tile[64][66];
-    const int a = blockIdx.y, k_tiles = (P.K + 63) / 64;
+    const int a = blockIdx.y;
     if (P.info[a].x == 0) return;
-    const bool is_a = (int)blockIdx.x < k_tiles;
-    const int c0 = ((int)blockIdx.x - (is_a ? 0 : k_tiles)) * 64;
-    // in [rows_in][cols_in] -> out [cols_in][rows_in]
-    const int64_t rows_in = is_a ? P.R : P.N, cols_in = is_a ? P.K : P.R;
-    const uint16_t* in = (is_a ? P.A : P.B) + (int64_t)a * rows_in * cols_in;
-    uint16_t* out = (is_a ? P.At : P.Bt) + (int64_t)a * rows_in * cols_in;
-    for (int r0 = 0; r0 < P.R; r0 += 64) {
-        const int64_t row0 = is_a ? r0 : c0, col0 = is_a ? c0 : r0;
-        for (int k = threadIdx.x; k < 64 * 64; k += 256) {
-            const int64_t r = row0 + k / 64, c = col0 + k % 64;
-            if (r < rows_in && c < cols_in) tile[k / 64][k % 64] = in[r * cols_in + c];
-        }
-        __syncthreads();
-        for (int k = threadIdx.x; k < 64 * 64; k += 256) {
-            const int64_t c = col0 + k / 64, r = row0 + k % 64;
-            if (r < rows_in && c < cols_in) out[c * rows_in + r] = tile[k % 64][k / 64];
-        }
-        __syncthreads();
-    }
+    const uint32_t rb = (uint32_t)P.R / 8, of_a = rb * (P.K / 8), of_b = rb * (P.N / 8);
+    uint32_t k = blockIdx.x * 256 + threadIdx.x;
+    const bool is_a = k < of_a;
+    if (!is_a) k -= of_a;
+    if (!is_a && k >= of_b) return;
+    // in [rows][cols] -> out [cols][rows]; neighbouring lanes along in's columns
+    const int64_t rows = is_a ? P.R : P.N, cols = is_a ? P.K : P.R;
+    const int64_t r0 = k / (cols / 8) * 8, c0 = k % (cols / 8) * 8;
+    const uint16_t* in = (is_a ? P.A : P.B) + a * rows * cols + r0 * cols + c0;
+    uint16_t* out = (is_a ? P.At : P.Bt) + a * rows * cols + c0 * rows + r0;
+    u32x4 z[8];
+#pragma unroll
+    for (int j = 0; j < 8; j++) z[j] = load16(in + j * cols);
+#pragma unroll
+    for (int c = 0; c < 8; c++) *reinterpret_cast<u32x4*>(out + c * rows) = column8(z, c);
 }
 
 // dA and dB of one row chunk and 128 columns: the sum over rows is the matrix
@@ -387,67 +557,74 @@ __global__ void __launch_bounds__(256) adapter_transpose_kernel(AdapterGrad P) {
 // turn.  A lane loads 8 columns of 8 rows; one byte permutation a register
 // turns them into operands with 8 rows of one column each, for eight products
 // whose columns lie 8 apart.  w and v are FP32 sums and go in as three BF16
-// values, which is all of their 24 bits.
+// values, which is all of their 24 bits, laid out as operands by adapter_kernel
+// (zeros behind the chunk's last row, where x and dy repeat it).
 // RB: ranks in blocks of 16 (blockIdx.z takes further ones).
 template <int RB>
-__global__ void __launch_bounds__(256) adapter_wgrad_kernel(AdapterGrad P) {
+__global__ void __launch_bounds__(256, 2) adapter_wgrad_kernel(AdapterGrad P) {
+    constexpr int kAhead = RB < 2 ? RB : 2;  // rank blocks whose w is in registers
     __shared__ __attribute__((aligned(16))) float red[4][16][132];
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, i = lane & 15, q = lane >> 4;
+    const int lane = threadIdx.x & 63, i = lane & 15, q = lane >> 4;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     if ((int)blockIdx.y >= P.n_tables[1]) return;
     const int4 t = P.chunks[blockIdx.y];
     const int a = t.x, count = t.z, k_slabs = (P.K + 127) / 128;
     const bool is_a = (int)blockIdx.x < k_slabs;
-    const int C = is_a ? P.K : P.N, c0 = ((int)blockIdx.x - (is_a ? 0 : k_slabs)) * 128, rank0 = blockIdx.z * 16 * RB;
-    const uint16_t* Z = is_a ? P.x : P.dy;
+    const int C = is_a ? P.K : P.N, c0 = ((int)blockIdx.x - (is_a ? 0 : k_slabs)) * 128, block0 = blockIdx.z * RB;
     const int64_t ldz = is_a ? P.ldx : P.ld_dy;
-    const float* W = is_a ? P.w : P.v;
+    const uint16_t* Z = (is_a ? P.x : P.dy) + min(c0 + 8 * i, C - 8);
+    const u32x4* W = (is_a ? P.w_pack : P.v_pack) + ((int64_t)P.chunk_step[blockIdx.y] * P.rank_blocks + block0) * 192 + lane;
+    const int32_t* order = P.order + t.y;
     f32x4 acc[8][RB];
 #pragma unroll
     for (int c = 0; c < 8; c++)
 #pragma unroll
         for (int r = 0; r < RB; r++) acc[c][r] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-    const int col = c0 + 8 * i;
-    for (int s = wave * 32; s < count; s += 128) {
-        u32x4 z[8];
-        float w[RB][8];
+    u32x4 z[8], w[kAhead][3];
+    auto load_rows = [&](int s) { return order[min(s + (lane & 31), count - 1)]; };
+    auto load_z = [&](int32_t rows) {
 #pragma unroll
-        for (int j = 0; j < 8; j++) {
-            const int at = s + 8 * q + j;
-            const bool live = at < count;
-            const int64_t r = P.order[t.y + min(at, count - 1)];
-            z[j] = u32x4{0, 0, 0, 0};
-            if (live && col < C) z[j] = load16(Z + r * ldz + col);
+        for (int j = 0; j < 8; j++) z[j] = load16(Z + (int64_t)__shfl(rows, 8 * q + j, kWave) * ldz);
+    };
+    auto load_w = [&](int b, int s) {
+        const u32x4* at = W + ((int64_t)(s / 32) * P.rank_blocks + b) * 192;
 #pragma unroll
-            for (int b = 0; b < RB; b++) {
-                const int rank = rank0 + 16 * b + i;
-                w[b][j] = 0.0f;
-                if (live && rank < P.R) w[b][j] = W[r * P.R + rank];
-            }
+        for (int p = 0; p < 3; p++) w[b % kAhead][p] = at[64 * p];
+    };
+    // One step; `more`: the wavefront's next step, 128 rows on, is loaded meanwhile.
+    int32_t rows = 0;
+    auto step = [&](int s, auto more) {
+        u32x4 zf[8];
+#pragma unroll
+        for (int c = 0; c < 8; c++) zf[c] = column8(z, c);
+        if constexpr (more.value) {
+            load_z(rows);
+            rows = load_rows(s + 256);
+            issue();
         }
-        u32x4 wf[RB][3];
 #pragma unroll
-        for (int b = 0; b < RB; b++)
+        for (int b = 0; b < RB; b++) {
 #pragma unroll
-            for (int p = 0; p < 3; p++)
+            for (int c = 0; c < 8; c++)
 #pragma unroll
-                for (int e = 0; e < 4; e++) {
-                    const uint32_t lo = bf16_piece(w[b][2 * e]);
-                    wf[b][p][e] = lo | (bf16_piece(w[b][2 * e + 1]) << 16);
-                }
-#pragma unroll
-        for (int c = 0; c < 8; c++) {
-            u32x4 zf;
-#pragma unroll
-            for (int e = 0; e < 4; e++)
-                zf[e] = __builtin_amdgcn_perm(z[2 * e + 1][c / 2], z[2 * e][c / 2], (c & 1) ? 0x07060302u : 0x05040100u);
-#pragma unroll
-            for (int b = 0; b < RB; b++)
-#pragma unroll
-                for (int p = 2; p >= 0; p--) acc[c][b] = mfma16(wf[b][p], zf, acc[c][b]);
+                for (int p = 2; p >= 0; p--) acc[c][b] = mfma16(w[b % kAhead][p], zf[c], acc[c][b]);
+            if (b + kAhead < RB)
+                load_w(b + kAhead, s);
+            else if constexpr (more.value)
+                load_w(b + kAhead - RB, s + 128);
         }
+    };
+    int s = wave * 32;
+    if (s < count) {
+        load_z(load_rows(s));
+#pragma unroll
+        for (int b = 0; b < kAhead; b++) load_w(b, s);
+        rows = load_rows(s + 128);
+        for (; s + 128 < count; s += 128) step(s, std::true_type{});
+        step(s, std::false_type{});
     }
-    // The wavefronts' sums, added in one order.
-    const float scale = P.scale ? P.scale[a] : 1.0f;
+    // The wavefronts' sums, added in one order.  (w holds the scale already.)
+    const float scale = P.scale && !is_a ? P.scale[a] : 1.0f;
     const int64_t each = (int64_t)P.R * (P.K + P.N);
     float* dA = t.w < 0 ? P.dA + (int64_t)a * P.R * P.K : P.slots + t.w * each;
     float* dB = t.w < 0 ? P.dB + (int64_t)a * P.R * P.N : P.slots + t.w * each + (int64_t)P.R * P.K;
@@ -460,7 +637,7 @@ __global__ void __launch_bounds__(256) adapter_wgrad_kernel(AdapterGrad P) {
             *reinterpret_cast<f32x4*>(&red[wave][4 * q + e][8 * i + 4]) = f32x4{acc[4][b][e], acc[5][b][e], acc[6][b][e], acc[7][b][e]};
         }
         __syncthreads();
-        const int rank = rank0 + 16 * b;
+        const int rank = (block0 + b) * 16;
         if (is_a) {
             const int r = threadIdx.x / 16, c = threadIdx.x % 16 * 8;
             if (rank + r < P.R && c0 + c < C)
@@ -469,7 +646,7 @@ __global__ void __launch_bounds__(256) adapter_wgrad_kernel(AdapterGrad P) {
                     f32x4 s[4];
 #pragma unroll
                     for (int k = 0; k < 4; k++) s[k] = *reinterpret_cast<const f32x4*>(&red[k][r][c + 4 * h]);
-                    *reinterpret_cast<f32x4*>(dA + (int64_t)(rank + r) * P.K + c0 + c + 4 * h) = ((s[0] + s[1]) + (s[2] + s[3])) * scale;
+                    *reinterpret_cast<f32x4*>(dA + (int64_t)(rank + r) * P.K + c0 + c + 4 * h) = (s[0] + s[1]) + (s[2] + s[3]);
                 }
         } else {
             const int c = threadIdx.x / 2, r = threadIdx.x % 2 * 8;
@@ -503,9 +680,6 @@ __global__ void __launch_bounds__(256) adapter_join_kernel(AdapterGrad P) {
     *reinterpret_cast<f32x4*>(out) = s;
 }
 
-// The row tile for a rank: RB * MB * 8 KiB of LDS join the wavefronts' sums.
-int adapter_tile(int32_t R) { return R <= 64 ? 32 : 16; }
-
 // A workgroup of the plan places 1024 rows, or as many as keep their number to
 // 256: each of them counts all rows.
 hipError_t launch_adapter_plan(AdapterPlan P, hipStream_t stream) {
@@ -518,21 +692,34 @@ hipError_t launch_adapter_plan(AdapterPlan P, hipStream_t stream) {
 
 namespace {
 
-template <int RB, int MB>
+template <int RB, bool kGrad, bool kBase>
+void adapter_start(const AdapterParams& P, int64_t tiles, hipStream_t s) {
+    const dim3 grid((unsigned)((tiles * P.slabs + 7) / 8 * 8));
+    hipLaunchKernelGGL((adapter_kernel<RB, kAdTile / 16, kGrad, kBase>), grid, dim3(kAdWaves * 64), 0, s, P);
+}
+template <int RB>
 hipError_t adapter_run(const AdapterParams& P, int64_t tiles, hipStream_t s) {
-    hipLaunchKernelGGL((adapter_kernel<RB, MB>), dim3((unsigned)(tiles * P.slabs)), dim3(kAdWaves * 64), 0, s, P);
+    if (P.w_pack)
+        P.base ? adapter_start<RB, true, true>(P, tiles, s) : adapter_start<RB, true, false>(P, tiles, s);
+    else
+        P.base ? adapter_start<RB, false, true>(P, tiles, s) : adapter_start<RB, false, false>(P, tiles, s);
     return hipGetLastError();
 }
 
 }  // namespace
 
+int adapter_rank_blocks(int32_t R) { return R <= 16 ? 1 : R <= 32 ? 2 : R <= 64 ? 4 : 8; }
+
 hipError_t launch_adapter(AdapterParams P, int64_t tiles, hipStream_t stream) {
+    const int cols = P.R <= 32 ? 128 * kAdWaves : 64 * kAdWaves;  // of a step
     // Few tiles: their columns are shared out, and each share repeats the first product.
-    P.slabs = (int32_t)std::max<int64_t>(1, std::min<int64_t>((P.N + kAdWaves * 64 - 1) / (kAdWaves * 64), 512 / tiles));
-    if (P.R <= 16) return adapter_run<1, 2>(P, tiles, stream);
-    if (P.R <= 32) return adapter_run<2, 2>(P, tiles, stream);
-    if (P.R <= 64) return adapter_run<4, 2>(P, tiles, stream);
-    return adapter_run<8, 1>(P, tiles, stream);
+    P.slabs = (int32_t)std::max<int64_t>(1, std::min<int64_t>((P.N + cols - 1) / cols, 512 / tiles));
+    switch (adapter_rank_blocks(P.R)) {
+        case 1: return adapter_run<1>(P, tiles, stream);
+        case 2: return adapter_run<2>(P, tiles, stream);
+        case 4: return adapter_run<4>(P, tiles, stream);
+        default: return adapter_run<8>(P, tiles, stream);
+    }
 }
 
 // Rows of a chunk of the gradients: the columns' slabs times the chunks are
@@ -543,7 +730,8 @@ int32_t adapter_chunk(int64_t M, int64_t K, int64_t N) {
 }
 
 hipError_t launch_adapter_transpose(const AdapterGrad& P, hipStream_t stream) {
-    hipLaunchKernelGGL(adapter_transpose_kernel, dim3((P.K + 63) / 64 + (P.N + 63) / 64, P.n), dim3(256), 0, stream, P);
+    const unsigned blocks = P.R / 8 * (P.K / 8 + P.N / 8);  // of 8 x 8
+    hipLaunchKernelGGL(adapter_transpose_kernel, dim3((blocks + 255) / 256, P.n), dim3(256), 0, stream, P);
     return hipGetLastError();
 }
 

@@ -231,16 +231,16 @@ int adapter_planes(const nvfp4moe_adapters* ad) {
     return NVFP4_OK;
 }
 // Workspace: the plan (rows by adapter, its tables) and, for the gradients, the
-// transposed adapters, w and partial sums.
+// transposed adapters, w and v as operands and partial sums.
 struct AdapterWork {
-    size_t order, tiles, chunks, info, at, bt, w, slots, total;
+    size_t order, tiles, chunks, steps, info, at, bt, v_pack, w_pack, slots, total;
     int64_t n_tiles, n_chunks;
     int32_t chunk;
 };
 AdapterWork adapter_work(const nvfp4moe_adapters* ad, int64_t M, bool backward) {
     AdapterWork w{};
-    const int64_t n = ad->n, R = ad->rank, K = ad->in_features, N = ad->out_features, tile = adapter_tile(ad->rank);
-    w.n_tiles = M / tile + std::min(M, n + 1);
+    const int64_t n = ad->n, R = ad->rank, K = ad->in_features, N = ad->out_features;
+    w.n_tiles = M / kAdTile + std::min(M, n + 1);
     w.order = kAlign;
     w.tiles = w.order + up(M * 4, kAlign);
     w.total = w.tiles + up(w.n_tiles * 16, kAlign);
@@ -248,11 +248,13 @@ AdapterWork adapter_work(const nvfp4moe_adapters* ad, int64_t M, bool backward) 
     w.chunk = adapter_chunk(M, K, N);
     w.n_chunks = M / w.chunk + std::min(M, n);
     w.chunks = w.total;
-    w.info = w.chunks + up(w.n_chunks * 16, kAlign);
+    w.steps = w.chunks + up(w.n_chunks * 16, kAlign);
+    w.info = w.steps + up(w.n_chunks * 4, kAlign);
     w.at = w.info + up(n * 8, kAlign);
     w.bt = w.at + up(n * R * K * 2, kAlign);
-    w.w = w.bt + up(n * R * N * 2, kAlign);
-    w.slots = w.w + up(M * R * 4, kAlign);
+    w.v_pack = w.bt + up(n * R * N * 2, kAlign);
+    w.w_pack = w.v_pack + (size_t)w.n_tiles * adapter_rank_blocks(ad->rank) * 3 * 1024;
+    w.slots = 2 * w.w_pack - w.v_pack;
     // chunks of adapters that have more than one: each such adapter has more
     // than `chunk` rows, so at most twice its rows / chunk of them
     w.total = w.slots + up((2 * M / w.chunk) * R * (K + N) * 4, kAlign);
@@ -494,7 +496,7 @@ int nvfp4moe_adapter_linear(const nvfp4moe_adapters* ad, const uint16_t* x, int6
     plan.ids = ids;
     plan.M = M;
     plan.n = ad->n;
-    plan.tile = adapter_tile(ad->rank);
+    plan.tile = kAdTile;
     plan.rest = base != out || v;
     plan.n_tables = (int32_t*)ws;
     plan.order = (int32_t*)(ws + w.order);
@@ -543,13 +545,14 @@ int nvfp4moe_adapter_backward(const nvfp4moe_adapters* ad, const uint16_t* x, in
     plan.ids = ids;
     plan.M = M;
     plan.n = ad->n;
-    plan.tile = adapter_tile(ad->rank);
+    plan.tile = kAdTile;
     plan.chunk = w.chunk;
     plan.rest = base != dx;
     plan.n_tables = (int32_t*)ws;
     plan.order = (int32_t*)(ws + w.order);
     plan.tiles = (int4*)(ws + w.tiles);
     plan.chunks = (int4*)(ws + w.chunks);
+    plan.chunk_step = (int32_t*)(ws + w.steps);
     plan.info = (int2*)(ws + w.info);
     if (launch_adapter_plan(plan, s) != hipSuccess) return NVFP4_E_HIP;
     AdapterGrad g{};
@@ -566,10 +569,12 @@ int nvfp4moe_adapter_backward(const nvfp4moe_adapters* ad, const uint16_t* x, in
     g.dy = dy;
     g.ldx = ldx;
     g.ld_dy = ld_dy;
-    g.v = v;
-    g.w = (float*)(ws + w.w);
+    g.v_pack = (u32x4*)(ws + w.v_pack);
+    g.w_pack = (u32x4*)(ws + w.w_pack);
+    g.rank_blocks = adapter_rank_blocks(ad->rank);
     g.order = plan.order;
     g.chunks = plan.chunks;
+    g.chunk_step = plan.chunk_step;
     g.n_tables = plan.n_tables;
     g.info = plan.info;
     g.slots = (float*)(ws + w.slots);
@@ -590,7 +595,9 @@ int nvfp4moe_adapter_backward(const nvfp4moe_adapters* ad, const uint16_t* x, in
         p.ld_base = ld_base;
         p.out = dx;
         p.ld_out = ld_dx;
-        p.v = (float*)(ws + w.w);
+        p.v_in = v;
+        p.v_pack = (u32x4*)(ws + w.v_pack);
+        p.w_pack = (u32x4*)(ws + w.w_pack);
         p.order = plan.order;
         p.tiles = plan.tiles;
         p.n_tiles = plan.n_tables;

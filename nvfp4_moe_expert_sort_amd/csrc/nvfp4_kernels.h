@@ -6,6 +6,8 @@
 
 namespace nvfp4 {
 
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+
 constexpr int kMAlign = 32;      // each expert's rows are padded to a multiple of this (one MFMA row tile)
 constexpr int kTileRows = 128;   // rows per GEMM wave tile (4 MFMA row tiles)
 constexpr int kTokPerBlk = 16;   // tokens per block in the sort kernels
@@ -161,6 +163,7 @@ hipError_t launch_balance(const BalanceParams& P, bool bf16, hipStream_t stream)
 
 // Low-rank adapters and their gradients (adapter.hip).
 constexpr int kMaxRank = 128;
+constexpr int kAdTile = 32;  // rows of a row tile, and of a step of the weights' gradients
 struct AdapterPlan {  // rows grouped by adapter
     const int32_t* ids;  // [M]
     int64_t M;
@@ -171,8 +174,9 @@ struct AdapterPlan {  // rows grouped by adapter
     bool rest;           // tiles for the rows without an adapter too
     int32_t* n_tables;   // [2]: row tiles, chunks
     int32_t* order;      // [M]
-    int4* tiles;         // {adapter or -1, first position in order, rows, 0}
+    int4* tiles;         // {adapter or -1, first position in order, rows, its own number}
     int4* chunks;        // {adapter, first position, rows, partial sum or -1: the adapter's only one}
+    int32_t* chunk_step; // number of a chunk's first tile
     int2* info;          // [n] {chunks, first partial sum}
 };
 hipError_t launch_adapter_plan(AdapterPlan P, hipStream_t stream);
@@ -192,8 +196,10 @@ struct AdapterParams {
     const int4* tiles;
     const int32_t* n_tiles;
     int32_t slabs;       // set by the launcher
+    const float* v_in;   // gradients: the forward's v, and the operands that it and w become:
+    u32x4 *v_pack, *w_pack;  // [tiles][rank blocks][3][64]
 };
-int adapter_tile(int32_t R);  // rows of a row tile
+int adapter_rank_blocks(int32_t R);  // blocks of 16 ranks that the kernels compute
 hipError_t launch_adapter(AdapterParams P, int64_t tiles_bound, hipStream_t stream);
 struct AdapterGrad {
     const uint16_t* A;
@@ -205,10 +211,11 @@ struct AdapterGrad {
     const uint16_t* x;
     const uint16_t* dy;
     int64_t ldx, ld_dy;
-    const float* v;      // [M][R] A x, and B^T dy
-    const float* w;
+    const u32x4 *v_pack, *w_pack;
+    int32_t rank_blocks;
     const int32_t* order;
     const int4* chunks;
+    const int32_t* chunk_step;
     const int32_t* n_tables;
     const int2* info;
     float* slots;        // partial sums, R (K + N) each
