@@ -243,12 +243,15 @@ __global__ void __launch_bounds__(kPlanThreads) adapter_plan_kernel(AdapterPlan 
 // RB: ranks in blocks of 16; MB: rows in blocks of 16.
 // kGrad: V and the forward's v also go, as three BF16 values, to the operands
 // of the weights' gradients.
-template <int RB, int MB, bool kGrad, bool kBase>
+// kSmall: at most 256 rows, without a plan.  The workgroup of each row looks for
+// the rows of the same adapter; every 16th of them takes the next 16.
+template <int RB, int MB, bool kGrad, bool kBase, bool kSmall>
 __global__ void __launch_bounds__(kAdWaves * 64, 2) adapter_kernel(AdapterParams P) {
     constexpr int kR = 16 * RB, kPieces = kGrad ? 3 : 2, kPitch = kPieces * kR + 8;
     constexpr int kRound = RB * MB < 8 ? RB * MB : 8;  // blocks of V joined at a time
     constexpr int kA = RB < 4 ? RB : 4;                // rank blocks turned over at a time
-    constexpr int kAhead = RB < 8 ? 2 : 1;             // steps of the first product whose loads are in registers
+    // Steps of the first product whose loads are in registers.
+    constexpr int kAhead = kSmall ? (RB < 4 ? 4 : RB < 8 ? 2 : 1) : RB < 8 ? 2 : 1;
     constexpr int NB = RB < 4 ? 8 : 4, kCols = 16 * NB;  // neighbouring columns of a lane; columns of a step
     constexpr int kB = (RB + 1) / 2, kBLoads = NB * RB / 2;  // operands a column; 16-byte loads of B a lane and step
     constexpr int kUnits1 = (MB + kA) * 128, kUnits2 = kBLoads * 64, kUnits = kUnits1 > kUnits2 ? kUnits1 : kUnits2;
@@ -260,13 +263,45 @@ __global__ void __launch_bounds__(kAdWaves * 64, 2) adapter_kernel(AdapterParams
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     u32x4* own = lds + wave * kUnits;
     // Consecutive tiles, which mostly share an adapter, on one XCD.
-    const uint32_t items = (uint32_t)*P.n_tiles * P.slabs, per = (items + 7) / 8, item = (blockIdx.x & 7) * per + (blockIdx.x >> 3);
+    const uint32_t items = (uint32_t)(kSmall ? P.M : *P.n_tiles) * P.slabs, per = (items + 7) / 8;
+    const uint32_t item = (blockIdx.x & 7) * per + (blockIdx.x >> 3);
     if ((blockIdx.x >> 3) >= per || item >= items) return;
     const int32_t slab = item % P.slabs;
-    const int4 t = P.tiles[item / P.slabs];
+    int4 t;
+    __shared__ int32_t rows[16];
+    if constexpr (kSmall) {
+        __shared__ uint64_t found[4];
+        const int leader = item / P.slabs, id = P.ids[leader], r = threadIdx.x;
+        t.x = id >= 0 && id < P.n ? id : -1;
+        bool same = false;
+        if (r < P.M) {
+            const int other = P.ids[r];
+            same = t.x < 0 ? other < 0 || other >= P.n : other == id;
+        }
+        const uint64_t mine = __ballot(same);
+        if (wave < 4 && lane == 0) found[wave] = mine;
+        __syncthreads();
+        int before = 0, mine_before = 0, total = 0;  // of the same: before the leader, before row r
+#pragma unroll
+        for (int w = 0; w < 4; w++) {
+            const uint64_t f = found[w];
+            total += __popcll(f);
+            before += w < leader / 64 ? __popcll(f) : w == leader / 64 ? __popcll(f & ((1ull << (leader & 63)) - 1)) : 0;
+            mine_before += w < wave ? __popcll(f) : w == wave ? __popcll(f & ((1ull << lane) - 1)) : 0;
+        }
+        if (before % 16 != 0 || (t.x < 0 && !P.rest)) return;
+        t.z = min(total - before, 16);
+        if (same && mine_before >= before && mine_before < before + 16) rows[mine_before - before] = r;
+        __syncthreads();
+    } else {
+        t = P.tiles[item / P.slabs];
+    }
     const int a = t.x, count = t.z;
     // Rows past `count` repeat the last one: its values, stored again.
-    auto row_of = [&](int m) { return (int64_t)P.order[t.y + min(m, count - 1)]; };
+    auto row_of = [&](int m) {
+        if constexpr (kSmall) return (int64_t)rows[min(m, count - 1)];
+        return (int64_t)P.order[t.y + min(m, count - 1)];
+    };
     if (a < 0) {  // rows without an adapter
         const int pieces = P.N / 8;
         for (int64_t k = slab * (kAdWaves * 64) + threadIdx.x; k < (int64_t)count * pieces; k += P.slabs * (kAdWaves * 64)) {
@@ -330,34 +365,23 @@ __global__ void __launch_bounds__(kAdWaves * 64, 2) adapter_kernel(AdapterParams
     {
         const int whole = P.K / 64;
         int c = wave;
-        if constexpr (kAhead == 2) {
-            if (c < whole) load1(0, c);
-            if (c + kAdWaves < whole) {
-                load1(1, c + kAdWaves);
-                for (; c + 3 * kAdWaves < whole; c += 2 * kAdWaves) {
-                    mul1(0, [&] { load1(0, c + 2 * kAdWaves); });
-                    mul1(1, [&] { load1(1, c + 3 * kAdWaves); });
-                }
-                if (c + 2 * kAdWaves < whole) {
-                    mul1(0, [&] { load1(0, c + 2 * kAdWaves); });
-                    mul1(1, nothing);
-                    mul1(0, nothing);
-                    c += 3 * kAdWaves;
-                } else {
-                    mul1(0, nothing);
-                    mul1(1, nothing);
-                    c += 2 * kAdWaves;
-                }
-            } else if (c < whole) {
-                mul1(0, nothing);
-                c += kAdWaves;
-            }
-        } else if (c < whole) {
-            load1(0, c);
-            for (; c + kAdWaves < whole; c += kAdWaves) mul1(0, [&] { load1(0, c + kAdWaves); });
-            mul1(0, nothing);
-            c += kAdWaves;
-        }
+        auto at = [&](int k) { return c + k * kAdWaves; };  // the wavefront's steps from c on
+#pragma unroll
+        for (int s = 0; s < kAhead; s++)
+            if (at(s) < whole) load1(s, at(s));
+        for (; at(2 * kAhead - 1) < whole; c = at(kAhead))
+#pragma unroll
+            for (int s = 0; s < kAhead; s++) mul1(s, [&] { load1(s, at(kAhead + s)); });
+#pragma unroll
+        for (int s = 0; s < kAhead; s++)
+            if (at(kAhead + s) < whole)
+                mul1(s, [&] { load1(s, at(kAhead + s)); });
+            else if (at(s) < whole)
+                mul1(s, nothing);
+#pragma unroll
+        for (int s = 0; s < kAhead - 1; s++)
+            if (at(kAhead + s) < whole) mul1(s, nothing);
+        c += max(0, (whole - c + kAdWaves - 1) / kAdWaves) * kAdWaves;
         if (c == whole && c * 64 < P.K) {  // the rest of K
             const bool in = c * 64 + 8 * piece < P.K;
             const int k0 = in ? c * 64 : -8 * piece;  // (the row's start)
@@ -694,8 +718,13 @@ namespace {
 
 template <int RB, bool kGrad, bool kBase>
 void adapter_start(const AdapterParams& P, int64_t tiles, hipStream_t s) {
-    const dim3 grid((unsigned)((tiles * P.slabs + 7) / 8 * 8));
-    hipLaunchKernelGGL((adapter_kernel<RB, kAdTile / 16, kGrad, kBase>), grid, dim3(kAdWaves * 64), 0, s, P);
+    const dim3 grid((unsigned)((tiles * P.slabs + 7) / 8 * 8)), block(kAdWaves * 64);
+    if constexpr (!kGrad)
+        if (P.ids) {
+            hipLaunchKernelGGL((adapter_kernel<RB, 1, false, kBase, true>), grid, block, 0, s, P);
+            return;
+        }
+    hipLaunchKernelGGL((adapter_kernel<RB, kAdTile / 16, kGrad, kBase, false>), grid, block, 0, s, P);
 }
 template <int RB>
 hipError_t adapter_run(const AdapterParams& P, int64_t tiles, hipStream_t s) {
@@ -710,10 +739,15 @@ hipError_t adapter_run(const AdapterParams& P, int64_t tiles, hipStream_t s) {
 
 int adapter_rank_blocks(int32_t R) { return R <= 16 ? 1 : R <= 32 ? 2 : R <= 64 ? 4 : 8; }
 
+// Up to 256 rows take one launch, which groups them itself.
+bool adapter_small(int64_t M) { return M <= 256; }
+
 hipError_t launch_adapter(AdapterParams P, int64_t tiles, hipStream_t stream) {
     const int cols = P.R <= 32 ? 128 * kAdWaves : 64 * kAdWaves;  // of a step
-    // Few tiles: their columns are shared out, and each share repeats the first product.
-    P.slabs = (int32_t)std::max<int64_t>(1, std::min<int64_t>((P.N + cols - 1) / cols, 512 / tiles));
+    // Few tiles: their columns are shared out, and each share repeats the first
+    // product.  (Of the M workgroups of a small call, those of other rows end at once.)
+    const int64_t working = P.ids ? std::min<int64_t>(P.M, P.n + 1 + P.M / 16) : tiles;
+    P.slabs = (int32_t)std::max<int64_t>(1, std::min<int64_t>((P.N + cols - 1) / cols, 512 / working));
     switch (adapter_rank_blocks(P.R)) {
         case 1: return adapter_run<1>(P, tiles, stream);
         case 2: return adapter_run<2>(P, tiles, stream);

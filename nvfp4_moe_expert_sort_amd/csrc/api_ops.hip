@@ -492,16 +492,6 @@ int nvfp4moe_adapter_linear(const nvfp4moe_adapters* ad, const uint16_t* x, int6
     if (workspace_bytes < w.total) return NVFP4_E_WORKSPACE;
     if (!aligned(ids, 4) || !aligned(v, 16) || !aligned(workspace, kAlign)) return NVFP4_E_ALIGN;
     uint8_t* ws = (uint8_t*)workspace;
-    AdapterPlan plan{};
-    plan.ids = ids;
-    plan.M = M;
-    plan.n = ad->n;
-    plan.tile = kAdTile;
-    plan.rest = base != out || v;
-    plan.n_tables = (int32_t*)ws;
-    plan.order = (int32_t*)(ws + w.order);
-    plan.tiles = (int4*)(ws + w.tiles);
-    if (launch_adapter_plan(plan, (hipStream_t)stream) != hipSuccess) return NVFP4_E_HIP;
     AdapterParams p{};
     p.x = x;
     p.ldx = ldx;
@@ -516,6 +506,23 @@ int nvfp4moe_adapter_linear(const nvfp4moe_adapters* ad, const uint16_t* x, int6
     p.out = out;
     p.ld_out = ld_out;
     p.v = v;
+    p.M = (int32_t)M;
+    p.n = ad->n;
+    p.rest = base != out || v;
+    if (adapter_small(M)) {
+        p.ids = ids;
+        return hip_status(launch_adapter(p, M, (hipStream_t)stream));
+    }
+    AdapterPlan plan{};
+    plan.ids = ids;
+    plan.M = M;
+    plan.n = ad->n;
+    plan.tile = kAdTile;
+    plan.rest = p.rest;
+    plan.n_tables = (int32_t*)ws;
+    plan.order = (int32_t*)(ws + w.order);
+    plan.tiles = (int4*)(ws + w.tiles);
+    if (launch_adapter_plan(plan, (hipStream_t)stream) != hipSuccess) return NVFP4_E_HIP;
     p.order = plan.order;
     p.tiles = plan.tiles;
     p.n_tiles = plan.n_tables;

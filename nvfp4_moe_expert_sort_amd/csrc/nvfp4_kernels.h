@@ -195,11 +195,15 @@ struct AdapterParams {
     const int32_t* order;
     const int4* tiles;
     const int32_t* n_tiles;
+    const int32_t* ids;  // a small call, without a plan: [M], or null
+    int32_t M, n;
+    bool rest;           // the rows without an adapter too
     int32_t slabs;       // set by the launcher
     const float* v_in;   // gradients: the forward's v, and the operands that it and w become:
     u32x4 *v_pack, *w_pack;  // [tiles][rank blocks][3][64]
 };
 int adapter_rank_blocks(int32_t R);  // blocks of 16 ranks that the kernels compute
+bool adapter_small(int64_t M);
 hipError_t launch_adapter(AdapterParams P, int64_t tiles_bound, hipStream_t stream);
 struct AdapterGrad {
     const uint16_t* A;
