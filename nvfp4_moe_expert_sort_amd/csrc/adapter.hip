@@ -86,22 +86,25 @@ __device__ __forceinline__ int find_bin(const int32_t* start, int n, int32_t i) 
 __device__ __forceinline__ int bin_of(const AdapterPlan& P, int32_t id) { return id >= 0 && id < P.n ? id : P.n; }
 
 // Counts the bins of the lanes' four consecutive rows in LDS, of which the
-// first `live` exist.  Neighbouring rows mostly share an adapter: one lane then
-// adds for all.
+// first `live` exist.  Neighbouring rows mostly share an adapter, and additions
+// of many lanes to one address take one turn each.
 __device__ __forceinline__ void count4(int32_t* hist, const AdapterPlan& P, int4 id, int64_t live) {
     if (live <= 0) return;
     const int b0 = bin_of(P, id.x), b1 = bin_of(P, id.y), b2 = bin_of(P, id.z), b3 = bin_of(P, id.w);
     const bool same = live >= 4 && b0 == b1 && b0 == b2 && b0 == b3;
-    if (__ballot(same && b0 == __builtin_amdgcn_readfirstlane(b0)) == ~0ull) {
-        if ((threadIdx.x & 63) == 0) atomicAdd(&hist[b0], 256);
-    } else if (same) {
-        atomicAdd(&hist[b0], 4);
-    } else {
-        atomicAdd(&hist[b0], 1);
-        if (live > 1) atomicAdd(&hist[b1], 1);
-        if (live > 2) atomicAdd(&hist[b2], 1);
-        if (live > 3) atomicAdd(&hist[b3], 1);
+    // Lanes whose four rows share an adapter: one addition for all lanes of it.
+    bool left = same;
+    while (const uint64_t m = __ballot(left)) {
+        const int first = __builtin_ctzll(m), bin = __builtin_amdgcn_readlane(b0, first);
+        const uint64_t run = __ballot(left && b0 == bin);
+        if ((int)(threadIdx.x & 63) == first) atomicAdd(&hist[bin], 4 * __popcll(run));
+        left = left && b0 != bin;
     }
+    if (same) return;
+    atomicAdd(&hist[b0], 1);
+    if (live > 1) atomicAdd(&hist[b1], 1);
+    if (live > 2) atomicAdd(&hist[b2], 1);
+    if (live > 3) atomicAdd(&hist[b3], 1);
 }
 
 }  // namespace
@@ -121,26 +124,32 @@ __global__ void __launch_bounds__(kPlanThreads) adapter_plan_kernel(AdapterPlan 
     for (int i = threadIdx.x; i <= bins; i += kPlanThreads) total[i] = 0;
     for (int i = threadIdx.x; i < bins; i += kPlanThreads) before[i] = 0;
     __syncthreads();
-    for (int64_t r0 = 0; r0 < P.M; r0 += 4 * kPlanThreads * kAhead) {
+    // Four rows a thread.  kAhead such pieces of 4096 rows are loaded before any
+    // is counted, the last piece (which may be a part) by itself.
+    const int64_t last = P.M > 0 ? (P.M - 1) / (4 * kPlanThreads) : 0;
+    for (int64_t p0 = 0; p0 < last; p0 += kAhead) {
         int4 id[kAhead];
 #pragma unroll
         for (int k = 0; k < kAhead; k++) {
-            const int64_t r = r0 + 4 * ((int64_t)k * kPlanThreads + threadIdx.x);
-            id[k] = make_int4(-1, -1, -1, -1);
-            if (P.vec && r + 4 <= P.M) {
-                id[k] = *reinterpret_cast<const int4*>(P.ids + r);
-            } else {
-                if (r < P.M) id[k].x = P.ids[r];
-                if (r + 1 < P.M) id[k].y = P.ids[r + 1];
-                if (r + 2 < P.M) id[k].z = P.ids[r + 2];
-                if (r + 3 < P.M) id[k].w = P.ids[r + 3];
-            }
+            const int32_t* at = P.ids + 4 * (min(p0 + k, last - 1) * kPlanThreads + threadIdx.x);
+            if (P.vec)
+                id[k] = *reinterpret_cast<const int4*>(at);
+            else
+                id[k] = make_int4(at[0], at[1], at[2], at[3]);
         }
+        issue();
 #pragma unroll
-        for (int k = 0; k < kAhead; k++) {
-            const int64_t r = r0 + 4 * ((int64_t)k * kPlanThreads + threadIdx.x);
-            count4(r < first ? before : total, P, id[k], P.M - r);
-        }
+        for (int k = 0; k < kAhead; k++)
+            if (p0 + k < last) count4(4 * ((p0 + k) * kPlanThreads + threadIdx.x) < first ? before : total, P, id[k], 4);
+    }
+    {
+        const int64_t r = 4 * (last * kPlanThreads + threadIdx.x);
+        int4 id = make_int4(-1, -1, -1, -1);
+        if (r < P.M) id.x = P.ids[r];
+        if (r + 1 < P.M) id.y = P.ids[r + 1];
+        if (r + 2 < P.M) id.z = P.ids[r + 2];
+        if (r + 3 < P.M) id.w = P.ids[r + 3];
+        count4(r < first ? before : total, P, id, P.M - r);
     }
     __syncthreads();
     for (int i = threadIdx.x; i <= bins; i += kPlanThreads) {
@@ -171,11 +180,13 @@ __global__ void __launch_bounds__(kPlanThreads) adapter_plan_kernel(AdapterPlan 
             if (live && rank == 0) mine[b] = (uint16_t)__popcll(same);
             __syncthreads();
             for (int i = threadIdx.x; i < bins; i += kPlanThreads) {
-                uint32_t run = 0;
+                uint32_t run = 0, n[kWaves];
+#pragma unroll
+                for (int w = 0; w < kWaves; w++) n[w] = counts[w][i];
+#pragma unroll
                 for (int w = 0; w < kWaves; w++) {
-                    const uint32_t n = counts[w][i];
                     counts[w][i] = (uint16_t)run;
-                    run += n;
+                    run += n[w];
                 }
                 before[i] = run;
             }
@@ -225,9 +236,9 @@ __global__ void __launch_bounds__(kPlanThreads) adapter_plan_kernel(AdapterPlan 
 
 // One workgroup: up to 16 MB rows of one adapter, and a share of the columns.
 //
-// The first product V = A x^T over K is split over the wavefronts (chunks of
-// 64 columns in turn) and joined in LDS in one fixed order, whatever the tile:
-// a row's bits do not depend on the rows beside it.  V, an FP32 sum, is passed
+// The first product V = A x^T over K is split over the wavefronts and joined in
+// LDS in one fixed order, whatever the tile: a row's bits do not depend on the
+// rows beside it.  V, an FP32 sum, is passed
 // on as two BF16 values (2^-16 of it may be lost, against the 2^-8 of the output's
 // one rounding): 32 of the second product's inputs are then 16 ranks twice,
 // which costs no instruction at rank 16.
@@ -243,15 +254,14 @@ __global__ void __launch_bounds__(kPlanThreads) adapter_plan_kernel(AdapterPlan 
 // RB: ranks in blocks of 16; MB: rows in blocks of 16.
 // kGrad: V and the forward's v also go, as three BF16 values, to the operands
 // of the weights' gradients.
-// kSmall: at most 256 rows, without a plan.  The workgroup of each row looks for
-// the rows of the same adapter; every 16th of them takes the next 16.
+// kSmall: at most 512 rows, without a plan: every workgroup groups them itself.
 template <int RB, int MB, bool kGrad, bool kBase, bool kSmall>
 __global__ void __launch_bounds__(kAdWaves * 64, 2) adapter_kernel(AdapterParams P) {
     constexpr int kR = 16 * RB, kPieces = kGrad ? 3 : 2, kPitch = kPieces * kR + 8;
     constexpr int kRound = RB * MB < 8 ? RB * MB : 8;  // blocks of V joined at a time
     constexpr int kA = RB < 4 ? RB : 4;                // rank blocks turned over at a time
     // Steps of the first product whose loads are in registers.
-    constexpr int kAhead = kSmall ? (RB < 4 ? 4 : RB < 8 ? 2 : 1) : RB < 8 ? 2 : 1;
+    constexpr int kAhead = kSmall && RB < 2 ? 4 : RB < 8 ? 2 : 1;
     constexpr int NB = RB < 4 ? 8 : 4, kCols = 16 * NB;  // neighbouring columns of a lane; columns of a step
     constexpr int kB = (RB + 1) / 2, kBLoads = NB * RB / 2;  // operands a column; 16-byte loads of B a lane and step
     constexpr int kUnits1 = (MB + kA) * 128, kUnits2 = kBLoads * 64, kUnits = kUnits1 > kUnits2 ? kUnits1 : kUnits2;
@@ -263,35 +273,61 @@ __global__ void __launch_bounds__(kAdWaves * 64, 2) adapter_kernel(AdapterParams
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     u32x4* own = lds + wave * kUnits;
     // Consecutive tiles, which mostly share an adapter, on one XCD.
-    const uint32_t items = (uint32_t)(kSmall ? P.M : *P.n_tiles) * P.slabs, per = (items + 7) / 8;
+    const uint32_t items = (uint32_t)(kSmall ? P.tile_bound : *P.n_tiles) * P.slabs, per = (items + 7) / 8;
     const uint32_t item = (blockIdx.x & 7) * per + (blockIdx.x >> 3);
     if ((blockIdx.x >> 3) >= per || item >= items) return;
     const int32_t slab = item % P.slabs;
     int4 t;
     __shared__ int32_t rows[16];
     if constexpr (kSmall) {
-        __shared__ uint64_t found[4];
-        const int leader = item / P.slabs, id = P.ids[leader], r = threadIdx.x;
-        t.x = id >= 0 && id < P.n ? id : -1;
-        bool same = false;
-        if (r < P.M) {
-            const int other = P.ids[r];
-            same = t.x < 0 ? other < 0 || other >= P.n : other == id;
+        // Thread r has row r.  Its rank among the rows of its adapter: equal
+        // lanes find each other by a ballot for each bit of the adapter; counts
+        // of the earlier wavefronts' in LDS.  Every 16th row of an adapter leads
+        // a tile; tiles are numbered by their leaders.
+        uint16_t* counts = reinterpret_cast<uint16_t*>(lds);  // [kAdWaves][bins]
+        const int bins = P.n + 1, r = threadIdx.x;
+        const bool live = r < P.M;
+        int bin = P.n;
+        if (live) bin = P.ids[r];
+        if (bin < 0 || bin > P.n) bin = P.n;
+        for (int k = threadIdx.x; k < kAdWaves * bins; k += kAdWaves * 64) counts[k] = 0;
+        uint64_t same = __ballot(live);
+        for (int bit = 0; (P.n >> bit) != 0; bit++) {
+            const bool on = (bin >> bit) & 1;
+            const uint64_t m = __ballot(on);
+            same &= on ? m : ~m;
         }
-        const uint64_t mine = __ballot(same);
-        if (wave < 4 && lane == 0) found[wave] = mine;
+        int rank = __popcll(same & ((1ull << lane) - 1));
         __syncthreads();
-        int before = 0, mine_before = 0, total = 0;  // of the same: before the leader, before row r
+        if (live && rank == 0) counts[wave * bins + bin] = (uint16_t)__popcll(same);
+        __syncthreads();
+        int total = 0;
 #pragma unroll
-        for (int w = 0; w < 4; w++) {
-            const uint64_t f = found[w];
-            total += __popcll(f);
-            before += w < leader / 64 ? __popcll(f) : w == leader / 64 ? __popcll(f & ((1ull << (leader & 63)) - 1)) : 0;
-            mine_before += w < wave ? __popcll(f) : w == wave ? __popcll(f & ((1ull << lane) - 1)) : 0;
+        for (int w = 0; w < kAdWaves; w++) {
+            const int n = counts[w * bins + bin];
+            total += n;
+            rank += w < wave ? n : 0;
         }
-        if (before % 16 != 0 || (t.x < 0 && !P.rest)) return;
-        t.z = min(total - before, 16);
-        if (same && mine_before >= before && mine_before < before + 16) rows[mine_before - before] = r;
+        __shared__ uint64_t leaders[kAdWaves];
+        __shared__ int4 lead;  // adapter, its rank, rows of the adapter
+        const bool leads = live && rank % 16 == 0 && (bin < P.n || P.rest);
+        const uint64_t mine = __ballot(leads);
+        if (lane == 0) leaders[wave] = mine;
+        __syncthreads();
+        int number = __popcll(mine & ((1ull << lane) - 1)), n_tiles = 0;
+#pragma unroll
+        for (int w = 0; w < kAdWaves; w++) {
+            n_tiles += __popcll(leaders[w]);
+            number += w < wave ? __popcll(leaders[w]) : 0;
+        }
+        const int tile = item / P.slabs;
+        if (tile >= n_tiles) return;
+        if (leads && number == tile) lead = make_int4(bin, rank, total, 0);
+        __syncthreads();
+        const int rank0 = lead.y;
+        t.x = lead.x < P.n ? lead.x : -1;
+        t.z = min(lead.z - rank0, 16);
+        if (live && bin == lead.x && rank >= rank0 && rank < rank0 + 16) rows[rank - rank0] = r;
         __syncthreads();
     } else {
         t = P.tiles[item / P.slabs];
@@ -363,9 +399,13 @@ __global__ void __launch_bounds__(kAdWaves * 64, 2) adapter_kernel(AdapterParams
     };
     auto nothing = [] {};
     {
-        const int whole = P.K / 64;
-        int c = wave;
-        auto at = [&](int k) { return c + k * kAdWaves; };  // the wavefront's steps from c on
+        // The wavefront's steps: consecutive ones, so that the wavefronts read
+        // far apart and rows of a power of two bytes do not all meet in a few
+        // channels of L2.  The last one may be a part.
+        const int steps = (P.K + 63) / 64, whole = min(steps * (wave + 1) / kAdWaves, P.K / 64);
+        int c = steps * wave / kAdWaves;
+        const bool rest = wave == kAdWaves - 1 && P.K % 64 != 0;
+        auto at = [&](int k) { return c + k; };
 #pragma unroll
         for (int s = 0; s < kAhead; s++)
             if (at(s) < whole) load1(s, at(s));
@@ -381,8 +421,8 @@ __global__ void __launch_bounds__(kAdWaves * 64, 2) adapter_kernel(AdapterParams
 #pragma unroll
         for (int s = 0; s < kAhead - 1; s++)
             if (at(kAhead + s) < whole) mul1(s, nothing);
-        c += max(0, (whole - c + kAdWaves - 1) / kAdWaves) * kAdWaves;
-        if (c == whole && c * 64 < P.K) {  // the rest of K
+        if (rest) {
+            c = P.K / 64;
             const bool in = c * 64 + 8 * piece < P.K;
             const int k0 = in ? c * 64 : -8 * piece;  // (the row's start)
             const u32x4 z = {0, 0, 0, 0};
@@ -424,9 +464,10 @@ __global__ void __launch_bounds__(kAdWaves * 64, 2) adapter_kernel(AdapterParams
         for (int k = 0; k < kBLoads; k++) bf[k] = load16(B + (int64_t)n0 * P.R + min(64 * k + lane, units - 1) * 8);
         issue();
     };
-    const int c_step = P.slabs * kAdWaves * kCols;
-    int n0 = (slab * kAdWaves + wave) * kCols;
-    if (n0 < P.N) load2(n0, min(units_b, (P.N - n0) * (P.R / 8)));
+    const int steps2 = (P.N + kCols - 1) / kCols, share = slab * kAdWaves + wave, shares = P.slabs * kAdWaves;
+    int n0 = (int)((int64_t)steps2 * share / shares) * kCols;
+    const int n_end = min((int)((int64_t)steps2 * (share + 1) / shares) * kCols, P.N);
+    if (n0 < n_end) load2(n0, min(units_b, (P.N - n0) * (P.R / 8)));
 
     const float scale = P.scale ? P.scale[a] : 1.0f;
     f32x4* red = reinterpret_cast<f32x4*>(lds);
@@ -512,9 +553,9 @@ __global__ void __launch_bounds__(kAdWaves * 64, 2) adapter_kernel(AdapterParams
         for (int m = 0; m < MB; m++)
 #pragma unroll
             for (int e = 0; e < 4; e++) keep[m][e] = old[m][e];
-        const int next = n0 + c_step;
+        const int next = n0 + kCols;
         issue();
-        if (next < P.N) load2(next, min(units_b, (P.N - next) * r8));
+        if (next < n_end) load2(next, min(units_b, (P.N - next) * r8));
         f32x4 y[MB][NB];
 #pragma unroll
         for (int b = 0; b < NB; b++) {
@@ -550,8 +591,8 @@ __global__ void __launch_bounds__(kAdWaves * 64, 2) adapter_kernel(AdapterParams
                 *reinterpret_cast<vec*>(P.out + out_row[m][e] * P.ld_out + n) = o;
             }
     };
-    for (; n0 + kCols <= P.N; n0 += c_step) step2(n0, std::true_type{});
-    if (n0 < P.N) step2(n0, std::false_type{});
+    for (; n0 + kCols <= n_end; n0 += kCols) step2(n0, std::true_type{});
+    if (n0 < n_end) step2(n0, std::false_type{});
 }
 
 // The adapters that have rows, transposed: At [n][K][R] and Bt [n][R][N].  A
@@ -739,15 +780,14 @@ hipError_t adapter_run(const AdapterParams& P, int64_t tiles, hipStream_t s) {
 
 int adapter_rank_blocks(int32_t R) { return R <= 16 ? 1 : R <= 32 ? 2 : R <= 64 ? 4 : 8; }
 
-// Up to 256 rows take one launch, which groups them itself.
-bool adapter_small(int64_t M) { return M <= 256; }
+// Up to 512 rows, one a thread, take one launch, which groups them itself.
+bool adapter_small(int64_t M) { return M <= kAdWaves * 64; }
 
 hipError_t launch_adapter(AdapterParams P, int64_t tiles, hipStream_t stream) {
     const int cols = P.R <= 32 ? 128 * kAdWaves : 64 * kAdWaves;  // of a step
-    // Few tiles: their columns are shared out, and each share repeats the first
-    // product.  (Of the M workgroups of a small call, those of other rows end at once.)
-    const int64_t working = P.ids ? std::min<int64_t>(P.M, P.n + 1 + P.M / 16) : tiles;
-    P.slabs = (int32_t)std::max<int64_t>(1, std::min<int64_t>((P.N + cols - 1) / cols, 512 / working));
+    if (P.ids) tiles = P.tile_bound = (int32_t)std::min<int64_t>(P.M, P.n + 1 + P.M / 16);
+    // Few tiles: their columns are shared out, and each share repeats the first product.
+    P.slabs = (int32_t)std::max<int64_t>(1, std::min<int64_t>((P.N + cols - 1) / cols, 256 / tiles));
     switch (adapter_rank_blocks(P.R)) {
         case 1: return adapter_run<1>(P, tiles, stream);
         case 2: return adapter_run<2>(P, tiles, stream);

@@ -198,7 +198,7 @@ struct AdapterParams {
     const int32_t* ids;  // a small call, without a plan: [M], or null
     int32_t M, n;
     bool rest;           // the rows without an adapter too
-    int32_t slabs;       // set by the launcher
+    int32_t tile_bound, slabs;  // set by the launcher
     const float* v_in;   // gradients: the forward's v, and the operands that it and w become:
     u32x4 *v_pack, *w_pack;  // [tiles][rank blocks][3][64]
 };
