@@ -247,7 +247,7 @@ __global__ void __launch_bounds__(kPlanThreads) adapter_plan_kernel(AdapterPlan 
 // gives 16 bytes of 16 lines at a time.  So each wavefront reads its operands
 // in whole lines and turns them over in a piece of LDS of its own (16-byte
 // units, exclusive-ored with the row so that operand reads meet no bank twice),
-// the loads two steps ahead in registers; base and out are accessed in runs of
+// the loads a step or two ahead in registers; base and out are accessed in runs of
 // 16 lanes a row, with the second product's columns dealt out so that a lane
 // holds neighbouring ones.
 //
@@ -255,20 +255,27 @@ __global__ void __launch_bounds__(kPlanThreads) adapter_plan_kernel(AdapterPlan 
 // kGrad: V and the forward's v also go, as three BF16 values, to the operands
 // of the weights' gradients.
 // kSmall: at most 512 rows, without a plan: every workgroup groups them itself.
+// The gradient's A and B, which are copies anyway, come from rank 33 on as the
+// products' operands (adapter_pack_kernel) and need not be turned over: 69
+// against 92 us at 8192 rows, rank 64 and 4096 columns; at rank 16, where the
+// second product's would be twice as long, 88 against 79 us for 128 experts.  (A
+// forward pass that packs first gains less than the packing takes.)
 template <int RB, int MB, bool kGrad, bool kBase, bool kSmall>
-__global__ void __launch_bounds__(kAdWaves * 64, 2) adapter_kernel(AdapterParams P) {
+__global__ void __launch_bounds__(kAdWaves * 64, RB < 4 || (RB == 4 && kGrad) ? 4 : 2) adapter_kernel(AdapterParams P) {
+    constexpr bool kPacked = kGrad && RB >= 4;
     constexpr int kR = 16 * RB, kPieces = kGrad ? 3 : 2, kPitch = kPieces * kR + 8;
-    constexpr int kRound = RB * MB < 8 ? RB * MB : 8;  // blocks of V joined at a time
-    constexpr int kA = RB < 4 ? RB : 4;                // rank blocks turned over at a time
+    constexpr int kMost = kPacked ? 4 : 8, kRound = RB * MB < kMost ? RB * MB : kMost;  // blocks of V joined at a time
+    constexpr int kA = RB < 2 ? RB : 2;                // rank blocks turned over at a time
     // Steps of the first product whose loads are in registers.
-    constexpr int kAhead = kSmall && RB < 2 ? 4 : RB < 8 ? 2 : 1;
-    constexpr int NB = RB < 4 ? 8 : 4, kCols = 16 * NB;  // neighbouring columns of a lane; columns of a step
+    constexpr int kAhead = RB < 2 || (RB < 4 && MB < 2) || (RB == 4 && !kPacked) ? 2 : 1;
+    constexpr int NB = 4, kCols = 16 * NB;  // neighbouring columns of a lane; columns of a step
     constexpr int kB = (RB + 1) / 2, kBLoads = NB * RB / 2;  // operands a column; 16-byte loads of B a lane and step
-    constexpr int kUnits1 = (MB + kA) * 128, kUnits2 = kBLoads * 64, kUnits = kUnits1 > kUnits2 ? kUnits1 : kUnits2;
+    constexpr int kUnits1 = (MB + (kPacked ? 0 : kA)) * 128, kUnits2 = kPacked ? 0 : kBLoads * 64, kUnits = kUnits1 > kUnits2 ? kUnits1 : kUnits2;
     constexpr int kRed = kRound * kAdWaves * 64;
     // Units of 16 bytes: the wavefronts' pieces, and in between their sums.
     __shared__ __attribute__((aligned(16))) u32x4 lds[kAdWaves * kUnits > kRed ? kAdWaves * kUnits : kRed];
     __shared__ __attribute__((aligned(16))) uint16_t vs[16 * MB][kPitch];
+    __shared__ int64_t base_at[16 * MB], out_at[16 * MB];  // where the rows start, in bytes
     const int lane = threadIdx.x & 63, i = lane & 15, q = lane >> 4;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     u32x4* own = lds + wave * kUnits;
@@ -357,6 +364,7 @@ __global__ void __launch_bounds__(kAdWaves * 64, 2) adapter_kernel(AdapterParams
 #pragma unroll
     for (int k = 0; k < 2 * MB; k++) xr[k] = P.x + row_of(8 * k + sub) * P.ldx + 8 * piece;
     const uint16_t* ar = P.A + ((int64_t)a * P.R + sub) * P.K + 8 * piece;
+    const u32x4* a_pack = reinterpret_cast<const u32x4*>(P.A) + a * P.units_a + lane;
     u32x4 xf[kAhead][2 * MB], af[kAhead][2 * RB];
     f32x4 acc[RB][MB];
 #pragma unroll
@@ -367,13 +375,34 @@ __global__ void __launch_bounds__(kAdWaves * 64, 2) adapter_kernel(AdapterParams
 #pragma unroll
         for (int k = 0; k < 2 * MB; k++) xf[s][k] = load16(xr[k] + c * 64);
 #pragma unroll
-        for (int k = 0; k < 2 * RB; k++) af[s][k] = load16(ar + (int64_t)min(8 * k, P.R - 8) * P.K + c * 64);
+        for (int k = 0; k < 2 * RB; k++)
+            if constexpr (kPacked)
+                af[s][k] = a_pack[((int64_t)c * (2 * RB) + k) * 64];
+            else
+                af[s][k] = load16(ar + (int64_t)min(8 * k, P.R - 8) * P.K + c * 64);
         issue();
     };
     auto mul1 = [&](int s, auto next) {
         u32x4* put = own + sub * 8 + (piece ^ sub);
 #pragma unroll
         for (int k = 0; k < 2 * MB; k++) put[64 * k] = xf[s][k];
+        if constexpr (kPacked) {
+            issue();
+#pragma unroll
+            for (int h = 0; h < 2; h++) {
+                const u32x4* at = own + i * 8 + ((4 * h + q) ^ (i & 7));
+                u32x4 x[MB];
+#pragma unroll
+                for (int m = 0; m < MB; m++) x[m] = at[128 * m];
+#pragma unroll
+                for (int r = 0; r < RB; r++)
+#pragma unroll
+                    for (int m = 0; m < MB; m++) acc[r][m] = mfma16(af[s][h * RB + r], x[m], acc[r][m]);
+            }
+            issue();
+            next();
+            return;
+        }
 #pragma unroll
         for (int r0 = 0; r0 < RB; r0 += kA) {
 #pragma unroll
@@ -433,8 +462,12 @@ __global__ void __launch_bounds__(kAdWaves * 64, 2) adapter_kernel(AdapterParams
             }
 #pragma unroll
             for (int k = 0; k < 2 * RB; k++) {
-                af[0][k] = load16(ar + (int64_t)min(8 * k, P.R - 8) * P.K + k0);
-                if (!in) af[0][k] = z;
+                if constexpr (kPacked) {
+                    af[0][k] = a_pack[((int64_t)c * (2 * RB) + k) * 64];
+                } else {
+                    af[0][k] = load16(ar + (int64_t)min(8 * k, P.R - 8) * P.K + k0);
+                    if (!in) af[0][k] = z;
+                }
             }
             mul1(0, nothing);
         }
@@ -443,23 +476,23 @@ __global__ void __launch_bounds__(kAdWaves * 64, 2) adapter_kernel(AdapterParams
     // The second product, kCols columns a step: lane i has columns NB i .. + NB - 1
     // of rows 4 q .. + 3 of each block; product b takes columns NB n + b.
     typedef uint32_t vec __attribute__((ext_vector_type(NB / 2)));
-    uint32_t out_row[MB][4];
-#pragma unroll
-    for (int m = 0; m < MB; m++)
-#pragma unroll
-        for (int e = 0; e < 4; e++) out_row[m][e] = (uint32_t)row_of(16 * m + 4 * q + e);
+    if (threadIdx.x < 16 * MB) {
+        const int64_t r = row_of(threadIdx.x);
+        base_at[threadIdx.x] = 2 * r * P.ld_base;
+        out_at[threadIdx.x] = 2 * r * P.ld_out;
+    }
     const uint16_t* B = P.B + (int64_t)a * P.N * P.R;
     const int units_b = kCols * P.R / 8;  // of B in a step: consecutive
-    vec old[MB][4];
-    u32x4 bf[kBLoads];
-    auto load2 = [&](int n0, int units) {  // `units` of B, at most units_b, and columns from n0 on exist
-        if (kBase) {
-            const int n = min(n0 + NB * i, P.N - NB);
+    u32x4 bf[kPacked ? NB * kB : kBLoads];
+    const u32x4* b_pack = reinterpret_cast<const u32x4*>(P.B) + a * P.units_b + lane;
+    auto load_b = [&](int n0) {  // (past the last column, its last unit)
+        if constexpr (kPacked) {
 #pragma unroll
-            for (int m = 0; m < MB; m++)
-#pragma unroll
-                for (int e = 0; e < 4; e++) old[m][e] = *reinterpret_cast<const vec*>(P.base + out_row[m][e] * P.ld_base + n);
+            for (int k = 0; k < NB * kB; k++) bf[k] = b_pack[((int64_t)(n0 / kCols) * (NB * kB) + k) * 64];
+            issue();
+            return;
         }
+        const int units = min(units_b, (P.N - n0) * (P.R / 8));
 #pragma unroll
         for (int k = 0; k < kBLoads; k++) bf[k] = load16(B + (int64_t)n0 * P.R + min(64 * k + lane, units - 1) * 8);
         issue();
@@ -467,7 +500,6 @@ __global__ void __launch_bounds__(kAdWaves * 64, 2) adapter_kernel(AdapterParams
     const int steps2 = (P.N + kCols - 1) / kCols, share = slab * kAdWaves + wave, shares = P.slabs * kAdWaves;
     int n0 = (int)((int64_t)steps2 * share / shares) * kCols;
     const int n_end = min((int)((int64_t)steps2 * (share + 1) / shares) * kCols, P.N);
-    if (n0 < n_end) load2(n0, min(units_b, (P.N - n0) * (P.R / 8)));
 
     const float scale = P.scale ? P.scale[a] : 1.0f;
     f32x4* red = reinterpret_cast<f32x4*>(lds);
@@ -479,6 +511,7 @@ __global__ void __launch_bounds__(kAdWaves * 64, 2) adapter_kernel(AdapterParams
 #pragma unroll
             for (int m = 0; m < MB; m++)
                 if (r * MB + m >= j0 && r * MB + m < j0 + kRound) red[(wave * kRound + r * MB + m - j0) * 64 + lane] = acc[r][m];
+        if (j0 + kRound == RB * MB && n0 < n_end) load_b(n0);
         __syncthreads();
         if (wave < kRound) {
             const int j = j0 + wave, m = j % MB, r = j / MB * 16 + 4 * q;  // the lane's ranks r .. r + 3 of row i
@@ -537,42 +570,54 @@ __global__ void __launch_bounds__(kAdWaves * 64, 2) adapter_kernel(AdapterParams
         }
     }
 
-    u32x4 vf[MB][RB];
-#pragma unroll
-    for (int m = 0; m < MB; m++)
-#pragma unroll
-        for (int j = 0; j < RB; j++) vf[m][j] = *reinterpret_cast<const u32x4*>(&vs[16 * m + i][32 * j + 8 * q]);
     // Unit p of B's piece lies at p ^ ((p / 16) ^ (p / 64)) % 16: reads of one
     // product are 16 NB rows apart, and these differ in that term.
     const int r8 = P.R / 8;
     auto step2 = [&](int n0, auto whole) {
+        vec old[MB][4];
+        const int n = n0 + NB * i;
+        if (kBase) {
+            const uint8_t* at = reinterpret_cast<const uint8_t*>(P.base + (whole.value ? n : min(n, P.N - NB)));
 #pragma unroll
-        for (int k = 0; k < kBLoads; k++) own[64 * k + (lane ^ (lane >> 4) ^ ((4 * k ^ k) & 15))] = bf[k];
-        vec keep[MB][4];
+            for (int m = 0; m < MB; m++)
 #pragma unroll
-        for (int m = 0; m < MB; m++)
-#pragma unroll
-            for (int e = 0; e < 4; e++) keep[m][e] = old[m][e];
-        const int next = n0 + kCols;
+                for (int e = 0; e < 4; e++) old[m][e] = *reinterpret_cast<const vec*>(at + base_at[16 * m + 4 * q + e]);
+        }
         issue();
-        if (next < n_end) load2(next, min(units_b, (P.N - next) * r8));
+        if constexpr (!kPacked) {
+#pragma unroll
+            for (int k = 0; k < kBLoads; k++) own[64 * k + (lane ^ (lane >> 4) ^ ((4 * k ^ k) & 15))] = bf[k];
+            issue();
+            if (n0 + kCols < n_end) load_b(n0 + kCols);
+        }
         f32x4 y[MB][NB];
 #pragma unroll
-        for (int b = 0; b < NB; b++) {
+        for (int b = 0; b < NB; b++)
 #pragma unroll
             for (int m = 0; m < MB; m++) y[m][b] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-            u32x4 w[kB];
 #pragma unroll
-            for (int j = 0; j < kB; j++) {
+        for (int j = 0; j < kB; j++) {
+            u32x4 w[NB];
+#pragma unroll
+            for (int b = 0; b < NB; b++) {
                 const int p = (NB * i + b) * r8 + min(RB == 1 ? q & 1 : 4 * j + q, r8 - 1);
-                w[j] = own[p ^ (((p >> 4) ^ (p >> 6)) & 15)];
+                w[b] = kPacked ? bf[kPacked ? b * kB + j : 0] : own[p ^ (((p >> 4) ^ (p >> 6)) & 15)];
             }
 #pragma unroll
-            for (int j = RB - 1; j >= 0; j--)
+            for (int h = RB > 1 ? 1 : 0; h >= 0; h--) {  // the second part of V first
+                u32x4 v[MB];
 #pragma unroll
-                for (int m = 0; m < MB; m++) y[m][b] = mfma16(vf[m][j], w[j % kB], y[m][b]);
+                for (int m = 0; m < MB; m++) v[m] = *reinterpret_cast<const u32x4*>(&vs[16 * m + i][32 * (j + h * kB) + 8 * q]);
+#pragma unroll
+                for (int b = 0; b < NB; b++)
+#pragma unroll
+                    for (int m = 0; m < MB; m++) y[m][b] = mfma16(v[m], w[b], y[m][b]);
+            }
         }
-        const int n = n0 + NB * i;
+        if constexpr (kPacked) {
+            issue();
+            if (n0 + kCols < n_end) load_b(n0 + kCols);
+        }
         if (!whole.value && n >= P.N) return;
 #pragma unroll
         for (int m = 0; m < MB; m++)
@@ -583,38 +628,58 @@ __global__ void __launch_bounds__(kAdWaves * 64, 2) adapter_kernel(AdapterParams
                 for (int k = 0; k < NB / 2; k++) {
                     float lo = y[m][2 * k][e], hi = y[m][2 * k + 1][e];
                     if (kBase) {
-                        lo += __uint_as_float(keep[m][e][k] << 16);
-                        hi += __uint_as_float(keep[m][e][k] & 0xFFFF0000u);
+                        lo += __uint_as_float(old[m][e][k] << 16);
+                        hi += __uint_as_float(old[m][e][k] & 0xFFFF0000u);
                     }
                     o[k] = bf16_hw(lo) | (bf16_hw(hi) << 16);
                 }
-                *reinterpret_cast<vec*>(P.out + out_row[m][e] * P.ld_out + n) = o;
+                *reinterpret_cast<vec*>(reinterpret_cast<uint8_t*>(P.out + n) + out_at[16 * m + 4 * q + e]) = o;
             }
     };
     for (; n0 + kCols <= n_end; n0 += kCols) step2(n0, std::true_type{});
     if (n0 < n_end) step2(n0, std::false_type{});
 }
 
-// The adapters that have rows, transposed: At [n][K][R] and Bt [n][R][N].  A
-// thread turns 8 x 8 elements over in registers, one byte permutation each two.
-__global__ void __launch_bounds__(256) adapter_transpose_kernel(AdapterGrad P) {
+// B^T and A^T, which take the places of A and B in the gradient's products, of
+// the adapters that have rows.  Up to rank 32 (RB 0) as matrices [R][N] and
+// [K][R]; from there as operands, ranks padded with zeros to 16 RB, N and K to
+// multiples of 64, in units of 16 bytes (8 elements):
+//   first product:  rank r, inputs 8 k .. + 7: ((k / 4) RB + r / 16) 64 + k % 4 * 16 + r % 16
+//   second product: column c, ranks 8 r .. + 7: ((c / 64 * 4 + c % 4) RB / 2 + r / 4) 64 + r % 4 * 16 + c % 64 / 4
+// A thread turns 8 x 8 elements over with one byte permutation each two.
+template <int RB>
+__global__ void __launch_bounds__(256) adapter_pack_kernel(AdapterPack P) {
     const int a = blockIdx.y;
     if (P.info[a].x == 0) return;
-    const uint32_t rb = (uint32_t)P.R / 8, of_a = rb * (P.K / 8), of_b = rb * (P.N / 8);
+    const uint32_t r8 = RB ? 2 * RB : P.R / 8, k8 = RB ? (P.K + 63) / 64 * 8 : P.K / 8, n8 = RB ? (P.N + 63) / 64 * 8 : P.N / 8;
     uint32_t k = blockIdx.x * 256 + threadIdx.x;
-    const bool is_a = k < of_a;
-    if (!is_a) k -= of_a;
-    if (!is_a && k >= of_b) return;
-    // in [rows][cols] -> out [cols][rows]; neighbouring lanes along in's columns
-    const int64_t rows = is_a ? P.R : P.N, cols = is_a ? P.K : P.R;
-    const int64_t r0 = k / (cols / 8) * 8, c0 = k % (cols / 8) * 8;
-    const uint16_t* in = (is_a ? P.A : P.B) + a * rows * cols + r0 * cols + c0;
-    uint16_t* out = (is_a ? P.At : P.Bt) + a * rows * cols + c0 * rows + r0;
+    const bool is_a = k < r8 * k8;
+    if (!is_a) k -= r8 * k8;
+    if (!is_a && k >= r8 * n8) return;
+    // 8 ranks from 8 r on, and 8 columns of A or rows of B from 8 c on
+    const uint32_t r = is_a ? k / k8 : k % r8, c = is_a ? k % k8 : k / r8;
+    const bool in = RB == 0 || (8 * (int)r < P.R && 8 * (int)c < (is_a ? P.K : P.N));
+    const uint16_t* at = in ? is_a ? P.A + ((int64_t)a * P.R + 8 * r) * P.K + 8 * c : P.B + ((int64_t)a * P.N + 8 * c) * P.R + 8 * r : P.A;
+    const int64_t ld = in ? is_a ? P.K : P.R : 0;
     u32x4 z[8];
 #pragma unroll
-    for (int j = 0; j < 8; j++) z[j] = load16(in + j * cols);
+    for (int j = 0; j < 8; j++) z[j] = load16(at + j * ld);
+    if (!in)
 #pragma unroll
-    for (int c = 0; c < 8; c++) *reinterpret_cast<u32x4*>(out + c * rows) = column8(z, c);
+        for (int j = 0; j < 8; j++) z[j] = u32x4{0, 0, 0, 0};
+    u32x4* out = is_a ? P.second + a * P.units_second : P.first + a * P.units_first;
+#pragma unroll
+    for (int j = 0; j < 8; j++) {
+        // of A: column 8 c + j, ranks 8 r ..; of B: rank 8 r + j, rows 8 c ..
+        uint32_t to;
+        if (RB == 0)
+            to = is_a ? (8 * c + j) * r8 + r : (8 * r + j) * n8 + c;
+        else if (is_a)
+            to = ((((8 * c + j) >> 6) * 4 + (j & 3)) * (RB / 2) + (r >> 2)) * 64 + (r & 3) * 16 + (((8 * c + j) & 63) >> 2);
+        else
+            to = ((c >> 2) * RB + ((8 * r + j) >> 4)) * 64 + (c & 3) * 16 + ((8 * r + j) & 15);
+        out[to] = column8(z, j);
+    }
 }
 
 // dA and dB of one row chunk and 128 columns: the sum over rows is the matrix
@@ -757,23 +822,20 @@ hipError_t launch_adapter_plan(AdapterPlan P, hipStream_t stream) {
 
 namespace {
 
-template <int RB, bool kGrad, bool kBase>
-void adapter_start(const AdapterParams& P, int64_t tiles, hipStream_t s) {
+template <int RB, bool kBase>
+hipError_t adapter_start(const AdapterParams& P, int64_t tiles, hipStream_t s) {
     const dim3 grid((unsigned)((tiles * P.slabs + 7) / 8 * 8)), block(kAdWaves * 64);
-    if constexpr (!kGrad)
-        if (P.ids) {
-            hipLaunchKernelGGL((adapter_kernel<RB, 1, false, kBase, true>), grid, block, 0, s, P);
-            return;
-        }
-    hipLaunchKernelGGL((adapter_kernel<RB, kAdTile / 16, kGrad, kBase, false>), grid, block, 0, s, P);
+    if (P.w_pack)
+        hipLaunchKernelGGL((adapter_kernel<RB, kAdTile / 16, true, kBase, false>), grid, block, 0, s, P);
+    else if (P.ids)
+        hipLaunchKernelGGL((adapter_kernel<RB, 1, false, kBase, true>), grid, block, 0, s, P);
+    else
+        hipLaunchKernelGGL((adapter_kernel<RB, adapter_tile(16 * RB) / 16, false, kBase, false>), grid, block, 0, s, P);
+    return hipGetLastError();
 }
 template <int RB>
 hipError_t adapter_run(const AdapterParams& P, int64_t tiles, hipStream_t s) {
-    if (P.w_pack)
-        P.base ? adapter_start<RB, true, true>(P, tiles, s) : adapter_start<RB, true, false>(P, tiles, s);
-    else
-        P.base ? adapter_start<RB, false, true>(P, tiles, s) : adapter_start<RB, false, false>(P, tiles, s);
-    return hipGetLastError();
+    return P.base ? adapter_start<RB, true>(P, tiles, s) : adapter_start<RB, false>(P, tiles, s);
 }
 
 }  // namespace
@@ -784,7 +846,7 @@ int adapter_rank_blocks(int32_t R) { return R <= 16 ? 1 : R <= 32 ? 2 : R <= 64 
 bool adapter_small(int64_t M) { return M <= kAdWaves * 64; }
 
 hipError_t launch_adapter(AdapterParams P, int64_t tiles, hipStream_t stream) {
-    const int cols = P.R <= 32 ? 128 * kAdWaves : 64 * kAdWaves;  // of a step
+    const int cols = 64 * kAdWaves;  // of a step
     if (P.ids) tiles = P.tile_bound = (int32_t)std::min<int64_t>(P.M, P.n + 1 + P.M / 16);
     // Few tiles: their columns are shared out, and each share repeats the first product.
     P.slabs = (int32_t)std::max<int64_t>(1, std::min<int64_t>((P.N + cols - 1) / cols, 256 / tiles));
@@ -803,9 +865,19 @@ int32_t adapter_chunk(int64_t M, int64_t K, int64_t N) {
     return (int32_t)std::min<int64_t>((std::max<int64_t>(M, 1) + 128 * chunks - 1) / (128 * chunks) * 128, (int64_t)1 << 30);
 }
 
-hipError_t launch_adapter_transpose(const AdapterGrad& P, hipStream_t stream) {
-    const unsigned blocks = P.R / 8 * (P.K / 8 + P.N / 8);  // of 8 x 8
-    hipLaunchKernelGGL(adapter_transpose_kernel, dim3((blocks + 255) / 256, P.n), dim3(256), 0, stream, P);
+int64_t adapter_units(int64_t cols, int32_t R) {
+    return R <= 32 ? cols * R / 8 : (cols + 63) / 64 * 128 * adapter_rank_blocks(R);
+}
+
+hipError_t launch_adapter_pack(const AdapterPack& P, hipStream_t stream) {
+    const unsigned blocks = (unsigned)((adapter_units(P.K, P.R) + adapter_units(P.N, P.R)) / 8);  // of 8 x 8
+    const dim3 grid((blocks + 255) / 256, P.n);
+    if (P.R <= 32)
+        hipLaunchKernelGGL(adapter_pack_kernel<0>, grid, dim3(256), 0, stream, P);
+    else if (P.R <= 64)
+        hipLaunchKernelGGL(adapter_pack_kernel<4>, grid, dim3(256), 0, stream, P);
+    else
+        hipLaunchKernelGGL(adapter_pack_kernel<8>, grid, dim3(256), 0, stream, P);
     return hipGetLastError();
 }
 

@@ -233,26 +233,27 @@ int adapter_planes(const nvfp4moe_adapters* ad) {
 // Workspace: the plan (rows by adapter, its tables) and, for the gradients, the
 // transposed adapters, w and v as operands and partial sums.
 struct AdapterWork {
-    size_t order, tiles, chunks, steps, info, at, bt, v_pack, w_pack, slots, total;
+    size_t order, tiles, chunks, steps, info, first, second, v_pack, w_pack, slots, total;
     int64_t n_tiles, n_chunks;
     int32_t chunk;
 };
 AdapterWork adapter_work(const nvfp4moe_adapters* ad, int64_t M, bool backward) {
     AdapterWork w{};
     const int64_t n = ad->n, R = ad->rank, K = ad->in_features, N = ad->out_features;
-    w.n_tiles = M / kAdTile + std::min(M, n + 1);
+    w.n_tiles = M / (backward ? kAdTile : adapter_tile(ad->rank)) + std::min(M, n + 1);
     w.order = kAlign;
     w.tiles = w.order + up(M * 4, kAlign);
     w.total = w.tiles + up(w.n_tiles * 16, kAlign);
     if (!backward) return w;
+    w.info = w.total;
+    w.first = w.info + up(n * 8, kAlign);
+    w.second = w.first + up(n * adapter_units(N, ad->rank) * 16, kAlign);
+    w.total = w.second + up(n * adapter_units(K, ad->rank) * 16, kAlign);
     w.chunk = adapter_chunk(M, K, N);
     w.n_chunks = M / w.chunk + std::min(M, n);
     w.chunks = w.total;
     w.steps = w.chunks + up(w.n_chunks * 16, kAlign);
-    w.info = w.steps + up(w.n_chunks * 4, kAlign);
-    w.at = w.info + up(n * 8, kAlign);
-    w.bt = w.at + up(n * R * K * 2, kAlign);
-    w.v_pack = w.bt + up(n * R * N * 2, kAlign);
+    w.v_pack = w.steps + up(w.n_chunks * 4, kAlign);
     w.w_pack = w.v_pack + (size_t)w.n_tiles * adapter_rank_blocks(ad->rank) * 3 * 1024;
     w.slots = 2 * w.w_pack - w.v_pack;
     // chunks of adapters that have more than one: each such adapter has more
@@ -517,7 +518,7 @@ int nvfp4moe_adapter_linear(const nvfp4moe_adapters* ad, const uint16_t* x, int6
     plan.ids = ids;
     plan.M = M;
     plan.n = ad->n;
-    plan.tile = kAdTile;
+    plan.tile = adapter_tile(ad->rank);
     plan.rest = p.rest;
     plan.n_tables = (int32_t*)ws;
     plan.order = (int32_t*)(ws + w.order);
@@ -563,15 +564,11 @@ int nvfp4moe_adapter_backward(const nvfp4moe_adapters* ad, const uint16_t* x, in
     plan.info = (int2*)(ws + w.info);
     if (launch_adapter_plan(plan, s) != hipSuccess) return NVFP4_E_HIP;
     AdapterGrad g{};
-    g.A = ad->A;
-    g.B = ad->B;
     g.scale = ad->scale;
     g.n = ad->n;
     g.R = ad->rank;
     g.K = K;
     g.N = N;
-    g.At = (uint16_t*)(ws + w.at);
-    g.Bt = (uint16_t*)(ws + w.bt);
     g.x = x;
     g.dy = dy;
     g.ldx = ldx;
@@ -588,12 +585,26 @@ int nvfp4moe_adapter_backward(const nvfp4moe_adapters* ad, const uint16_t* x, in
     g.dA = dA;
     g.dB = dB;
     if (M > 0) {
-        if (launch_adapter_transpose(g, s) != hipSuccess) return NVFP4_E_HIP;
+        AdapterPack k{};
+        k.A = ad->A;
+        k.B = ad->B;
+        k.info = plan.info;
+        k.n = ad->n;
+        k.R = ad->rank;
+        k.K = K;
+        k.N = N;
+        k.first = (u32x4*)(ws + w.first);
+        k.second = (u32x4*)(ws + w.second);
+        k.units_first = adapter_units(N, ad->rank);
+        k.units_second = adapter_units(K, ad->rank);
+        if (launch_adapter_pack(k, s) != hipSuccess) return NVFP4_E_HIP;
         AdapterParams p{};
+        p.A = (const uint16_t*)k.first;
+        p.B = (const uint16_t*)k.second;
+        p.units_a = k.units_first;
+        p.units_b = k.units_second;
         p.x = dy;
         p.ldx = ld_dy;
-        p.A = g.Bt;
-        p.B = g.At;
         p.scale = ad->scale;
         p.R = ad->rank;
         p.K = N;

@@ -163,7 +163,8 @@ hipError_t launch_balance(const BalanceParams& P, bool bf16, hipStream_t stream)
 
 // Low-rank adapters and their gradients (adapter.hip).
 constexpr int kMaxRank = 128;
-constexpr int kAdTile = 32;  // rows of a row tile, and of a step of the weights' gradients
+constexpr int kAdTile = 32;  // rows of a row tile of the gradients, a step of the weights' own
+constexpr int adapter_tile(int32_t R) { return R <= 32 ? 16 : 32; }  // and of the forward pass
 struct AdapterPlan {  // rows grouped by adapter
     const int32_t* ids;  // [M]
     int64_t M;
@@ -183,8 +184,9 @@ hipError_t launch_adapter_plan(AdapterPlan P, hipStream_t stream);
 struct AdapterParams {
     const uint16_t* x;
     int64_t ldx;
-    const uint16_t* A;   // [n][R][K]
+    const uint16_t* A;   // [n][R][K] (the gradient's: from adapter_pack_kernel)
     const uint16_t* B;   // [n][N][R]
+    int64_t units_a, units_b;  // the gradient's: 16-byte units of an adapter
     const float* scale;  // [n] or null
     int32_t R, K, N;
     const uint16_t* base;  // or null
@@ -205,13 +207,20 @@ struct AdapterParams {
 int adapter_rank_blocks(int32_t R);  // blocks of 16 ranks that the kernels compute
 bool adapter_small(int64_t M);
 hipError_t launch_adapter(AdapterParams P, int64_t tiles_bound, hipStream_t stream);
-struct AdapterGrad {
+struct AdapterPack {  // B^T and A^T for the gradient's products
     const uint16_t* A;
     const uint16_t* B;
+    const int2* info;    // [n]: only adapters with rows
+    int32_t n, R, K, N;
+    u32x4* first;        // [n][units_first]
+    u32x4* second;
+    int64_t units_first, units_second;
+};
+int64_t adapter_units(int64_t cols, int32_t R);  // units of 16 bytes of one adapter's transposed matrix
+hipError_t launch_adapter_pack(const AdapterPack& P, hipStream_t stream);
+struct AdapterGrad {
     const float* scale;
     int32_t n, R, K, N;
-    uint16_t* At;        // [n][K][R]
-    uint16_t* Bt;        // [n][R][N]
     const uint16_t* x;
     const uint16_t* dy;
     int64_t ldx, ld_dy;
@@ -227,7 +236,6 @@ struct AdapterGrad {
     float* dB;
 };
 int32_t adapter_chunk(int64_t M, int64_t K, int64_t N);
-hipError_t launch_adapter_transpose(const AdapterGrad& P, hipStream_t stream);
 hipError_t launch_adapter_wgrad(const AdapterGrad& P, int64_t chunks_bound, hipStream_t stream);
 
 // MXFP4 quantizers (mxfp4_quant.hip) and products (mxfp4_gemm.hip).
