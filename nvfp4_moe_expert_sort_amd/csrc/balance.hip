@@ -16,7 +16,9 @@ namespace nvfp4 {
 
 namespace {
 
-constexpr int kBalThreads = 256;
+constexpr int kBalThreads = 256;     // of the gradient
+constexpr int kChunkThreads = 1024;  // of the loss: 64 tokens at a time, or 16
+constexpr int kJoinThreads = 1024;   // 16 stripes of 64 experts
 
 // e^d for d <= 0 within a few 2^-24 wherever it is a normal number: the part
 // of d log2 e that its rounding to FP32 drops is put back to first order.
@@ -29,6 +31,14 @@ __device__ __forceinline__ float exp_neg(float d) {
     return __builtin_fmaf(e, r * 0.693147182f, e);
 }
 
+// Sum over a wavefront, in all lanes, in one order.
+template <typename T>
+__device__ __forceinline__ T wave_sum(T v) {
+#pragma unroll
+    for (int o = 32; o > 0; o >>= 1) v += __shfl_xor(v, o, kWave);
+    return v;
+}
+
 // Terms w_e >= 0 of the token's probabilities, p_e = w_e / sum w, from its
 // clean logits; for sigmoid scores other = 1 - sigma.  Both are shifted so
 // that the sum cannot vanish: by the largest logit, or for sigmoid scores by
@@ -39,7 +49,16 @@ __device__ __forceinline__ void score_terms(const float (&l)[NV], bool sigmoid, 
 #pragma unroll
     for (int i = 1; i < NV; i++) mx = max32(mx, l[i]);
     mx = max32(tok_max<LT>(mx), -kFltMax);
-    if (sigmoid) {
+    if (sigmoid && __ballot(mx < 0.0f) == 0) {  // (no token of the wavefront has m < 0: e^(l - m) is e^-|l| again)
+#pragma unroll
+        for (int i = 0; i < NV; i++) {
+            const bool neg = l[i] < 0.0f;
+            const float t = exp_neg(-fabsf(l[i])), inv = __builtin_amdgcn_rcpf(1.0f + t), ti = t * inv;
+            w[i] = neg ? ti : inv;
+            w[i] = l[i] > -__builtin_inff() ? w[i] : 0.0f;
+            other[i] = neg ? inv : ti;
+        }
+    } else if (sigmoid) {
         mx = min32(mx, 0.0f);
 #pragma unroll
         for (int i = 0; i < NV; i++) {
@@ -64,16 +83,28 @@ __device__ __forceinline__ int64_t seq_start(const BalanceParams& P, int32_t s) 
 }
 // The sequence that holds row t, -1 before the first and S behind the last:
 // how many of the S + 1 offsets are <= t, less one.  All threads call it.
+template <int kThreads>
 __device__ __forceinline__ int32_t find_sequence(const BalanceParams& P, int64_t t, int32_t* lds) {
     if (!P.offsets) return 0;
     int32_t n = 0;
-    for (int32_t i = threadIdx.x; i <= P.S; i += kBalThreads) n += seq_start(P, i) <= t ? 1 : 0;
-#pragma unroll
-    for (int o = 32; o > 0; o >>= 1) n += __shfl_xor(n, o, kWave);
+    if (P.S < 256) {  // every wavefront by itself
+        for (int32_t i = threadIdx.x & 63; i <= P.S; i += 64) n += seq_start(P, i) <= t ? 1 : 0;
+        return wave_sum(n) - 1;
+    }
+    for (int32_t i = threadIdx.x; i <= P.S; i += kThreads) n += seq_start(P, i) <= t ? 1 : 0;
+    n = wave_sum(n);
     __syncthreads();
     if ((threadIdx.x & 63) == 0) lds[threadIdx.x >> 6] = n;
     __syncthreads();
-    return lds[0] + lds[1] + lds[2] + lds[3] - 1;
+    n = 0;
+    for (int w = 0; w < kThreads / 64; w++) n += lds[w];
+    return n - 1;
+}
+
+// The loss of sum_s 1 / T_s sum_e n_se sum_t p_te.
+__device__ __forceinline__ float balance_scaled(const BalanceParams& P, double total) {
+    const double tokens = (double)max(seq_start(P, P.S) - seq_start(P, 0), (int64_t)1);
+    return (float)(total * (double)P.coef * (double)P.E / ((double)P.K * tokens));
 }
 
 template <int LT, int NV, typename L>
@@ -90,28 +121,30 @@ __device__ __forceinline__ void load_row(const L* row, const BalanceParams& P, i
 }  // namespace
 
 // A workgroup takes P.chunk rows.  For each sequence in them it adds up the
-// probabilities (a lane its own experts over its tokens, then the token slots
-// in LDS) and the counts; chunk b's part of sequence s goes to slot b + s: a
-// walk along the rows raises b or s at every step, so no two parts share one.
+// probabilities (a lane its own experts over its tokens, then the wavefront's
+// token slots by exchanges, then the wavefronts in LDS) and the counts; chunk
+// b's part of sequence s goes to slot b + s: a walk along the rows raises b or s
+// at every step, so no two parts share one.  A call of one chunk has its
+// sequences whole here and needs no join.
 template <int LT, int NV, typename L>
-__global__ void __launch_bounds__(kBalThreads) balance_chunk_kernel(BalanceParams P) {
-    constexpr int kTok = kBalThreads / LT;
-    __shared__ float part[kTok][LT * NV];
+__global__ void __launch_bounds__(kChunkThreads) balance_chunk_kernel(BalanceParams P) {
+    constexpr int kTok = kChunkThreads / LT, kWaves = kChunkThreads / 64;
+    __shared__ float part[kWaves][LT * NV];
     __shared__ int32_t hist[LT * NV];
-    __shared__ int32_t found[4];
-    const int lane = threadIdx.x & (LT - 1), slot = threadIdx.x / LT;
+    __shared__ int32_t found[kWaves];
+    __shared__ double shares[kWaves];
+    const int lane = threadIdx.x & (LT - 1), slot = threadIdx.x / LT, wave = threadIdx.x >> 6;
     const int64_t first = (int64_t)blockIdx.x * P.chunk, past = min(P.T, first + P.chunk);
+    const bool whole = gridDim.x == 1;
+    double total = 0.0;  // whole: of loss / factor
+    int32_t s_next = 0;
     if (blockIdx.x == 0 && threadIdx.x == 0) *P.done = 0;
-    for (int32_t s = max(find_sequence(P, first, found), 0); s < P.S; s++) {
+    for (int32_t s = max(find_sequence<kChunkThreads>(P, first, found), 0); s < P.S; s++) {
         const int64_t s0 = seq_start(P, s), lo = max(s0, first), hi = min(seq_start(P, s + 1), past);
         if (s0 >= past) break;
         if (lo >= hi) continue;
-        for (int e = threadIdx.x; e < P.E; e += kBalThreads) hist[e] = 0;
+        for (int e = threadIdx.x; e < P.E; e += kChunkThreads) hist[e] = 0;
         __syncthreads();
-        for (int64_t i = lo * P.K + threadIdx.x; i < hi * P.K; i += kBalThreads) {
-            const int32_t e = P.ids[i];
-            if (e >= 0 && e < P.E) atomicAdd(&hist[e], 1);
-        }
         float acc[NV];
 #pragma unroll
         for (int i = 0; i < NV; i++) acc[i] = 0.0f;
@@ -119,6 +152,11 @@ __global__ void __launch_bounds__(kBalThreads) balance_chunk_kernel(BalanceParam
             const bool live = t0 + slot < hi;
             float l[NV], w[NV], other[NV];
             load_row<LT, NV, L>((const L*)P.logits + min(t0 + slot, hi - 1) * P.ld, P, lane, l);
+            if (t0 == lo)  // (between the load and its use)
+                for (int64_t i = lo * P.K + threadIdx.x; i < hi * P.K; i += kChunkThreads) {
+                    const int32_t e = P.ids[i];
+                    if (e >= 0 && e < P.E) atomicAdd(&hist[e], 1);
+                }
             score_terms<LT, NV>(l, P.sigmoid, w, other);
             float sum = 0.0f;
 #pragma unroll
@@ -128,25 +166,57 @@ __global__ void __launch_bounds__(kBalThreads) balance_chunk_kernel(BalanceParam
 #pragma unroll
             for (int i = 0; i < NV; i++) acc[i] = __builtin_fmaf(w[i], inv, acc[i]);
         }
+        if (LT == 16)
 #pragma unroll
-        for (int i = 0; i < NV; i++) part[slot][((i >> 2) * LT + lane) * 4 + (i & 3)] = acc[i];
+            for (int i = 0; i < NV; i++) {
+                acc[i] += __shfl_xor(acc[i], 16, kWave);
+                acc[i] += __shfl_xor(acc[i], 32, kWave);
+            }
+        if (LT == 64 || (threadIdx.x & 63) < 16)
+#pragma unroll
+            for (int i = 0; i < NV / 4; i++)
+                *reinterpret_cast<float4*>(&part[wave][(i * LT + lane) * 4]) = float4{acc[4 * i], acc[4 * i + 1], acc[4 * i + 2], acc[4 * i + 3]};
         __syncthreads();
-        const int64_t at = ((int64_t)blockIdx.x + s) * P.E;
-        for (int e = threadIdx.x; e < P.E; e += kBalThreads) {
+        const int64_t at = (whole ? s : (int64_t)blockIdx.x + s) * P.E;
+        double share = 0.0;
+        for (int e = threadIdx.x; e < P.E; e += kChunkThreads) {
             float sum = 0.0f;
-            for (int k = 0; k < kTok; k++) sum += part[k][e];
-            P.psum[at + e] = sum;
-            P.csum[at + e] = hist[e];
+#pragma unroll
+            for (int k = 0; k < kWaves; k++) sum += part[k][e];
+            const int32_t n = hist[e];
+            if (whole) {
+                P.counts[at + e] = n;
+                share += (double)sum * (double)n;
+            } else {
+                P.psum[at + e] = sum;
+                P.csum[at + e] = n;
+            }
+        }
+        if (whole) {
+            share = wave_sum(share);
+            if ((threadIdx.x & 63) == 0) shares[wave] = share;
+            for (int64_t i = (int64_t)s_next * P.E + threadIdx.x; i < (int64_t)s * P.E; i += kChunkThreads) P.counts[i] = 0;
+            s_next = s + 1;
         }
         __syncthreads();
+        if (whole) {
+            share = 0.0;
+            for (int k = 0; k < kWaves; k++) share += shares[k];
+            total += share / (double)(hi - lo);
+        }
+    }
+    if (whole) {  // (sequences without rows have no counts)
+        for (int64_t i = (int64_t)s_next * P.E + threadIdx.x; i < (int64_t)P.S * P.E; i += kChunkThreads) P.counts[i] = 0;
+        if (threadIdx.x == 0) *P.loss = balance_scaled(P, total);
     }
 }
 
 // Adds the slots of one sequence and 64 experts in FP64, in one order; the
 // workgroup that is last to finish adds up the workgroups' shares of the loss.
-__global__ void __launch_bounds__(kBalThreads) balance_join_kernel(BalanceParams P) {
-    __shared__ double sums[4][64];
-    __shared__ int32_t cnts[4][64];
+__global__ void __launch_bounds__(kJoinThreads) balance_join_kernel(BalanceParams P) {
+    constexpr int kStripes = kJoinThreads / 64, kAhead = 4;
+    __shared__ double sums[kStripes][64];
+    __shared__ int32_t cnts[kStripes][64];
     __shared__ bool last;
     const int groups = (P.E + 63) / 64, col = threadIdx.x & 63, stripe = threadIdx.x >> 6;
     const int32_t s = blockIdx.x / groups;
@@ -155,21 +225,37 @@ __global__ void __launch_bounds__(kBalThreads) balance_join_kernel(BalanceParams
     double sum = 0.0;
     int32_t n = 0;
     if (hi > lo && e < P.E) {
-        for (int64_t b = lo / P.chunk + stripe; b <= (hi - 1) / P.chunk; b += 4) {
-            sum += (double)P.psum[(b + s) * P.E + e];
-            n += P.csum[(b + s) * P.E + e];
+        const int64_t b1 = (hi - 1) / P.chunk;
+        for (int64_t b = lo / P.chunk + stripe; b <= b1; b += kStripes * kAhead) {
+            float p[kAhead];
+            int32_t c[kAhead];
+#pragma unroll
+            for (int k = 0; k < kAhead; k++) {
+                const int64_t at = (min(b + k * kStripes, b1) + s) * P.E + e;
+                p[k] = P.psum[at];
+                c[k] = P.csum[at];
+            }
+#pragma unroll
+            for (int k = 0; k < kAhead; k++)
+                if (b + k * kStripes <= b1) {
+                    sum += (double)p[k];
+                    n += c[k];
+                }
         }
     }
     sums[stripe][col] = sum;
     cnts[stripe][col] = n;
     __syncthreads();
     if (stripe == 0) {
-        sum = (sums[0][col] + sums[1][col]) + (sums[2][col] + sums[3][col]);
-        n = (cnts[0][col] + cnts[1][col]) + (cnts[2][col] + cnts[3][col]);
-        if (e < P.E) P.counts[(int64_t)s * P.E + e] = n;
-        double v = hi > lo ? sum * (double)n / (double)(hi - lo) : 0.0;
+        sum = 0.0;
+        n = 0;
 #pragma unroll
-        for (int o = 32; o > 0; o >>= 1) v += __shfl_xor(v, o, kWave);
+        for (int k = 0; k < kStripes; k++) {
+            sum += sums[k][col];
+            n += cnts[k][col];
+        }
+        if (e < P.E) P.counts[(int64_t)s * P.E + e] = n;
+        const double v = wave_sum(hi > lo ? sum * (double)n / (double)(hi - lo) : 0.0);
         if (col == 0) {
             P.part[blockIdx.x] = v;
             __threadfence();
@@ -180,15 +266,14 @@ __global__ void __launch_bounds__(kBalThreads) balance_join_kernel(BalanceParams
     if (!last) return;
     __threadfence();
     double total = 0.0;
-    for (uint32_t i = threadIdx.x; i < gridDim.x; i += kBalThreads) total += P.part[i];
-#pragma unroll
-    for (int o = 32; o > 0; o >>= 1) total += __shfl_xor(total, o, kWave);
+    for (uint32_t i = threadIdx.x; i < gridDim.x; i += kJoinThreads) total += P.part[i];
+    total = wave_sum(total);
     if (col == 0) sums[0][stripe] = total;
     __syncthreads();
     if (threadIdx.x == 0) {
-        const double tokens = (double)max(seq_start(P, P.S) - seq_start(P, 0), (int64_t)1);
-        total = (sums[0][0] + sums[0][1]) + (sums[0][2] + sums[0][3]);
-        *P.loss = (float)(total * (double)P.coef * (double)P.E / ((double)P.K * tokens));
+        total = 0.0;
+        for (int k = 0; k < kStripes; k++) total += sums[0][k];
+        *P.loss = balance_scaled(P, total);
     }
 }
 
@@ -215,7 +300,7 @@ __global__ void __launch_bounds__(kBalThreads) balance_backward_kernel(BalancePa
 #pragma unroll
             for (int j = 0; j < 4; j++) add[4 * i + j] = v[j];
         }
-        int32_t s = max(find_sequence(P, tile * kTok, found), 0);
+        int32_t s = max(find_sequence<kBalThreads>(P, tile * kTok, found), 0);
         while (s < P.S && seq_start(P, s + 1) <= tr) s++;
         double c = 0.0;  // rows of no sequence get no gradient
         if (s < P.S) {
@@ -282,10 +367,10 @@ namespace {
 template <int LT, int NV, typename L>
 hipError_t loss_run(const BalanceParams& P, hipStream_t s) {
     const int64_t chunks = std::max<int64_t>(1, (P.T + P.chunk - 1) / P.chunk);
-    hipLaunchKernelGGL((balance_chunk_kernel<LT, NV, L>), dim3((unsigned)chunks), dim3(kBalThreads), 0, s, P);
+    hipLaunchKernelGGL((balance_chunk_kernel<LT, NV, L>), dim3((unsigned)chunks), dim3(kChunkThreads), 0, s, P);
     const hipError_t e = hipGetLastError();
-    if (e != hipSuccess) return e;
-    hipLaunchKernelGGL(balance_join_kernel, dim3((unsigned)(P.S * ((P.E + 63) / 64))), dim3(kBalThreads), 0, s, P);
+    if (e != hipSuccess || chunks == 1) return e;
+    hipLaunchKernelGGL(balance_join_kernel, dim3((unsigned)(P.S * ((P.E + 63) / 64))), dim3(kJoinThreads), 0, s, P);
     return hipGetLastError();
 }
 template <int LT, int NV, typename L>
@@ -309,11 +394,14 @@ hipError_t balance_type(const BalanceParams& P, hipStream_t s) {
 
 }  // namespace
 
-// Rows of a workgroup of the loss: few enough that 256 CUs have one each, at
-// most 256 (a lane then adds 16 tokens in FP32 before FP64 takes over).
+// Rows of a workgroup of the loss: up to 256 in one, whose single launch takes
+// less than a second one would; else 64 and, so that there are at most 512
+// workgroups, up to 256 (a lane then adds 4 tokens, or 16 in rows of more than
+// 256 experts, in FP32 before FP64 takes over).
 int32_t balance_chunk(int64_t T) {
-    int32_t chunk = 16;
-    while (chunk < 256 && (T + chunk - 1) / chunk > 256) chunk *= 2;
+    if (T <= 256) return 256;
+    int32_t chunk = 64;
+    while (chunk < 256 && (T + chunk - 1) / chunk > 512) chunk *= 2;
     return chunk;
 }
 
