@@ -49,26 +49,44 @@ __device__ __forceinline__ u32x4 column8(const u32x4 (&z)[8], int c) {
     return f;
 }
 
-// Sum over the workgroup's earlier entries of a[0..n), in place; every thread calls it.
-__device__ __forceinline__ void block_scan(int32_t* a, int n, int32_t* lds) {
+// Sums over the earlier entries of N arrays [n], in place; every thread of the
+// workgroup calls it.
+template <int N>
+struct Arrays {
+    int32_t* of[N];
+};
+template <int N>
+__device__ __forceinline__ void block_scan(Arrays<N> a, int n, int32_t (*lds)[3]) {
     const int per = (n + kPlanThreads - 1) / kPlanThreads, lo = min((int)threadIdx.x * per, n), hi = min(lo + per, n);
-    int32_t sum = 0;
-    for (int i = lo; i < hi; i++) sum += a[i];
-    int32_t incl = sum;
+    int32_t sum[N], incl[N];
 #pragma unroll
-    for (int o = 1; o < 64; o <<= 1) {
-        const int32_t v = __shfl_up(incl, o, kWave);
-        if ((threadIdx.x & 63) >= o) incl += v;
+    for (int k = 0; k < N; k++) {
+        sum[k] = 0;
+        for (int i = lo; i < hi; i++) sum[k] += a.of[k][i];
+        incl[k] = sum[k];
     }
+#pragma unroll
+    for (int o = 1; o < 64; o <<= 1)
+#pragma unroll
+        for (int k = 0; k < N; k++) {
+            const int32_t v = __shfl_up(incl[k], o, kWave);
+            if ((int)(threadIdx.x & 63) >= o) incl[k] += v;
+        }
     __syncthreads();
-    if ((threadIdx.x & 63) == 63) lds[threadIdx.x >> 6] = incl;
+    if ((threadIdx.x & 63) == 63)
+#pragma unroll
+        for (int k = 0; k < N; k++) lds[threadIdx.x >> 6][k] = incl[k];
     __syncthreads();
-    int32_t run = incl - sum;
-    for (int w = 0; w < (int)(threadIdx.x >> 6); w++) run += lds[w];
-    for (int i = lo; i < hi; i++) {
-        const int32_t v = a[i];
-        a[i] = run;
-        run += v;
+#pragma unroll
+    for (int k = 0; k < N; k++) {
+        int32_t run = incl[k] - sum[k];
+#pragma unroll
+        for (int w = 0; w < kPlanThreads / 64; w++) run += w < (int)(threadIdx.x >> 6) ? lds[w][k] : 0;
+        for (int i = lo; i < hi; i++) {
+            const int32_t v = a.of[k][i];
+            a.of[k][i] = run;
+            run += v;
+        }
     }
     __syncthreads();
 }
@@ -107,26 +125,87 @@ __device__ __forceinline__ void count4(int32_t* hist, const AdapterPlan& P, int4
     if (live > 3) atomicAdd(&hist[b3], 1);
 }
 
+// B^T and A^T, which take the places of A and B in the gradient's products, of
+// the adapters that have rows.  Up to rank 32 (RB 0) as matrices [R][N] and
+// [K][R]; from there as operands, ranks padded with zeros to 16 RB, N and K to
+// multiples of 64, in units of 16 bytes (8 elements):
+//   first product:  rank r, inputs 8 k .. + 7: ((k / 4) RB + r / 16) 64 + k % 4 * 16 + r % 16
+//   second product: column c, ranks 8 r .. + 7: ((c / 64 * 4 + c % 4) RB / 2 + r / 4) 64 + r % 4 * 16 + c % 64 / 4
+// A thread turns 8 x 8 elements over with one byte permutation each two.
+template <int RB>
+__device__ __forceinline__ void pack_adapters(const AdapterPack& P, int64_t item) {
+    const uint32_t r8 = RB ? 2 * RB : P.R / 8, k8 = RB ? (P.K + 63) / 64 * 8 : P.K / 8, n8 = RB ? (P.N + 63) / 64 * 8 : P.N / 8;
+    const uint32_t each = r8 * (k8 + n8);
+    const int a = (int)(item / each);
+    if (a >= P.n || (P.info && P.info[a].x == 0)) return;
+    uint32_t k = (uint32_t)(item % each);
+    const bool is_a = k < r8 * k8;
+    if (!is_a) k -= r8 * k8;
+    // 8 ranks from 8 r on, and 8 columns of A or rows of B from 8 c on
+    const uint32_t r = is_a ? k / k8 : k % r8, c = is_a ? k % k8 : k / r8;
+    const bool in = RB == 0 || (8 * (int)r < P.R && 8 * (int)c < (is_a ? P.K : P.N));
+    const uint16_t* at = in ? is_a ? P.A + ((int64_t)a * P.R + 8 * r) * P.K + 8 * c : P.B + ((int64_t)a * P.N + 8 * c) * P.R + 8 * r : P.A;
+    const int64_t ld = in ? is_a ? P.K : P.R : 0;
+    u32x4 z[8];
+#pragma unroll
+    for (int j = 0; j < 8; j++) z[j] = load16(at + j * ld);
+    if (!in)
+#pragma unroll
+        for (int j = 0; j < 8; j++) z[j] = u32x4{0, 0, 0, 0};
+    u32x4* out = is_a ? P.second + a * P.units_second : P.first + a * P.units_first;
+#pragma unroll
+    for (int j = 0; j < 8; j++) {
+        // of A: column 8 c + j, ranks 8 r ..; of B: rank 8 r + j, rows 8 c ..
+        uint32_t to;
+        if (RB == 0)
+            to = is_a ? (8 * c + j) * r8 + r : (8 * r + j) * n8 + c;
+        else if (is_a)
+            to = ((((8 * c + j) >> 6) * 4 + (j & 3)) * (RB / 2) + (r >> 2)) * 64 + (r & 3) * 16 + (((8 * c + j) & 63) >> 2);
+        else
+            to = ((c >> 2) * RB + ((8 * r + j) >> 4)) * 64 + (c & 3) * 16 + ((8 * r + j) & 15);
+        out[to] = column8(z, j);
+    }
+}
+__device__ __forceinline__ void pack_adapters(const AdapterPack& P, int64_t item) {
+    if (P.R <= 32)
+        pack_adapters<0>(P, item);
+    else if (P.R <= 64)
+        pack_adapters<4>(P, item);
+    else
+        pack_adapters<8>(P, item);
+}
+
 }  // namespace
 
 // Rows grouped by adapter, each adapter's in their order, rows without one
 // behind them; the row tiles and, for the gradients, the row chunks, which the
 // last workgroup writes.  Every workgroup counts all rows for itself (16 K rows
 // of ids in flight at once), which saves a launch that only counts.
-__global__ void __launch_bounds__(kPlanThreads) adapter_plan_kernel(AdapterPlan P) {
-    constexpr int kWaves = kPlanThreads / 64, kAhead = 4;
-    __shared__ int32_t total[kBins + 1], start[kBins + 1], before[kBins], scan[kWaves];
+// Workgroups behind those transpose the adapters, if that need not wait for the
+// plan to say which of them have rows.
+__global__ void __launch_bounds__(kPlanThreads) adapter_plan_kernel(AdapterPlan P, AdapterPack pack) {
+    constexpr int kWaves = kPlanThreads / 64, kAhead = 8;
+    __shared__ int32_t total[kBins + 1], start[kBins + 1], before[kBins], scan[kWaves][3];
     __shared__ uint16_t counts[kWaves][kBins];
     __shared__ int32_t tile0[kBins], chunk0[kBins], slot0[kBins];  // (a tile is a step of the gradients)
     const int bins = P.n + 1, wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
-    const bool tables = blockIdx.x == gridDim.x - 1;
+    if ((int)blockIdx.x >= P.blocks) {
+        pack_adapters(pack, ((int64_t)blockIdx.x - P.blocks) * kPlanThreads + threadIdx.x);
+        return;
+    }
+    const bool tables = (int)blockIdx.x == P.blocks - 1;
     const int64_t first = tables ? 0 : (int64_t)blockIdx.x * P.rows;  // a multiple of 256: a wavefront's rows lie on one side
     for (int i = threadIdx.x; i <= bins; i += kPlanThreads) total[i] = 0;
     for (int i = threadIdx.x; i < bins; i += kPlanThreads) before[i] = 0;
     __syncthreads();
     // Four rows a thread.  kAhead such pieces of 4096 rows are loaded before any
-    // is counted, the last piece (which may be a part) by itself.
-    const int64_t last = P.M > 0 ? (P.M - 1) / (4 * kPlanThreads) : 0;
+    // is counted, and the last piece (which may be a part) before all.
+    const int64_t last = P.M > 0 ? (P.M - 1) / (4 * kPlanThreads) : 0, r_last = 4 * (last * kPlanThreads + threadIdx.x);
+    int4 id_last = make_int4(-1, -1, -1, -1);
+    if (r_last < P.M) id_last.x = P.ids[r_last];
+    if (r_last + 1 < P.M) id_last.y = P.ids[r_last + 1];
+    if (r_last + 2 < P.M) id_last.z = P.ids[r_last + 2];
+    if (r_last + 3 < P.M) id_last.w = P.ids[r_last + 3];
     for (int64_t p0 = 0; p0 < last; p0 += kAhead) {
         int4 id[kAhead];
 #pragma unroll
@@ -142,22 +221,14 @@ __global__ void __launch_bounds__(kPlanThreads) adapter_plan_kernel(AdapterPlan 
         for (int k = 0; k < kAhead; k++)
             if (p0 + k < last) count4(4 * ((p0 + k) * kPlanThreads + threadIdx.x) < first ? before : total, P, id[k], 4);
     }
-    {
-        const int64_t r = 4 * (last * kPlanThreads + threadIdx.x);
-        int4 id = make_int4(-1, -1, -1, -1);
-        if (r < P.M) id.x = P.ids[r];
-        if (r + 1 < P.M) id.y = P.ids[r + 1];
-        if (r + 2 < P.M) id.z = P.ids[r + 2];
-        if (r + 3 < P.M) id.w = P.ids[r + 3];
-        count4(r < first ? before : total, P, id, P.M - r);
-    }
+    count4(r_last < first ? before : total, P, id_last, P.M - r_last);
     __syncthreads();
     for (int i = threadIdx.x; i <= bins; i += kPlanThreads) {
         if (i < bins) total[i] += before[i];
         start[i] = total[i];
     }
     __syncthreads();
-    block_scan(start, bins + 1, scan);
+    block_scan<1>({start}, bins + 1, scan);
     if (!tables) {
         // 1024 rows at a time, one a thread.  Lanes of one bin find each other
         // by a ballot for each bit of it; a row's place is the bin's next one,
@@ -198,7 +269,8 @@ __global__ void __launch_bounds__(kPlanThreads) adapter_plan_kernel(AdapterPlan 
         return;
     }
     for (int i = threadIdx.x; i < bins; i += kPlanThreads) {
-        const int32_t chunks = i < P.n && P.chunk ? (total[i] + P.chunk - 1) / P.chunk : 0;
+        // (an adapter without rows has an empty chunk, whose sums are zeros)
+        const int32_t chunks = i < P.n && P.chunk ? max(1, (total[i] + P.chunk - 1) / P.chunk) : 0;
         tile0[i] = i < P.n || P.rest ? (total[i] + P.tile - 1) / P.tile : 0;
         chunk0[i] = chunks;
         slot0[i] = chunks > 1 ? chunks : 0;
@@ -206,14 +278,11 @@ __global__ void __launch_bounds__(kPlanThreads) adapter_plan_kernel(AdapterPlan 
     __syncthreads();
     const int32_t last_tiles = tile0[bins - 1];  // (the rows without an adapter have no chunks)
     __syncthreads();
-    block_scan(tile0, bins, scan);
-    const int32_t n_tiles = tile0[bins - 1] + last_tiles;
-    int32_t n_chunks = 0;
-    if (P.chunk) {
-        block_scan(chunk0, bins, scan);
-        block_scan(slot0, bins, scan);
-        n_chunks = chunk0[bins - 1];
-    }
+    if (P.chunk)
+        block_scan<3>({tile0, chunk0, slot0}, bins, scan);
+    else
+        block_scan<1>({tile0}, bins, scan);
+    const int32_t n_tiles = tile0[bins - 1] + last_tiles, n_chunks = P.chunk ? chunk0[bins - 1] : 0;
     if (threadIdx.x == 0) {
         P.n_tables[0] = n_tiles;
         P.n_tables[1] = n_chunks;
@@ -578,10 +647,20 @@ __global__ void __launch_bounds__(kAdWaves * 64, RB < 4 || (RB == 4 && kGrad) ? 
         const int n = n0 + NB * i;
         if (kBase) {
             const uint8_t* at = reinterpret_cast<const uint8_t*>(P.base + (whole.value ? n : min(n, P.N - NB)));
+            if (P.stream) {  // (the fences: or the compiler makes one load of the two kinds)
+                asm volatile("" ::: "memory");
 #pragma unroll
-            for (int m = 0; m < MB; m++)
+                for (int m = 0; m < MB; m++)
 #pragma unroll
-                for (int e = 0; e < 4; e++) old[m][e] = *reinterpret_cast<const vec*>(at + base_at[16 * m + 4 * q + e]);
+                    for (int e = 0; e < 4; e++)
+                        old[m][e] = __builtin_nontemporal_load(reinterpret_cast<const vec*>(at + base_at[16 * m + 4 * q + e]));
+                asm volatile("" ::: "memory");
+            } else {
+#pragma unroll
+                for (int m = 0; m < MB; m++)
+#pragma unroll
+                    for (int e = 0; e < 4; e++) old[m][e] = *reinterpret_cast<const vec*>(at + base_at[16 * m + 4 * q + e]);
+            }
         }
         issue();
         if constexpr (!kPacked) {
@@ -640,70 +719,38 @@ __global__ void __launch_bounds__(kAdWaves * 64, RB < 4 || (RB == 4 && kGrad) ? 
     if (n0 < n_end) step2(n0, std::false_type{});
 }
 
-// B^T and A^T, which take the places of A and B in the gradient's products, of
-// the adapters that have rows.  Up to rank 32 (RB 0) as matrices [R][N] and
-// [K][R]; from there as operands, ranks padded with zeros to 16 RB, N and K to
-// multiples of 64, in units of 16 bytes (8 elements):
-//   first product:  rank r, inputs 8 k .. + 7: ((k / 4) RB + r / 16) 64 + k % 4 * 16 + r % 16
-//   second product: column c, ranks 8 r .. + 7: ((c / 64 * 4 + c % 4) RB / 2 + r / 4) 64 + r % 4 * 16 + c % 64 / 4
-// A thread turns 8 x 8 elements over with one byte permutation each two.
-template <int RB>
 __global__ void __launch_bounds__(256) adapter_pack_kernel(AdapterPack P) {
-    const int a = blockIdx.y;
-    if (P.info[a].x == 0) return;
-    const uint32_t r8 = RB ? 2 * RB : P.R / 8, k8 = RB ? (P.K + 63) / 64 * 8 : P.K / 8, n8 = RB ? (P.N + 63) / 64 * 8 : P.N / 8;
-    uint32_t k = blockIdx.x * 256 + threadIdx.x;
-    const bool is_a = k < r8 * k8;
-    if (!is_a) k -= r8 * k8;
-    if (!is_a && k >= r8 * n8) return;
-    // 8 ranks from 8 r on, and 8 columns of A or rows of B from 8 c on
-    const uint32_t r = is_a ? k / k8 : k % r8, c = is_a ? k % k8 : k / r8;
-    const bool in = RB == 0 || (8 * (int)r < P.R && 8 * (int)c < (is_a ? P.K : P.N));
-    const uint16_t* at = in ? is_a ? P.A + ((int64_t)a * P.R + 8 * r) * P.K + 8 * c : P.B + ((int64_t)a * P.N + 8 * c) * P.R + 8 * r : P.A;
-    const int64_t ld = in ? is_a ? P.K : P.R : 0;
-    u32x4 z[8];
-#pragma unroll
-    for (int j = 0; j < 8; j++) z[j] = load16(at + j * ld);
-    if (!in)
-#pragma unroll
-        for (int j = 0; j < 8; j++) z[j] = u32x4{0, 0, 0, 0};
-    u32x4* out = is_a ? P.second + a * P.units_second : P.first + a * P.units_first;
-#pragma unroll
-    for (int j = 0; j < 8; j++) {
-        // of A: column 8 c + j, ranks 8 r ..; of B: rank 8 r + j, rows 8 c ..
-        uint32_t to;
-        if (RB == 0)
-            to = is_a ? (8 * c + j) * r8 + r : (8 * r + j) * n8 + c;
-        else if (is_a)
-            to = ((((8 * c + j) >> 6) * 4 + (j & 3)) * (RB / 2) + (r >> 2)) * 64 + (r & 3) * 16 + (((8 * c + j) & 63) >> 2);
-        else
-            to = ((c >> 2) * RB + ((8 * r + j) >> 4)) * 64 + (c & 3) * 16 + ((8 * r + j) & 15);
-        out[to] = column8(z, j);
-    }
+    pack_adapters(P, (int64_t)blockIdx.x * 256 + threadIdx.x);
 }
 
 // dA and dB of one row chunk and 128 columns: the sum over rows is the matrix
-// instruction's inner dimension, 32 rows a step, the wavefronts taking steps in
-// turn.  A lane loads 8 columns of 8 rows; one byte permutation a register
-// turns them into operands with 8 rows of one column each, for eight products
-// whose columns lie 8 apart.  w and v are FP32 sums and go in as three BF16
-// values, which is all of their 24 bits, laid out as operands by adapter_kernel
-// (zeros behind the chunk's last row, where x and dy repeat it).
-// RB: ranks in blocks of 16 (blockIdx.z takes further ones).
-template <int RB>
-__global__ void __launch_bounds__(256, 2) adapter_wgrad_kernel(AdapterGrad P) {
+// instruction's inner dimension, 32 rows a step.  A lane loads 8 columns of 8
+// rows; one byte permutation a register turns them into operands with 8 rows of
+// one column each, for eight products whose columns lie 8 apart.  w and v are
+// FP32 sums and go in as three BF16 values, which is all of their 24 bits, laid
+// out as operands by adapter_kernel (zeros behind the chunk's last row, where x
+// and dy repeat it).
+// RB: ranks in blocks of 16 (blockIdx.z takes further ones).  The NW wavefronts
+// take steps in turn and join their sums in LDS.  (Wavefronts that take 128
+// columns each and all steps have nothing to join, but uneven experts then leave
+// CUs idle: 71 against 63 us for 128 of them.)
+template <int RB, int NW>
+__global__ void __launch_bounds__(NW * 64, RB < 2 ? 4 : 2) adapter_wgrad_kernel(AdapterGrad P) {
     constexpr int kAhead = RB < 2 ? RB : 2;  // rank blocks whose w is in registers
-    __shared__ __attribute__((aligned(16))) float red[4][16][132];
+    __shared__ __attribute__((aligned(16))) f32x4 red[NW * 8 * 64];
     const int lane = threadIdx.x & 63, i = lane & 15, q = lane >> 4;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    if ((int)blockIdx.y >= P.n_tables[1]) return;
-    const int4 t = P.chunks[blockIdx.y];
-    const int a = t.x, count = t.z, k_slabs = (P.K + 127) / 128;
-    const bool is_a = (int)blockIdx.x < k_slabs;
-    const int C = is_a ? P.K : P.N, c0 = ((int)blockIdx.x - (is_a ? 0 : k_slabs)) * 128, block0 = blockIdx.z * RB;
+    // The last rows first, and of them dy: what adapter_kernel read last is still
+    // in the last-level cache.
+    const int chunk = P.n_tables[1] - 1 - (int)blockIdx.y;
+    if (chunk < 0) return;
+    const int4 t = P.chunks[chunk];
+    const int a = t.x, count = t.z, n_slabs = (P.N + 127) / 128, slab = blockIdx.x;
+    const bool is_a = slab >= n_slabs;
+    const int C = is_a ? P.K : P.N, c0 = (is_a ? slab - n_slabs : slab) * 128, block0 = blockIdx.z * RB;
     const int64_t ldz = is_a ? P.ldx : P.ld_dy;
     const uint16_t* Z = (is_a ? P.x : P.dy) + min(c0 + 8 * i, C - 8);
-    const u32x4* W = (is_a ? P.w_pack : P.v_pack) + ((int64_t)P.chunk_step[blockIdx.y] * P.rank_blocks + block0) * 192 + lane;
+    const u32x4* W = (is_a ? P.w_pack : P.v_pack) + ((int64_t)P.chunk_step[chunk] * P.rank_blocks + block0) * 192 + lane;
     const int32_t* order = P.order + t.y;
     f32x4 acc[8][RB];
 #pragma unroll
@@ -721,7 +768,8 @@ __global__ void __launch_bounds__(256, 2) adapter_wgrad_kernel(AdapterGrad P) {
 #pragma unroll
         for (int p = 0; p < 3; p++) w[b % kAhead][p] = at[64 * p];
     };
-    // One step; `more`: the wavefront's next step, 128 rows on, is loaded meanwhile.
+    // One step; `more`: the wavefront's next step is loaded meanwhile.
+    constexpr int kStep = 32 * NW;
     int32_t rows = 0;
     auto step = [&](int s, auto more) {
         u32x4 zf[8];
@@ -729,7 +777,7 @@ __global__ void __launch_bounds__(256, 2) adapter_wgrad_kernel(AdapterGrad P) {
         for (int c = 0; c < 8; c++) zf[c] = column8(z, c);
         if constexpr (more.value) {
             load_z(rows);
-            rows = load_rows(s + 256);
+            rows = load_rows(s + 2 * kStep);
             issue();
         }
 #pragma unroll
@@ -741,7 +789,7 @@ __global__ void __launch_bounds__(256, 2) adapter_wgrad_kernel(AdapterGrad P) {
             if (b + kAhead < RB)
                 load_w(b + kAhead, s);
             else if constexpr (more.value)
-                load_w(b + kAhead - RB, s + 128);
+                load_w(b + kAhead - RB, s + kStep);
         }
     };
     int s = wave * 32;
@@ -749,58 +797,50 @@ __global__ void __launch_bounds__(256, 2) adapter_wgrad_kernel(AdapterGrad P) {
         load_z(load_rows(s));
 #pragma unroll
         for (int b = 0; b < kAhead; b++) load_w(b, s);
-        rows = load_rows(s + 128);
-        for (; s + 128 < count; s += 128) step(s, std::true_type{});
+        rows = load_rows(s + kStep);
+        for (; s + kStep < count; s += kStep) step(s, std::true_type{});
         step(s, std::false_type{});
     }
-    // The wavefronts' sums, added in one order.  (w holds the scale already.)
-    const float scale = P.scale && !is_a ? P.scale[a] : 1.0f;
+    const float scale = P.scale && !is_a ? P.scale[a] : 1.0f;  // (w holds it already)
     const int64_t each = (int64_t)P.R * (P.K + P.N);
     float* dA = t.w < 0 ? P.dA + (int64_t)a * P.R * P.K : P.slots + t.w * each;
     float* dB = t.w < 0 ? P.dB + (int64_t)a * P.R * P.N : P.slots + t.w * each + (int64_t)P.R * P.K;
 #pragma unroll
     for (int b = 0; b < RB; b++) {
+        const int rank = (block0 + b) * 16 + 4 * q;
+        // Piece k of the block: of dA rank 4 q + k / 2 and columns 8 i + 4 (k % 2) .. + 3,
+        // of dB column 8 i + k and ranks 4 q .. + 3.
+        auto piece = [&](int k) {
+            const int e = k >> 1, h = 4 * (k & 1);
+            return is_a ? f32x4{acc[h][b][e], acc[h + 1][b][e], acc[h + 2][b][e], acc[h + 3][b][e]} : acc[k][b];
+        };
+        auto put = [&](int k, f32x4 v) {
+            if (is_a) {
+                const int c = c0 + 8 * i + 4 * (k & 1);
+                if (rank + (k >> 1) < P.R && c < C) *reinterpret_cast<f32x4*>(dA + (int64_t)(rank + (k >> 1)) * P.K + c) = v;
+            } else {
+                const int c = c0 + 8 * i + k;
+                if (rank < P.R && c < C) *reinterpret_cast<f32x4*>(dB + (int64_t)c * P.R + rank) = v * scale;
+            }
+        };
+        if (b) __syncthreads();
+#pragma unroll
+        for (int k = 0; k < 8; k++) red[(wave * 8 + k) * 64 + lane] = piece(k);
         __syncthreads();
+        for (int k = wave; k < 8; k += NW) {  // the wavefronts' sums, in one order
+            f32x4 v = red[k * 64 + lane];
 #pragma unroll
-        for (int e = 0; e < 4; e++) {
-            *reinterpret_cast<f32x4*>(&red[wave][4 * q + e][8 * i]) = f32x4{acc[0][b][e], acc[1][b][e], acc[2][b][e], acc[3][b][e]};
-            *reinterpret_cast<f32x4*>(&red[wave][4 * q + e][8 * i + 4]) = f32x4{acc[4][b][e], acc[5][b][e], acc[6][b][e], acc[7][b][e]};
-        }
-        __syncthreads();
-        const int rank = (block0 + b) * 16;
-        if (is_a) {
-            const int r = threadIdx.x / 16, c = threadIdx.x % 16 * 8;
-            if (rank + r < P.R && c0 + c < C)
-#pragma unroll
-                for (int h = 0; h < 2; h++) {
-                    f32x4 s[4];
-#pragma unroll
-                    for (int k = 0; k < 4; k++) s[k] = *reinterpret_cast<const f32x4*>(&red[k][r][c + 4 * h]);
-                    *reinterpret_cast<f32x4*>(dA + (int64_t)(rank + r) * P.K + c0 + c + 4 * h) = (s[0] + s[1]) + (s[2] + s[3]);
-                }
-        } else {
-            const int c = threadIdx.x / 2, r = threadIdx.x % 2 * 8;
-            if (rank + r < P.R && c0 + c < C)
-#pragma unroll
-                for (int h = 0; h < 2; h++) {
-                    f32x4 o;
-#pragma unroll
-                    for (int e = 0; e < 4; e++) {
-                        const int k = r + 4 * h + e;
-                        o[e] = ((red[0][k][c] + red[1][k][c]) + (red[2][k][c] + red[3][k][c])) * scale;
-                    }
-                    *reinterpret_cast<f32x4*>(dB + (int64_t)(c0 + c) * P.R + rank + r + 4 * h) = o;
-                }
+            for (int j = 1; j < NW; j++) v += red[(j * 8 + k) * 64 + lane];
+            put(k, v);
         }
     }
 }
 
 // Adapters whose rows filled several chunks: the chunks' sums, in order.
-// Adapters without rows: zeros.
 __global__ void __launch_bounds__(256) adapter_join_kernel(AdapterGrad P) {
     const int a = blockIdx.y;
     const int2 info = P.info[a];
-    if (info.x == 1) return;
+    if (info.x <= 1) return;
     const int64_t of_a = (int64_t)P.R * P.K, each = of_a + (int64_t)P.R * P.N;
     const int64_t k = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 4;
     if (k >= each) return;
@@ -810,13 +850,30 @@ __global__ void __launch_bounds__(256) adapter_join_kernel(AdapterGrad P) {
     *reinterpret_cast<f32x4*>(out) = s;
 }
 
+int adapter_rank_blocks(int32_t R) { return R <= 16 ? 1 : R <= 32 ? 2 : R <= 64 ? 4 : 8; }
+int64_t adapter_units(int64_t cols, int32_t R) {
+    return R <= 32 ? cols * R / 8 : (cols + 63) / 64 * 128 * adapter_rank_blocks(R);
+}
+
 // A workgroup of the plan places 1024 rows, or as many as keep their number to
 // 256: each of them counts all rows.
-hipError_t launch_adapter_plan(AdapterPlan P, hipStream_t stream) {
+hipError_t launch_adapter_plan(AdapterPlan P, const AdapterPack* pack, hipStream_t stream) {
     P.rows = std::max<int64_t>(1, (P.M + 256 * kPlanThreads - 1) / (256 * kPlanThreads)) * kPlanThreads;
     P.vec = (uintptr_t)P.ids % 16 == 0;
-    const int64_t blocks = (P.M + P.rows - 1) / P.rows + 1;
-    hipLaunchKernelGGL(adapter_plan_kernel, dim3((unsigned)blocks), dim3(kPlanThreads), 0, stream, P);
+    P.blocks = (int32_t)((P.M + P.rows - 1) / P.rows + 1);
+    AdapterPack k{};
+    int64_t more = 0;
+    // All adapters, where their bytes are a small part of the rows'; else those with rows, afterwards.
+    if (pack && (int64_t)pack->n * pack->R <= P.M / 4) {
+        k = *pack;
+        k.info = nullptr;
+        more = (k.n * (adapter_units(k.K, k.R) + adapter_units(k.N, k.R)) / 8 + kPlanThreads - 1) / kPlanThreads;
+    }
+    hipLaunchKernelGGL(adapter_plan_kernel, dim3((unsigned)(P.blocks + more)), dim3(kPlanThreads), 0, stream, P, k);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess || !pack || more) return e;
+    const int64_t items = pack->n * (adapter_units(pack->K, pack->R) + adapter_units(pack->N, pack->R)) / 8;
+    hipLaunchKernelGGL(adapter_pack_kernel, dim3((unsigned)((items + 255) / 256)), dim3(256), 0, stream, *pack);
     return hipGetLastError();
 }
 
@@ -840,8 +897,6 @@ hipError_t adapter_run(const AdapterParams& P, int64_t tiles, hipStream_t s) {
 
 }  // namespace
 
-int adapter_rank_blocks(int32_t R) { return R <= 16 ? 1 : R <= 32 ? 2 : R <= 64 ? 4 : 8; }
-
 // Up to 512 rows, one a thread, take one launch, which groups them itself.
 bool adapter_small(int64_t M) { return M <= kAdWaves * 64; }
 
@@ -850,6 +905,11 @@ hipError_t launch_adapter(AdapterParams P, int64_t tiles, hipStream_t stream) {
     if (P.ids) tiles = P.tile_bound = (int32_t)std::min<int64_t>(P.M, P.n + 1 + P.M / 16);
     // Few tiles: their columns are shared out, and each share repeats the first product.
     P.slabs = (int32_t)std::max<int64_t>(1, std::min<int64_t>((P.N + cols - 1) / cols, 256 / tiles));
+    // Where the rows' tensors (of the gradient x too) exceed the 256 MB of the
+    // last-level cache, base, which is read once, stays out of it: 128 experts'
+    // 335 MB forward 76 -> 60 us, their gradient 80 + 63 -> 74 + 55.  Below, it may be
+    // there already: 201 MB 37 us, and 46 past the cache.
+    P.stream = 2 * P.M * ((P.w_pack ? 2 : 1) * (int64_t)P.K + 2 * P.N) > ((int64_t)1 << 28);
     switch (adapter_rank_blocks(P.R)) {
         case 1: return adapter_run<1>(P, tiles, stream);
         case 2: return adapter_run<2>(P, tiles, stream);
@@ -858,42 +918,34 @@ hipError_t launch_adapter(AdapterParams P, int64_t tiles, hipStream_t stream) {
     }
 }
 
-// Rows of a chunk of the gradients: the columns' slabs times the chunks are
-// about 1024 workgroups.
-int32_t adapter_chunk(int64_t M, int64_t K, int64_t N) {
-    const int64_t slabs = (K + 127) / 128 + (N + 127) / 128, chunks = std::max<int64_t>(1, 1024 / slabs);
-    return (int32_t)std::min<int64_t>((std::max<int64_t>(M, 1) + 128 * chunks - 1) / (128 * chunks) * 128, (int64_t)1 << 30);
-}
-
-int64_t adapter_units(int64_t cols, int32_t R) {
-    return R <= 32 ? cols * R / 8 : (cols + 63) / 64 * 128 * adapter_rank_blocks(R);
-}
-
-hipError_t launch_adapter_pack(const AdapterPack& P, hipStream_t stream) {
-    const unsigned blocks = (unsigned)((adapter_units(P.K, P.R) + adapter_units(P.N, P.R)) / 8);  // of 8 x 8
-    const dim3 grid((blocks + 255) / 256, P.n);
-    if (P.R <= 32)
-        hipLaunchKernelGGL(adapter_pack_kernel<0>, grid, dim3(256), 0, stream, P);
-    else if (P.R <= 64)
-        hipLaunchKernelGGL(adapter_pack_kernel<4>, grid, dim3(256), 0, stream, P);
-    else
-        hipLaunchKernelGGL(adapter_pack_kernel<8>, grid, dim3(256), 0, stream, P);
-    return hipGetLastError();
-}
-
-hipError_t launch_adapter_wgrad(const AdapterGrad& P, int64_t chunks, hipStream_t stream) {
-    const unsigned slabs = (P.K + 127) / 128 + (P.N + 127) / 128;
-    if (chunks > 0) {
-        const dim3 grid(slabs, (unsigned)chunks, P.R > 64 ? 2 : 1);
-        if (P.R <= 16)
-            hipLaunchKernelGGL(adapter_wgrad_kernel<1>, grid, dim3(256), 0, stream, P);
-        else if (P.R <= 32)
-            hipLaunchKernelGGL(adapter_wgrad_kernel<2>, grid, dim3(256), 0, stream, P);
-        else
-            hipLaunchKernelGGL(adapter_wgrad_kernel<4>, grid, dim3(256), 0, stream, P);
-        const hipError_t e = hipGetLastError();
-        if (e != hipSuccess) return e;
+// Rows of a chunk of the weights' gradients, how a workgroup takes them
+// (adapter_wgrad_kernel), and whether an adapter may have several.
+AdapterSplit adapter_split(int64_t M, int32_t R, int64_t K, int64_t N) {
+    const int64_t slabs = (K + 127) / 128 + (N + 127) / 128;
+    AdapterSplit s{};
+    if (R <= 16 && M <= 1024) {  // one chunk, and its steps one or two a wavefront: no sums to join
+        s.waves16 = true;
+        s.chunk = 1024;
+    } else {  // the columns' slabs times the chunks are the workgroups that the CUs hold at a time
+        const int64_t chunks = std::max<int64_t>(1, (R <= 16 ? 1024 : 512) / slabs);
+        s.chunk = (int32_t)std::min<int64_t>((std::max<int64_t>(M, 1) + 128 * chunks - 1) / (128 * chunks) * 128, (int64_t)1 << 30);
     }
+    s.join = M > s.chunk;
+    return s;
+}
+
+hipError_t launch_adapter_wgrad(const AdapterGrad& P, const AdapterSplit& split, int64_t chunks, hipStream_t stream) {
+    const dim3 grid((P.K + 127) / 128 + (P.N + 127) / 128, (unsigned)chunks, P.R > 64 ? 2 : 1);
+    if (split.waves16)
+        hipLaunchKernelGGL((adapter_wgrad_kernel<1, 16>), grid, dim3(1024), 0, stream, P);
+    else if (P.R <= 16)
+        hipLaunchKernelGGL((adapter_wgrad_kernel<1, 4>), grid, dim3(256), 0, stream, P);
+    else if (P.R <= 32)
+        hipLaunchKernelGGL((adapter_wgrad_kernel<2, 4>), grid, dim3(256), 0, stream, P);
+    else
+        hipLaunchKernelGGL((adapter_wgrad_kernel<4, 4>), grid, dim3(256), 0, stream, P);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess || !split.join) return e;
     const int64_t each = (int64_t)P.R * (P.K + P.N);
     hipLaunchKernelGGL(adapter_join_kernel, dim3((unsigned)((each / 4 + 255) / 256), P.n), dim3(256), 0, stream, P);
     return hipGetLastError();

@@ -235,7 +235,7 @@ int adapter_planes(const nvfp4moe_adapters* ad) {
 struct AdapterWork {
     size_t order, tiles, chunks, steps, info, first, second, v_pack, w_pack, slots, total;
     int64_t n_tiles, n_chunks;
-    int32_t chunk;
+    AdapterSplit split;
 };
 AdapterWork adapter_work(const nvfp4moe_adapters* ad, int64_t M, bool backward) {
     AdapterWork w{};
@@ -249,8 +249,8 @@ AdapterWork adapter_work(const nvfp4moe_adapters* ad, int64_t M, bool backward) 
     w.first = w.info + up(n * 8, kAlign);
     w.second = w.first + up(n * adapter_units(N, ad->rank) * 16, kAlign);
     w.total = w.second + up(n * adapter_units(K, ad->rank) * 16, kAlign);
-    w.chunk = adapter_chunk(M, K, N);
-    w.n_chunks = M / w.chunk + std::min(M, n);
+    w.split = adapter_split(M, ad->rank, K, N);
+    w.n_chunks = M / w.split.chunk + n;
     w.chunks = w.total;
     w.steps = w.chunks + up(w.n_chunks * 16, kAlign);
     w.v_pack = w.steps + up(w.n_chunks * 4, kAlign);
@@ -258,7 +258,7 @@ AdapterWork adapter_work(const nvfp4moe_adapters* ad, int64_t M, bool backward) 
     w.slots = 2 * w.w_pack - w.v_pack;
     // chunks of adapters that have more than one: each such adapter has more
     // than `chunk` rows, so at most twice its rows / chunk of them
-    w.total = w.slots + up((2 * M / w.chunk) * R * (K + N) * 4, kAlign);
+    w.total = w.slots + (w.split.join ? up((2 * M / w.split.chunk) * R * (K + N) * 4, kAlign) : 0);
     return w;
 }
 int adapter_rows(const uint16_t* p, int64_t ld, int64_t cols) {
@@ -507,7 +507,7 @@ int nvfp4moe_adapter_linear(const nvfp4moe_adapters* ad, const uint16_t* x, int6
     p.out = out;
     p.ld_out = ld_out;
     p.v = v;
-    p.M = (int32_t)M;
+    p.M = M;
     p.n = ad->n;
     p.rest = base != out || v;
     if (adapter_small(M)) {
@@ -523,7 +523,7 @@ int nvfp4moe_adapter_linear(const nvfp4moe_adapters* ad, const uint16_t* x, int6
     plan.n_tables = (int32_t*)ws;
     plan.order = (int32_t*)(ws + w.order);
     plan.tiles = (int4*)(ws + w.tiles);
-    if (launch_adapter_plan(plan, (hipStream_t)stream) != hipSuccess) return NVFP4_E_HIP;
+    if (launch_adapter_plan(plan, nullptr, (hipStream_t)stream) != hipSuccess) return NVFP4_E_HIP;
     p.order = plan.order;
     p.tiles = plan.tiles;
     p.n_tiles = plan.n_tables;
@@ -554,7 +554,7 @@ int nvfp4moe_adapter_backward(const nvfp4moe_adapters* ad, const uint16_t* x, in
     plan.M = M;
     plan.n = ad->n;
     plan.tile = kAdTile;
-    plan.chunk = w.chunk;
+    plan.chunk = w.split.chunk;
     plan.rest = base != dx;
     plan.n_tables = (int32_t*)ws;
     plan.order = (int32_t*)(ws + w.order);
@@ -562,7 +562,19 @@ int nvfp4moe_adapter_backward(const nvfp4moe_adapters* ad, const uint16_t* x, in
     plan.chunks = (int4*)(ws + w.chunks);
     plan.chunk_step = (int32_t*)(ws + w.steps);
     plan.info = (int2*)(ws + w.info);
-    if (launch_adapter_plan(plan, s) != hipSuccess) return NVFP4_E_HIP;
+    AdapterPack k{};
+    k.A = ad->A;
+    k.B = ad->B;
+    k.info = plan.info;
+    k.n = ad->n;
+    k.R = ad->rank;
+    k.K = K;
+    k.N = N;
+    k.first = (u32x4*)(ws + w.first);
+    k.second = (u32x4*)(ws + w.second);
+    k.units_first = adapter_units(N, ad->rank);
+    k.units_second = adapter_units(K, ad->rank);
+    if (launch_adapter_plan(plan, M > 0 ? &k : nullptr, s) != hipSuccess) return NVFP4_E_HIP;
     AdapterGrad g{};
     g.scale = ad->scale;
     g.n = ad->n;
@@ -585,19 +597,6 @@ int nvfp4moe_adapter_backward(const nvfp4moe_adapters* ad, const uint16_t* x, in
     g.dA = dA;
     g.dB = dB;
     if (M > 0) {
-        AdapterPack k{};
-        k.A = ad->A;
-        k.B = ad->B;
-        k.info = plan.info;
-        k.n = ad->n;
-        k.R = ad->rank;
-        k.K = K;
-        k.N = N;
-        k.first = (u32x4*)(ws + w.first);
-        k.second = (u32x4*)(ws + w.second);
-        k.units_first = adapter_units(N, ad->rank);
-        k.units_second = adapter_units(K, ad->rank);
-        if (launch_adapter_pack(k, s) != hipSuccess) return NVFP4_E_HIP;
         AdapterParams p{};
         p.A = (const uint16_t*)k.first;
         p.B = (const uint16_t*)k.second;
@@ -616,12 +615,13 @@ int nvfp4moe_adapter_backward(const nvfp4moe_adapters* ad, const uint16_t* x, in
         p.v_in = v;
         p.v_pack = (u32x4*)(ws + w.v_pack);
         p.w_pack = (u32x4*)(ws + w.w_pack);
+        p.M = M;
         p.order = plan.order;
         p.tiles = plan.tiles;
         p.n_tiles = plan.n_tables;
         if (launch_adapter(p, w.n_tiles, s) != hipSuccess) return NVFP4_E_HIP;
     }
-    return hip_status(launch_adapter_wgrad(g, w.n_chunks, s));
+    return hip_status(launch_adapter_wgrad(g, w.split, w.n_chunks, s));
 }
 
 int nvfp4moe_grad_plan_bytes(const nvfp4moe_grad* grads, int32_t n_grads, size_t* bytes, int64_t* n_chunks) {

@@ -168,7 +168,8 @@ constexpr int adapter_tile(int32_t R) { return R <= 32 ? 16 : 32; }  // and of t
 struct AdapterPlan {  // rows grouped by adapter
     const int32_t* ids;  // [M]
     int64_t M;
-    int64_t rows;        // rows per workgroup, and whether ids allow four-element loads; set by the launcher
+    int64_t rows;        // rows per workgroup, workgroups, whether ids allow four-element loads; set by the launcher
+    int32_t blocks;
     bool vec;
     int32_t n, tile;
     int32_t chunk;       // rows of a chunk of the gradients, 0: forward
@@ -180,7 +181,6 @@ struct AdapterPlan {  // rows grouped by adapter
     int32_t* chunk_step; // number of a chunk's first tile
     int2* info;          // [n] {chunks, first partial sum}
 };
-hipError_t launch_adapter_plan(AdapterPlan P, hipStream_t stream);
 struct AdapterParams {
     const uint16_t* x;
     int64_t ldx;
@@ -198,7 +198,9 @@ struct AdapterParams {
     const int4* tiles;
     const int32_t* n_tiles;
     const int32_t* ids;  // a small call, without a plan: [M], or null
-    int32_t M, n;
+    int64_t M;
+    int32_t n;
+    bool stream;         // base is read past the last-level cache; set by the launcher
     bool rest;           // the rows without an adapter too
     int32_t tile_bound, slabs;  // set by the launcher
     const float* v_in;   // gradients: the forward's v, and the operands that it and w become:
@@ -210,14 +212,14 @@ hipError_t launch_adapter(AdapterParams P, int64_t tiles_bound, hipStream_t stre
 struct AdapterPack {  // B^T and A^T for the gradient's products
     const uint16_t* A;
     const uint16_t* B;
-    const int2* info;    // [n]: only adapters with rows
+    const int2* info;    // [n]: only adapters with rows; null: all
     int32_t n, R, K, N;
     u32x4* first;        // [n][units_first]
     u32x4* second;
     int64_t units_first, units_second;
 };
 int64_t adapter_units(int64_t cols, int32_t R);  // units of 16 bytes of one adapter's transposed matrix
-hipError_t launch_adapter_pack(const AdapterPack& P, hipStream_t stream);
+hipError_t launch_adapter_plan(AdapterPlan P, const AdapterPack* pack, hipStream_t stream);  // pack: or null
 struct AdapterGrad {
     const float* scale;
     int32_t n, R, K, N;
@@ -235,8 +237,12 @@ struct AdapterGrad {
     float* dA;
     float* dB;
 };
-int32_t adapter_chunk(int64_t M, int64_t K, int64_t N);
-hipError_t launch_adapter_wgrad(const AdapterGrad& P, int64_t chunks_bound, hipStream_t stream);
+struct AdapterSplit {
+    int32_t chunk;
+    bool waves16, join;
+};
+AdapterSplit adapter_split(int64_t M, int32_t R, int64_t K, int64_t N);
+hipError_t launch_adapter_wgrad(const AdapterGrad& P, const AdapterSplit& split, int64_t chunks_bound, hipStream_t stream);
 
 // MXFP4 quantizers (mxfp4_quant.hip) and products (mxfp4_gemm.hip).
 constexpr int kMxUnroll = 4;  // 8-element groups per thread
