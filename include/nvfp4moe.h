@@ -474,6 +474,9 @@ typedef struct {
     float coef;          /* finite */
 } nvfp4moe_balance_config;
 
+/* Up to this many rows the loss takes one launch, and its workspace may be NULL. */
+enum { NVFP4MOE_BALANCE_ONE_LAUNCH = 256 };
+
 /* logits [T, E] (rows ld elements apart), ids [T, K] int32 -> loss (device
  * float), counts [S, E] int32, every element written.  The probabilities are
  * summed in FP32 over at most 256 tokens and in FP64 from there, in one order:

@@ -905,11 +905,11 @@ hipError_t launch_adapter(AdapterParams P, int64_t tiles, hipStream_t stream) {
     if (P.ids) tiles = P.tile_bound = (int32_t)std::min<int64_t>(P.M, P.n + 1 + P.M / 16);
     // Few tiles: their columns are shared out, and each share repeats the first product.
     P.slabs = (int32_t)std::max<int64_t>(1, std::min<int64_t>((P.N + cols - 1) / cols, 256 / tiles));
-    // Where the rows' tensors (of the gradient x too) exceed the 256 MB of the
+    // Where the rows' tensors (of the gradient x too) fill the 256 MB of the
     // last-level cache, base, which is read once, stays out of it: 128 experts'
     // 335 MB forward 76 -> 60 us, their gradient 80 + 63 -> 74 + 55.  Below, it may be
     // there already: 201 MB 37 us, and 46 past the cache.
-    P.stream = 2 * P.M * ((P.w_pack ? 2 : 1) * (int64_t)P.K + 2 * P.N) > ((int64_t)1 << 28);
+    P.stream = 2 * P.M * ((P.w_pack ? 2 : 1) * (int64_t)P.K + 2 * P.N) >= ((int64_t)1 << 28);
     switch (adapter_rank_blocks(P.R)) {
         case 1: return adapter_run<1>(P, tiles, stream);
         case 2: return adapter_run<2>(P, tiles, stream);

@@ -16,6 +16,8 @@ using namespace nvfp4;
 
 namespace {
 
+static_assert(kBalanceOneLaunch == NVFP4MOE_BALANCE_ONE_LAUNCH, "the header's constant");
+
 constexpr size_t kAlign = 256;
 size_t up(size_t v, size_t a) { return (v + a - 1) / a * a; }
 bool aligned(const void* p, size_t a) { return ((uintptr_t)p % a) == 0; }
@@ -353,8 +355,8 @@ int nvfp4moe_router_balance_loss(const nvfp4moe_balance_config* cfg, const void*
     if (st != NVFP4_OK) return st;
     BalanceWork w;
     if (!balance_work(T, P.E, P.S, &w)) return NVFP4_E_SHAPE;
-    if (!loss || !counts || !workspace || (T > 0 && (!logits || !ids))) return NVFP4_E_NULL;
-    if (workspace_bytes < w.total) return NVFP4_E_WORKSPACE;
+    if (!loss || !counts || (T > kBalanceOneLaunch && !workspace) || (T > 0 && (!logits || !ids))) return NVFP4_E_NULL;
+    if (T > kBalanceOneLaunch && workspace_bytes < w.total) return NVFP4_E_WORKSPACE;
     if (!aligned(ids, 4) || !aligned(loss, 4) || !aligned(counts, 4) || !aligned(workspace, kAlign)) return NVFP4_E_ALIGN;
     uint8_t* ws = (uint8_t*)workspace;
     P.ids = ids;

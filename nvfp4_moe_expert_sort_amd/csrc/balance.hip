@@ -138,7 +138,7 @@ __global__ void __launch_bounds__(kChunkThreads) balance_chunk_kernel(BalancePar
     const bool whole = gridDim.x == 1;
     double total = 0.0;  // whole: of loss / factor
     int32_t s_next = 0;
-    if (blockIdx.x == 0 && threadIdx.x == 0) *P.done = 0;
+    if (!whole && blockIdx.x == 0 && threadIdx.x == 0) *P.done = 0;
     for (int32_t s = max(find_sequence<kChunkThreads>(P, first, found), 0); s < P.S; s++) {
         const int64_t s0 = seq_start(P, s), lo = max(s0, first), hi = min(seq_start(P, s + 1), past);
         if (s0 >= past) break;
@@ -399,7 +399,7 @@ hipError_t balance_type(const BalanceParams& P, hipStream_t s) {
 // workgroups, up to 256 (a lane then adds 4 tokens, or 16 in rows of more than
 // 256 experts, in FP32 before FP64 takes over).
 int32_t balance_chunk(int64_t T) {
-    if (T <= 256) return 256;
+    if (T <= kBalanceOneLaunch) return kBalanceOneLaunch;
     int32_t chunk = 64;
     while (chunk < 256 && (T + chunk - 1) / chunk > 512) chunk *= 2;
     return chunk;

@@ -135,6 +135,7 @@ hipError_t launch_router_select_backward(const SelectParams& P, bool bf16, hipSt
 
 // The balance loss, the experts' counts and the loss's gradient (balance.hip).
 constexpr int32_t kMaxSequences = 65536;
+constexpr int32_t kBalanceOneLaunch = 256;  // rows of one workgroup, which then ends the loss itself
 struct BalanceParams {
     const void* logits;  // FP32 or BF16 [T, E], rows ld apart
     int64_t ld, T;

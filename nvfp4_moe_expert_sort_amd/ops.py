@@ -12,7 +12,7 @@ import functools
 
 import torch
 
-from . import (BF16, F32, GROUP_MAX, LAYOUT_GEMM, LAYOUT_LOGICAL, MXFP4_SCALE_FLOOR, SCORE_SOFTMAX, Adapters, BalanceConfig,
+from . import (BALANCE_ONE_LAUNCH, BF16, F32, GROUP_MAX, LAYOUT_GEMM, LAYOUT_LOGICAL, MXFP4_SCALE_FLOOR, SCORE_SOFTMAX, Adapters, BalanceConfig,
                Grad, Mxfp4Tensor, Nvfp4Error, SelectConfig, _check, lib)
 
 _BF16 = (torch.bfloat16, torch.int16, torch.uint16)  # storage of BF16 bits
@@ -187,10 +187,10 @@ def router_balance_loss(logits, ids, coef: float, score: int = SCORE_SOFTMAX, of
     loss = torch.empty((1,), dtype=torch.float32, device=logits.device)
     counts = torch.empty((S, E), dtype=torch.int32, device=logits.device)
     n = _balance_workspace_bytes(T, E, S)
-    ws = torch.empty((n,), dtype=torch.uint8, device=logits.device)
+    ws = torch.empty((n,), dtype=torch.uint8, device=logits.device) if T > BALANCE_ONE_LAUNCH else None  # not used below
     st = lib().nvfp4moe_router_balance_loss(_balance_config(E, k, score, kind, coef), logits.data_ptr(), ld, T,
-                                            ids.data_ptr(), off, S, loss.data_ptr(), counts.data_ptr(), ws.data_ptr(), n,
-                                            _raw_stream(logits))
+                                            ids.data_ptr(), off, S, loss.data_ptr(), counts.data_ptr(),
+                                            None if ws is None else ws.data_ptr(), n, _raw_stream(logits))
     _check(st, "nvfp4moe_router_balance_loss")
     return loss, counts
 
@@ -213,13 +213,14 @@ def router_balance_backward(logits, counts, k: int, coef: float, score: int = SC
         with _there(stream, logits, counts, offsets, dloss, add, out):
             return router_balance_backward(logits, counts, k, coef, score, offsets, dloss, add, out)
     if out is None:
-        out = torch.empty((T, E), dtype=logits.dtype, device=logits.device)
+        out, ld_out = torch.empty((T, E), dtype=logits.dtype, device=logits.device), E
     else:
         _need(where, out, "out", (logits.dtype,), (T, E), logits.device, contiguous=False)
+        ld_out = _ld(where, out, "out")
     st = lib().nvfp4moe_router_balance_backward(
         _balance_config(E, k, score, kind, coef), logits.data_ptr(), ld, T, counts.data_ptr(), off, S,
         None if dloss is None else dloss.data_ptr(), None if add is None else add.data_ptr(),
-        0 if add is None else _ld(where, add, "add"), out.data_ptr(), _ld(where, out, "out"), _raw_stream(logits))
+        0 if add is None else _ld(where, add, "add"), out.data_ptr(), ld_out, _raw_stream(logits))
     _check(st, "nvfp4moe_router_balance_backward")
     return out
 
@@ -362,28 +363,29 @@ def adapter_alloc_workspace(M: int, K: int, N: int, rank: int, n: int, backward:
     return torch.empty((adapter_workspace_bytes(M, K, N, rank, n, backward),), dtype=torch.uint8, device=device)
 
 
+def _rows(where, t, name, shape, device):
+    """Address and row stride of a BF16 matrix of that shape, whose rows may be strided."""
+    if t.dtype not in _BF16 or t.shape != shape or t.device != device:
+        _need(where, t, name, _BF16, shape, device, contiguous=False)
+    ld, step = t.stride()
+    if step != 1 or ld < shape[1] or shape[0] < 2:
+        ld = _ld(where, t, name)
+    return t.data_ptr(), ld
+
+
 def _adapters(where, x, ids, A, B, scale):
     """Checks a set of adapters and the rows they apply to; the set, and its sizes (M, K, N, rank, n)."""
     if A.dim() != 3 or B.dim() != 3 or x.dim() != 2:
         raise ValueError(f"{where}: needs x [M, K], A [n, rank, K] and B [n, N, rank], got {tuple(x.shape)}, "
                          f"{tuple(A.shape)} and {tuple(B.shape)}")
     n, rank, K = A.shape
-    M, N = x.shape[0], B.shape[1]
-    _need(where, x, "x", _BF16, (M, K), x.device, contiguous=False)
-    _need(where, ids, "ids", (torch.int32,), (M,), x.device)
-    _need(where, A, "A", _BF16, (n, rank, K), x.device)
-    _need(where, B, "B", _BF16, (n, N, rank), x.device)
+    M, N, dev = x.shape[0], B.shape[1], x.device
+    _need(where, ids, "ids", (torch.int32,), (M,), dev)
+    _need(where, A, "A", _BF16, (n, rank, K), dev)
+    _need(where, B, "B", _BF16, (n, N, rank), dev)
     if scale is not None:
-        _need(where, scale, "scale", (torch.float32,), (n,), x.device)
+        _need(where, scale, "scale", (torch.float32,), (n,), dev)
     return Adapters(A.data_ptr(), B.data_ptr(), None if scale is None else scale.data_ptr(), n, rank, K, N), (M, K, N, rank, n)
-
-
-def _rows(where, t, name, shape, device):
-    """Address and row stride of a BF16 matrix, or of none."""
-    if t is None:
-        return None, 0
-    _need(where, t, name, _BF16, shape, device, contiguous=False)
-    return t.data_ptr(), _ld(where, t, name)
 
 
 def adapter_linear(x, ids, A, B, base=None, scale=None, out=None, v=None, workspace=None, stream=None):
@@ -395,22 +397,25 @@ def adapter_linear(x, ids, A, B, base=None, scale=None, out=None, v=None, worksp
     where = "adapter_linear"
     ad, (M, K, N, rank, n) = _adapters(where, x, ids, A, B, scale)
     dev = x.device
-    base_at, ld_base = _rows(where, base, "base", (M, N), dev)
+    x_at, ldx = _rows(where, x, "x", (M, K), dev)
+    base_at, ld_base = (None, 0) if base is None else _rows(where, base, "base", (M, N), dev)
     if _elsewhere(x, stream):
         with _there(stream, x, ids, A, B, base, scale, out, v, workspace):
             return adapter_linear(x, ids, A, B, base, scale, out, v, workspace)
-    if out is None:
+    if out is not None:
+        out_at, ld_out = _rows(where, out, "out", (M, N), dev)
+    else:
         out = torch.empty((M, N), dtype=x.dtype, device=dev)
-    out_at, ld_out = _rows(where, out, "out", (M, N), dev)
+        out_at, ld_out = out.data_ptr(), N
     if v is not None:
         _need(where, v, "v", (torch.float32,), (M, rank), dev)
     if workspace is None:
         workspace = adapter_alloc_workspace(M, K, N, rank, n, False, dev)
     else:
         _need(where, workspace, "workspace", (torch.uint8,), (workspace.numel(),), dev)
-    st = lib().nvfp4moe_adapter_linear(ad, x.data_ptr(), M, _ld(where, x, "x"), ids.data_ptr(), base_at, ld_base, out_at,
-                                       ld_out, None if v is None else v.data_ptr(), workspace.data_ptr(),
-                                       workspace.numel(), _raw_stream(x))
+    st = lib().nvfp4moe_adapter_linear(ad, x_at, M, ldx, ids.data_ptr(), base_at, ld_base, out_at, ld_out,
+                                       None if v is None else v.data_ptr(), workspace.data_ptr(), workspace.numel(),
+                                       _raw_stream(x))
     _check(st, "nvfp4moe_adapter_linear")
     return out
 
@@ -422,9 +427,10 @@ def adapter_backward(x, ids, A, B, v, dy, base=None, scale=None, out=None, works
     where = "adapter_backward"
     ad, (M, K, N, rank, n) = _adapters(where, x, ids, A, B, scale)
     dev = x.device
+    x_at, ldx = _rows(where, x, "x", (M, K), dev)
     _need(where, v, "v", (torch.float32,), (M, rank), dev)
     dy_at, ld_dy = _rows(where, dy, "dy", (M, N), dev)
-    base_at, ld_base = _rows(where, base, "base", (M, K), dev)
+    base_at, ld_base = (None, 0) if base is None else _rows(where, base, "base", (M, K), dev)
     if _elsewhere(x, stream):
         with _there(stream, x, ids, A, B, v, dy, base, scale, workspace, *(out or ())):
             return adapter_backward(x, ids, A, B, v, dy, base, scale, out, workspace)
@@ -441,9 +447,9 @@ def adapter_backward(x, ids, A, B, v, dy, base=None, scale=None, out=None, works
         workspace = adapter_alloc_workspace(M, K, N, rank, n, True, dev)
     else:
         _need(where, workspace, "workspace", (torch.uint8,), (workspace.numel(),), dev)
-    st = lib().nvfp4moe_adapter_backward(ad, x.data_ptr(), M, _ld(where, x, "x"), ids.data_ptr(), v.data_ptr(), dy_at, ld_dy,
-                                         base_at, ld_base, dx_at, ld_dx, dA.data_ptr(), dB.data_ptr(),
-                                         workspace.data_ptr(), workspace.numel(), _raw_stream(x))
+    st = lib().nvfp4moe_adapter_backward(ad, x_at, M, ldx, ids.data_ptr(), v.data_ptr(), dy_at, ld_dy, base_at, ld_base,
+                                         dx_at, ld_dx, dA.data_ptr(), dB.data_ptr(), workspace.data_ptr(),
+                                         workspace.numel(), _raw_stream(x))
     _check(st, "nvfp4moe_adapter_backward")
     return dx, dA, dB
 

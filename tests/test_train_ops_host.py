@@ -49,7 +49,7 @@ def test_balance_refuses_bad_arguments(m):
     for bad in (dict(ld=127), dict(T=-1), dict(T=1 << 31), dict(S=0), dict(S=65537), dict(off=None, S=2)):
         assert _loss(m, c, **bad) == _back(m, c, **bad) == SHAPE, bad
     assert _back(m, c, ldo=127) == _back(m, c, add=FAKE, ld_add=127) == SHAPE
-    for bad in (dict(logits=None), dict(ids=None), dict(loss=None), dict(counts=None), dict(ws=None)):
+    for bad in (dict(logits=None), dict(ids=None), dict(loss=None), dict(counts=None), dict(ws=None, T=257)):
         assert _loss(m, c, **bad) == NULL, bad
     for bad in (dict(logits=None), dict(counts=None), dict(out=None)):
         assert _back(m, c, **bad) == NULL, bad
@@ -59,8 +59,9 @@ def test_balance_refuses_bad_arguments(m):
         assert _back(m, c, **bad) == ALIGN, bad
     assert _back(m, c, add=FAKE, ld_add=256) == ARG  # in place, another stride
     assert _back(m, c, T=0, logits=None, counts=None, out=None) == 0
-    need = m.lib().nvfp4moe_balance_workspace_bytes(4, 128, 2)
-    assert need % 256 == 0 and _loss(m, c, n=need - 1) == WORKSPACE
+    need = m.lib().nvfp4moe_balance_workspace_bytes(257, 128, 2)
+    assert need % 256 == 0 and _loss(m, c, T=257, n=need - 1) == WORKSPACE
+    assert m.BALANCE_ONE_LAUNCH == 256
 
 
 def test_balance_workspace(m):
