@@ -591,7 +591,7 @@ NVFP4MOE_API int nvfp4moe_mxfp4_grouped_linear(const uint16_t* x, int64_t R, int
  * [out_features, rank], both BF16 and contiguous, and the factor scale[a]
  * (FP32 [n], or NULL for 1).  Adapters of a lower rank are padded with zeros.
  * n 1..1024; rank 8..128, in_features and out_features 8..2^24 - 1, all three
- * multiples of 8; A and B 16-byte aligned. */
+ * multiples of 8; fewer than 2^37 elements of A and B; both 16-byte aligned. */
 typedef struct {
     const uint16_t* A;
     const uint16_t* B;
@@ -609,7 +609,8 @@ typedef struct {
  * with base the shared projection's output (nvfp4moe_mxfp4_linear's, say) or
  * NULL for 0.  Rows whose id lies outside [0, n) have no adapter: out_r is
  * base_r to the bit (or 0), v_r is 0.  Sums are FP32, rounded once at the end;
- * v enters the second product as two BF16 values (within 2^-16 of it).  A
+ * v enters the second product as two BF16 values (within 2^-16 of it; an
+ * infinite element of B gives NaN where the formula may have an infinity).  A
  * row's bits depend on that row alone: not on the batch, nor on its place in it.
  * x [M, in_features], base and out [M, out_features] BF16, rows ldx, ld_base
  * and ld_out apart (multiples of 8, pointers 16-byte aligned); out may be base
@@ -632,7 +633,8 @@ NVFP4MOE_API int nvfp4moe_adapter_linear(const nvfp4moe_adapters* ad, const uint
  * or NULL for 0 (rows without an adapter: dx_r is base_r or 0).  Every element
  * of dA and dB is written, those of adapters without rows with zeros; the same
  * inputs give the same bits in every run.  w and v enter the sums in full (three
- * BF16 values each).  dx may be base (the same stride); outputs may not overlap
+ * BF16 values each; an infinite element of A, B, x or dy gives NaN in what it
+ * enters where the formula may have an infinity).  dx may be base (the same stride); outputs may not overlap
  * anything else.  dA and dB 16-byte aligned, the rest as for the forward. */
 NVFP4MOE_API int nvfp4moe_adapter_backward(const nvfp4moe_adapters* ad, const uint16_t* x, int64_t M, int64_t ldx,
                                            const int32_t* ids, const float* v, const uint16_t* dy, int64_t ld_dy,

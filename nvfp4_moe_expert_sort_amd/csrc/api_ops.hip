@@ -225,6 +225,8 @@ int adapter_shape(const nvfp4moe_adapters* ad, int64_t M) {
     for (const int32_t w : {ad->in_features, ad->out_features})
         if (w < 8 || w % 8 != 0 || w >= (1 << 24)) return NVFP4_E_SHAPE;
     if (M < 0 || M >= ((int64_t)1 << 26)) return NVFP4_E_SHAPE;
+    // (of A and B together; more than any memory holds, and what the launches' sizes allow)
+    if ((int64_t)ad->n * ad->rank * ((int64_t)ad->in_features + ad->out_features) >= ((int64_t)1 << 37)) return NVFP4_E_SHAPE;
     return NVFP4_OK;
 }
 int adapter_planes(const nvfp4moe_adapters* ad) {

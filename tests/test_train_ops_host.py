@@ -85,7 +85,8 @@ def _grad(m, ad, x=FAKE, M=4, ldx=64, ids=FAKE, v=FAKE, dy=FAKE, ldy=72, base=No
 
 
 @pytest.mark.parametrize("bad", [dict(n=0), dict(n=1025), dict(rank=0), dict(rank=4), dict(rank=12), dict(rank=136),
-                                 dict(K=0), dict(K=60), dict(K=1 << 24), dict(N=-8), dict(N=70), dict(N=1 << 24)])
+                                 dict(K=0), dict(K=60), dict(K=1 << 24), dict(N=-8), dict(N=70), dict(N=1 << 24),
+                                 dict(n=1024, rank=128, K=1 << 19, N=1 << 19)])
 def test_adapters_refuse_bad_sizes(m, bad):
     ad = _ad(m, **bad)
     assert _lin(m, ad, ldx=1 << 25, ldo=1 << 25) == _grad(m, ad, ldx=1 << 25, ldy=1 << 25, ldo=1 << 25) == SHAPE
