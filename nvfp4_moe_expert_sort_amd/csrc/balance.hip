@@ -120,15 +120,19 @@ __device__ __forceinline__ void load_row(const L* row, const BalanceParams& P, i
 
 }  // namespace
 
-// A workgroup takes P.chunk rows.  For each sequence in them it adds up the
-// probabilities (a lane its own experts over its tokens, then the wavefront's
-// token slots by exchanges, then the wavefronts in LDS) and the counts; chunk
-// b's part of sequence s goes to slot b + s: a walk along the rows raises b or s
-// at every step, so no two parts share one.  A call of one chunk has its
+// A workgroup takes P.chunk rows, kTok at a time.  Their probabilities are
+// formed once, whatever sequences they belong to, and then added up sequence by
+// sequence (a lane its own experts over its tokens, then the wavefront's token
+// slots by exchanges, then the wavefronts in LDS), like the counts: a workgroup
+// whose rows belong to several, which the kernel's end waits for, repeats only
+// the sums (once the whole pass, 16384 rows in 13 sequences: LOSS_OLD against LOSS_NEW us).
+// Chunk b's part of sequence s goes to slot b + s: a walk along the rows raises
+// b or s at every step, so no two parts share one.  A call of one chunk has its
 // sequences whole here and needs no join.
 template <int LT, int NV, typename L>
 __global__ void __launch_bounds__(kChunkThreads) balance_chunk_kernel(BalanceParams P) {
     constexpr int kTok = kChunkThreads / LT, kWaves = kChunkThreads / 64;
+    constexpr int kIds = (kTok * kMaxTopK + kChunkThreads - 1) / kChunkThreads;
     __shared__ float part[kWaves][LT * NV];
     __shared__ int32_t hist[LT * NV];
     __shared__ int32_t found[kWaves];
@@ -137,35 +141,28 @@ __global__ void __launch_bounds__(kChunkThreads) balance_chunk_kernel(BalancePar
     const int64_t first = (int64_t)blockIdx.x * P.chunk, past = min(P.T, first + P.chunk);
     const bool whole = gridDim.x == 1;
     double total = 0.0;  // whole: of loss / factor
-    int32_t s_next = 0;
+    int32_t s_next = 0;  // whole: the first sequence whose counts are not written
     if (!whole && blockIdx.x == 0 && threadIdx.x == 0) *P.done = 0;
-    for (int32_t s = max(find_sequence<kChunkThreads>(P, first, found), 0); s < P.S; s++) {
-        const int64_t s0 = seq_start(P, s), lo = max(s0, first), hi = min(seq_start(P, s + 1), past);
-        if (s0 >= past) break;
-        if (lo >= hi) continue;
-        for (int e = threadIdx.x; e < P.E; e += kChunkThreads) hist[e] = 0;
-        __syncthreads();
-        float acc[NV];
+    float l[NV], acc[NV];
+    int32_t id[kIds], id_tok[kIds];  // the thread's ids of a pass, and which token's each is
+    auto load = [&](int64_t t0) {
+        load_row<LT, NV, L>((const L*)P.logits + min(t0 + slot, past - 1) * P.ld, P, lane, l);
 #pragma unroll
-        for (int i = 0; i < NV; i++) acc[i] = 0.0f;
-        for (int64_t t0 = lo; t0 < hi; t0 += kTok) {
-            const bool live = t0 + slot < hi;
-            float l[NV], w[NV], other[NV];
-            load_row<LT, NV, L>((const L*)P.logits + min(t0 + slot, hi - 1) * P.ld, P, lane, l);
-            if (t0 == lo)  // (between the load and its use)
-                for (int64_t i = lo * P.K + threadIdx.x; i < hi * P.K; i += kChunkThreads) {
-                    const int32_t e = P.ids[i];
-                    if (e >= 0 && e < P.E) atomicAdd(&hist[e], 1);
-                }
-            score_terms<LT, NV>(l, P.sigmoid, w, other);
-            float sum = 0.0f;
+        for (int j = 0; j < kIds; j++)
+            id[j] = id_tok[j] < min((int64_t)kTok, past - t0) ? P.ids[t0 * P.K + j * kChunkThreads + threadIdx.x] : -1;
+    };
 #pragma unroll
-            for (int i = 0; i < NV; i++) sum += w[i];
-            sum = tok_sum<LT>(sum);
-            const float inv = live && sum > 0.0f ? 1.0f / sum : 0.0f;
+    for (int j = 0; j < kIds; j++) id_tok[j] = (j * kChunkThreads + (int)threadIdx.x) / P.K;
+    if (first < past) load(first);  // (on its way while the sequence is looked up)
 #pragma unroll
-            for (int i = 0; i < NV; i++) acc[i] = __builtin_fmaf(w[i], inv, acc[i]);
-        }
+    for (int i = 0; i < NV; i++) acc[i] = 0.0f;
+    for (int e = threadIdx.x; e < P.E; e += kChunkThreads) hist[e] = 0;
+    // The sequence that the walk has come to, and its rows.
+    int32_t s = max(find_sequence<kChunkThreads>(P, first, found), 0);
+    int64_t lo = seq_start(P, min(s, P.S)), hi = seq_start(P, min(s + 1, P.S));
+    __syncthreads();
+    // Writes the sums and counts of the sequence's rows in this chunk, and clears them.
+    auto flush = [&] {
         if (LT == 16)
 #pragma unroll
             for (int i = 0; i < NV; i++) {
@@ -176,6 +173,8 @@ __global__ void __launch_bounds__(kChunkThreads) balance_chunk_kernel(BalancePar
 #pragma unroll
             for (int i = 0; i < NV / 4; i++)
                 *reinterpret_cast<float4*>(&part[wave][(i * LT + lane) * 4]) = float4{acc[4 * i], acc[4 * i + 1], acc[4 * i + 2], acc[4 * i + 3]};
+#pragma unroll
+        for (int i = 0; i < NV; i++) acc[i] = 0.0f;
         __syncthreads();
         const int64_t at = (whole ? s : (int64_t)blockIdx.x + s) * P.E;
         double share = 0.0;
@@ -184,6 +183,7 @@ __global__ void __launch_bounds__(kChunkThreads) balance_chunk_kernel(BalancePar
 #pragma unroll
             for (int k = 0; k < kWaves; k++) sum += part[k][e];
             const int32_t n = hist[e];
+            hist[e] = 0;
             if (whole) {
                 P.counts[at + e] = n;
                 share += (double)sum * (double)n;
@@ -204,6 +204,33 @@ __global__ void __launch_bounds__(kChunkThreads) balance_chunk_kernel(BalancePar
             for (int k = 0; k < kWaves; k++) share += shares[k];
             total += share / (double)(hi - lo);
         }
+    };
+    for (int64_t t0 = first; t0 < past; t0 += kTok) {
+        if (t0 > first) load(t0);
+        const int64_t end = min(t0 + kTok, past);
+        float w[NV], other[NV];
+        score_terms<LT, NV>(l, P.sigmoid, w, other);
+        float sum = 0.0f;
+#pragma unroll
+        for (int i = 0; i < NV; i++) sum += w[i];
+        sum = tok_sum<LT>(sum);
+        const float inv = t0 + slot < end && sum > 0.0f ? 1.0f / sum : 0.0f;
+        while (s < P.S && lo < end) {
+            if (hi > max(lo, t0)) {
+                const int from = (int)max(lo - t0, (int64_t)0), to = (int)min(hi - t0, end - t0);  // of the pass's tokens
+                const float in = slot >= from && slot < to ? inv : 0.0f;
+#pragma unroll
+                for (int i = 0; i < NV; i++) acc[i] = __builtin_fmaf(w[i], in, acc[i]);
+#pragma unroll
+                for (int j = 0; j < kIds; j++)
+                    if (id_tok[j] >= from && id_tok[j] < to && id[j] >= 0 && id[j] < P.E) atomicAdd(&hist[id[j]], 1);
+                if (hi <= end || end == past) flush();
+            }
+            if (hi > end || (hi == end && end == past)) break;
+            s++;
+            lo = hi;
+            hi = seq_start(P, min(s + 1, P.S));
+        }
     }
     if (whole) {  // (sequences without rows have no counts)
         for (int64_t i = (int64_t)s_next * P.E + threadIdx.x; i < (int64_t)P.S * P.E; i += kChunkThreads) P.counts[i] = 0;
@@ -213,6 +240,10 @@ __global__ void __launch_bounds__(kChunkThreads) balance_chunk_kernel(BalancePar
 
 // Adds the slots of one sequence and 64 experts in FP64, in one order; the
 // workgroup that is last to finish adds up the workgroups' shares of the loss.
+// Each share is one value, stored and loaded at the scope of the device, which
+// no L2 keeps for itself, and stored for certain before its workgroup is
+// counted: with nothing else handed over, no cache has to be written back or
+// dropped (two fences: 7.8 us a launch at 13 sequences of 256 experts; so: 5.0).
 __global__ void __launch_bounds__(kJoinThreads) balance_join_kernel(BalanceParams P) {
     constexpr int kStripes = kJoinThreads / 64, kAhead = 4;
     __shared__ double sums[kStripes][64];
@@ -257,16 +288,17 @@ __global__ void __launch_bounds__(kJoinThreads) balance_join_kernel(BalanceParam
         if (e < P.E) P.counts[(int64_t)s * P.E + e] = n;
         const double v = wave_sum(hi > lo ? sum * (double)n / (double)(hi - lo) : 0.0);
         if (col == 0) {
-            P.part[blockIdx.x] = v;
-            __threadfence();
-            last = atomicAdd(P.done, 1u) == gridDim.x - 1;
+            __hip_atomic_store(&P.part[blockIdx.x], v, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+            asm volatile("" ::: "memory");
+            __builtin_amdgcn_s_waitcnt(0);  // the store has reached memory
+            asm volatile("" ::: "memory");
+            last = __hip_atomic_fetch_add(P.done, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) == gridDim.x - 1;
         }
     }
     __syncthreads();
     if (!last) return;
-    __threadfence();
     double total = 0.0;
-    for (uint32_t i = threadIdx.x; i < gridDim.x; i += kJoinThreads) total += P.part[i];
+    for (uint32_t i = threadIdx.x; i < gridDim.x; i += kJoinThreads) total += __hip_atomic_load(&P.part[i], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
     total = wave_sum(total);
     if (col == 0) sums[0][stripe] = total;
     __syncthreads();
