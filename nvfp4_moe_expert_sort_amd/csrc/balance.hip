@@ -133,7 +133,7 @@ template <int LT, int NV, typename L>
 __global__ void __launch_bounds__(kChunkThreads) balance_chunk_kernel(BalanceParams P) {
     constexpr int kTok = kChunkThreads / LT, kWaves = kChunkThreads / 64;
     constexpr int kIds = (kTok * kMaxTopK + kChunkThreads - 1) / kChunkThreads;
-    __shared__ float part[kWaves][LT * NV];
+    __shared__ __attribute__((aligned(16))) float part[kWaves][LT * NV];
     __shared__ int32_t hist[LT * NV];
     __shared__ int32_t found[kWaves];
     __shared__ double shares[kWaves];
@@ -163,16 +163,32 @@ __global__ void __launch_bounds__(kChunkThreads) balance_chunk_kernel(BalancePar
     __syncthreads();
     // Writes the sums and counts of the sequence's rows in this chunk, and clears them.
     auto flush = [&] {
-        if (LT == 16)
+        if constexpr (LT == 16) {
+            // Of each two values, the half of the wavefront that adds up the first
+            // gives the other half its part of the second; so do the halves' rows of
+            // 16 lanes.  Row r is left with the sums of acc[r NV / 4] and on (every lane
+            // fetching all of its counterparts' values: 3 us more of 13).
+            constexpr int kLeft = NV / 4;
+            float sum2[2 * kLeft], sum4[kLeft];
 #pragma unroll
-            for (int i = 0; i < NV; i++) {
-                acc[i] += __shfl_xor(acc[i], 16, kWave);
-                acc[i] += __shfl_xor(acc[i], 32, kWave);
+            for (int i = 0; i < 2 * kLeft; i++) {
+                const auto v = __builtin_amdgcn_permlane32_swap(__float_as_uint(acc[i]), __float_as_uint(acc[i + 2 * kLeft]), false, false);
+                sum2[i] = __uint_as_float(v[0]) + __uint_as_float(v[1]);
             }
-        if (LT == 64 || (threadIdx.x & 63) < 16)
+#pragma unroll
+            for (int i = 0; i < kLeft; i++) {
+                const auto v = __builtin_amdgcn_permlane16_swap(__float_as_uint(sum2[i]), __float_as_uint(sum2[i + kLeft]), false, false);
+                sum4[i] = __uint_as_float(v[0]) + __uint_as_float(v[1]);
+            }
+            const int first_acc = (threadIdx.x & 63) / 16 * kLeft;
+            float* to = &part[wave][(first_acc / 4 * LT + lane) * 4 + first_acc % 4];
+#pragma unroll
+            for (int i = 0; i < kLeft; i++) to[i] = sum4[i];
+        } else {
 #pragma unroll
             for (int i = 0; i < NV / 4; i++)
                 *reinterpret_cast<float4*>(&part[wave][(i * LT + lane) * 4]) = float4{acc[4 * i], acc[4 * i + 1], acc[4 * i + 2], acc[4 * i + 3]};
+        }
 #pragma unroll
         for (int i = 0; i < NV; i++) acc[i] = 0.0f;
         __syncthreads();
