@@ -414,12 +414,23 @@ __global__ void __launch_bounds__(kAdWaves * 64, RB < 4 || (RB == 4 && kGrad) ? 
         if constexpr (kSmall) return (int64_t)rows[min(m, count - 1)];
         return (int64_t)P.order[t.y + min(m, count - 1)];
     };
-    if (a < 0) {  // rows without an adapter
-        const int pieces = P.N / 8;
-        for (int64_t k = slab * (kAdWaves * 64) + threadIdx.x; k < (int64_t)count * pieces; k += P.slabs * (kAdWaves * 64)) {
-            const int64_t r = row_of(k / pieces), c = k % pieces * 8;
-            const u32x4 z = {0, 0, 0, 0};
-            *reinterpret_cast<u32x4*>(P.out + r * P.ld_out + c) = kBase ? load16(P.base + r * P.ld_base + c) : z;
+    if (a < 0) {
+        // Rows without an adapter, one a wavefront, eight loads in flight (one: 32
+        // rows of 4096 columns take 19 us, as long as a tile with an adapter).
+        constexpr int kLoads = 8;
+        const int pieces = P.N / 8, c0 = (int)((int64_t)pieces * slab / P.slabs), c1 = (int)((int64_t)pieces * (slab + 1) / P.slabs);
+        for (int m = wave; m < count; m += kAdWaves) {
+            const int64_t r = row_of(m);
+            uint16_t* to = P.out + r * P.ld_out;
+            for (int c = c0 + lane; c < c1; c += 64 * kLoads) {
+                u32x4 z[kLoads];
+#pragma unroll
+                for (int j = 0; j < kLoads; j++) z[j] = kBase ? load16(P.base + r * P.ld_base + 8 * min(c + 64 * j, c1 - 1)) : u32x4{0, 0, 0, 0};
+                issue();
+#pragma unroll
+                for (int j = 0; j < kLoads; j++)
+                    if (c + 64 * j < c1) *reinterpret_cast<u32x4*>(to + 8 * (c + 64 * j)) = z[j];
+            }
         }
         if (!kGrad && P.v && slab == 0)
             for (int k = threadIdx.x; k < count * P.R; k += kAdWaves * 64) P.v[row_of(k / P.R) * P.R + k % P.R] = 0.0f;
