@@ -483,11 +483,11 @@ enum { NVFP4MOE_BALANCE_ONE_LAUNCH = 256 };
  * the same bits in every run.
  * Requirements: 0 <= T < 2^31, 1 <= S <= 65536, ld >= E; logits aligned to
  * their element, the others to 4 bytes; workspace 256-byte aligned,
- * nvfp4moe_balance_workspace_bytes(T, E, S) bytes (0 for sizes out of range),
- * not shared by calls that may run at the same time.  Offsets outside [0, T]
- * are taken as the nearer end; with decreasing ones the results are undefined
- * (no access leaves the buffers).  Outputs may not overlap inputs.  No
- * synchronisation. */
+ * nvfp4moe_balance_workspace_bytes(T, E, S) bytes (0 for sizes out of range;
+ * enough for fewer rows too), not shared by calls that may run at the same
+ * time.  Offsets outside [0, T] are taken as the nearer end; with decreasing
+ * ones the results are undefined (no access leaves the buffers).  Outputs may
+ * not overlap inputs.  No synchronisation. */
 NVFP4MOE_API size_t nvfp4moe_balance_workspace_bytes(int64_t T, int32_t n_experts, int32_t n_sequences);
 NVFP4MOE_API int nvfp4moe_router_balance_loss(const nvfp4moe_balance_config* cfg, const void* logits, int64_t ld, int64_t T,
                                               const int32_t* ids, const int32_t* seq_offsets, int32_t n_sequences,
@@ -618,8 +618,9 @@ typedef struct {
  * [M, rank], 16-byte aligned, may be NULL) is what the gradients need of the
  * forward pass.  M < 2^26; M == 0 is a no-op.
  * Workspace: nvfp4moe_adapter_workspace_bytes(ad, M, backward) bytes (0 for
- * sizes out of range; ad's pointers are not read), 256-byte aligned, not shared
- * by calls that may run at the same time.  No synchronisation. */
+ * sizes out of range; ad's pointers are not read; enough for fewer rows too,
+ * and with backward for both passes), 256-byte aligned, not shared by calls that
+ * may run at the same time.  No synchronisation. */
 NVFP4MOE_API size_t nvfp4moe_adapter_workspace_bytes(const nvfp4moe_adapters* ad, int64_t M, int32_t backward);
 NVFP4MOE_API int nvfp4moe_adapter_linear(const nvfp4moe_adapters* ad, const uint16_t* x, int64_t M, int64_t ldx,
                                          const int32_t* ids, const uint16_t* base, int64_t ld_base, uint16_t* out,

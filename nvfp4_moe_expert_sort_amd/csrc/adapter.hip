@@ -888,6 +888,13 @@ hipError_t launch_adapter_plan(AdapterPlan P, const AdapterPack* pack, hipStream
     return hipGetLastError();
 }
 
+// Rows of a forward tile.  Up to rank 16 always 16 rows, of which a CU holds two
+// tiles.  Above, 16 rows take a tile less time as long as every CU has one at
+// most (4096 rows of 4096 columns: rank 64 29 against 33 us, rank 128 40 against
+// 46), and 32 read the adapters half as often (65536 rows: rank 32 365 against
+// 344 us, rank 64 500 against 377, rank 128 705 against 484).
+int adapter_tile(int32_t R, int64_t M, int64_t n) { return R <= 16 || M / 16 + n + 1 <= 256 ? 16 : 32; }
+
 namespace {
 
 template <int RB, bool kBase>
@@ -897,8 +904,10 @@ hipError_t adapter_start(const AdapterParams& P, int64_t tiles, hipStream_t s) {
         hipLaunchKernelGGL((adapter_kernel<RB, kAdTile / 16, true, kBase, false>), grid, block, 0, s, P);
     else if (P.ids)
         hipLaunchKernelGGL((adapter_kernel<RB, 1, false, kBase, true>), grid, block, 0, s, P);
-    else
-        hipLaunchKernelGGL((adapter_kernel<RB, adapter_tile(16 * RB) / 16, false, kBase, false>), grid, block, 0, s, P);
+    else if (adapter_tile(P.R, P.M, P.n) == 16)
+        hipLaunchKernelGGL((adapter_kernel<RB, 1, false, kBase, false>), grid, block, 0, s, P);
+    else if constexpr (RB > 1)
+        hipLaunchKernelGGL((adapter_kernel<RB, 2, false, kBase, false>), grid, block, 0, s, P);
     return hipGetLastError();
 }
 template <int RB>
@@ -937,9 +946,11 @@ AdapterSplit adapter_split(int64_t M, int32_t R, int64_t K, int64_t N) {
     if (R <= 16 && M <= 1024) {  // one chunk, and its steps one or two a wavefront: no sums to join
         s.waves16 = true;
         s.chunk = 1024;
+        s.most = (int32_t)(M / 1024);
     } else {  // the columns' slabs times the chunks are the workgroups that the CUs hold at a time
         const int64_t chunks = std::max<int64_t>(1, (R <= 16 ? 1024 : 512) / slabs);
         s.chunk = (int32_t)std::min<int64_t>((std::max<int64_t>(M, 1) + 128 * chunks - 1) / (128 * chunks) * 128, (int64_t)1 << 30);
+        s.most = (int32_t)std::min<int64_t>(chunks, M / 128);
     }
     s.join = M > s.chunk;
     return s;

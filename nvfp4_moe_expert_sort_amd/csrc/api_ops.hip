@@ -89,7 +89,8 @@ struct BalanceWork {
 };
 bool balance_work(int64_t T, int64_t E, int64_t S, BalanceWork* w) {
     if (T < 0 || T >= ((int64_t)1 << 31) || E < 1 || E > kMaxExperts || S < 1 || S > kMaxSequences) return false;
-    const int64_t chunk = balance_chunk(T), slots = (T + chunk - 1) / chunk + S;
+    // chunks of 64 rows up to 512 of them, then of more: the most that any smaller T has
+    const int64_t slots = std::max(std::min<int64_t>((T + 63) / 64, 512), (T + 255) / 256) + S;
     w->csum = up(slots * E * 4, kAlign);
     w->part = 2 * w->csum;
     w->done = w->part + up(S * ((E + 63) / 64) * 8, kAlign);
@@ -235,7 +236,8 @@ int adapter_planes(const nvfp4moe_adapters* ad) {
     return NVFP4_OK;
 }
 // Workspace: the plan (rows by adapter, its tables) and, for the gradients, the
-// transposed adapters, w and v as operands and partial sums.
+// transposed adapters, w and v as operands and partial sums.  A size for M rows
+// is enough for fewer: no part of it falls as M grows.
 struct AdapterWork {
     size_t order, tiles, chunks, steps, info, first, second, v_pack, w_pack, slots, total;
     int64_t n_tiles, n_chunks;
@@ -244,7 +246,7 @@ struct AdapterWork {
 AdapterWork adapter_work(const nvfp4moe_adapters* ad, int64_t M, bool backward) {
     AdapterWork w{};
     const int64_t n = ad->n, R = ad->rank, K = ad->in_features, N = ad->out_features;
-    w.n_tiles = M / (backward ? kAdTile : adapter_tile(ad->rank)) + std::min(M, n + 1);
+    w.n_tiles = M / (backward ? kAdTile : 16) + std::min(M, n + 1);
     w.order = kAlign;
     w.tiles = w.order + up(M * 4, kAlign);
     w.total = w.tiles + up(w.n_tiles * 16, kAlign);
@@ -254,15 +256,15 @@ AdapterWork adapter_work(const nvfp4moe_adapters* ad, int64_t M, bool backward) 
     w.second = w.first + up(n * adapter_units(N, ad->rank) * 16, kAlign);
     w.total = w.second + up(n * adapter_units(K, ad->rank) * 16, kAlign);
     w.split = adapter_split(M, ad->rank, K, N);
-    w.n_chunks = M / w.split.chunk + n;
+    w.n_chunks = w.split.most + n;
     w.chunks = w.total;
     w.steps = w.chunks + up(w.n_chunks * 16, kAlign);
     w.v_pack = w.steps + up(w.n_chunks * 4, kAlign);
     w.w_pack = w.v_pack + (size_t)w.n_tiles * adapter_rank_blocks(ad->rank) * 3 * 1024;
     w.slots = 2 * w.w_pack - w.v_pack;
-    // chunks of adapters that have more than one: each such adapter has more
-    // than `chunk` rows, so at most twice its rows / chunk of them
-    w.total = w.slots + (w.split.join ? up((2 * M / w.split.chunk) * R * (K + N) * 4, kAlign) : 0);
+    // chunks of adapters that have more than one: at most floor(rows / chunk) + 1
+    // each, which is at most twice the first term
+    w.total = w.slots + (w.split.waves16 ? 0 : up(2 * w.split.most * R * (K + N) * 4, kAlign));
     return w;
 }
 int adapter_rows(const uint16_t* p, int64_t ld, int64_t cols) {
@@ -522,7 +524,7 @@ int nvfp4moe_adapter_linear(const nvfp4moe_adapters* ad, const uint16_t* x, int6
     plan.ids = ids;
     plan.M = M;
     plan.n = ad->n;
-    plan.tile = adapter_tile(ad->rank);
+    plan.tile = adapter_tile(ad->rank, M, ad->n);
     plan.rest = p.rest;
     plan.n_tables = (int32_t*)ws;
     plan.order = (int32_t*)(ws + w.order);

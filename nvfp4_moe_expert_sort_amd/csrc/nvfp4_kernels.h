@@ -165,7 +165,7 @@ hipError_t launch_balance(const BalanceParams& P, bool bf16, hipStream_t stream)
 // Low-rank adapters and their gradients (adapter.hip).
 constexpr int kMaxRank = 128;
 constexpr int kAdTile = 32;  // rows of a row tile of the gradients, a step of the weights' own
-constexpr int adapter_tile(int32_t R) { return R <= 32 ? 16 : 32; }  // and of the forward pass
+int adapter_tile(int32_t R, int64_t M, int64_t n);  // and of the forward pass
 struct AdapterPlan {  // rows grouped by adapter
     const int32_t* ids;  // [M]
     int64_t M;
@@ -240,6 +240,7 @@ struct AdapterGrad {
 };
 struct AdapterSplit {
     int32_t chunk;
+    int32_t most;  // at least M / chunk, and not falling as M grows
     bool waves16, join;
 };
 AdapterSplit adapter_split(int64_t M, int32_t R, int64_t K, int64_t N);

@@ -170,3 +170,15 @@ def test_plain_adapter_against_autograd():
     assert torch.allclose(out, torch.stack(rows).detach())
     (dx, dA, dB), _ = R.adapter_backward(x.detach(), ids, A.detach(), B.detach(), v, dy, None, scale)
     assert torch.allclose(dx, x.grad) and torch.allclose(dA, A.grad) and torch.allclose(dB, B.grad)
+
+
+def test_a_workspace_is_enough_for_fewer_rows(m):
+    """Whatever sizes the kernels choose for a number of rows, in steps around each of their changes."""
+    rows = sorted({max(0, b + d) for b in (0, 16, 64, 128, 256, 512, 1000, 1024, 2048, 4096, 8192, 16384, 32768, 65536, 131072, 1 << 20)
+                   for d in (-129, -1, 0, 1, 17, 130)})
+    for n, rank, K, N in ((1, 8, 64, 64), (8, 16, 4096, 4096), (3, 32, 64, 200), (128, 16, 2048, 768), (4, 64, 4096, 4096), (1024, 128, 72, 64)):
+        size = m.lib().nvfp4moe_adapter_workspace_bytes
+        fwd, both = ([size(_ad(m, n=n, rank=rank, K=K, N=N), M, back) for M in rows] for back in (0, 1))
+        assert fwd == sorted(fwd) and both == sorted(both) and fwd[0] > 0 and all(a <= b for a, b in zip(fwd, both))
+    sizes = [m.lib().nvfp4moe_balance_workspace_bytes(T, 128, 7) for T in rows]
+    assert sizes == sorted(sizes) and sizes[0] > 0
