@@ -20,6 +20,7 @@ typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 typedef float f32x4 __attribute__((ext_vector_type(4)));
 
 constexpr int kAdWaves = 8;          // wavefronts that share the first product's K
+constexpr uint32_t kCus = 256;
 constexpr int kPlanThreads = 1024;
 constexpr int kBins = kMaxExperts + 1;  // adapters, and the rows without one
 
@@ -348,11 +349,18 @@ __global__ void __launch_bounds__(kAdWaves * 64, RB < 4 || (RB == 4 && kGrad) ? 
     const int lane = threadIdx.x & 63, i = lane & 15, q = lane >> 4;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     u32x4* own = lds + wave * kUnits;
-    // Consecutive tiles, which mostly share an adapter, on one XCD.
-    const uint32_t items = (uint32_t)(kSmall ? P.tile_bound : *P.n_tiles) * P.slabs, per = (items + 7) / 8;
-    const uint32_t item = (blockIdx.x & 7) * per + (blockIdx.x >> 3);
-    if ((blockIdx.x >> 3) >= per || item >= items) return;
-    const int32_t slab = item % P.slabs;
+    // Whole tiles in multiples of the CUs; the rest are shared out by columns
+    // between all CUs (each share repeats the first product).  One tile too many
+    // would otherwise be worked on by one CU, at less than half of its speed beside
+    // another, long after the others are done: the gradients' 257 tiles of rank 64
+    // and 4096 columns 65 us, shared out 50, and 256 tiles 45.  Consecutive tiles,
+    // which mostly share an adapter, on one XCD.
+    const uint32_t n_all = kSmall ? P.tile_bound : *P.n_tiles, n_whole = kSmall ? 0 : n_all / kCus * kCus;
+    const uint32_t slabs = blockIdx.x < n_whole ? 1 : kSmall ? P.slabs : max(1u, min((uint32_t)P.slabs, kCus / max(n_all - n_whole, 1u)));
+    const uint32_t first = blockIdx.x < n_whole ? 0 : n_whole, items = blockIdx.x < n_whole ? n_whole : (n_all - n_whole) * slabs;
+    const uint32_t per = (items + 7) / 8, block = blockIdx.x - first, item = (block & 7) * per + (block >> 3);
+    if ((block >> 3) >= per || item >= items) return;
+    const int32_t tile = first + item / slabs, slab = item % slabs;
     int4 t;
     __shared__ int32_t rows[16];
     if constexpr (kSmall) {
@@ -396,7 +404,6 @@ __global__ void __launch_bounds__(kAdWaves * 64, RB < 4 || (RB == 4 && kGrad) ? 
             n_tiles += __popcll(leaders[w]);
             number += w < wave ? __popcll(leaders[w]) : 0;
         }
-        const int tile = item / P.slabs;
         if (tile >= n_tiles) return;
         if (leads && number == tile) lead = make_int4(bin, rank, total, 0);
         __syncthreads();
@@ -406,7 +413,7 @@ __global__ void __launch_bounds__(kAdWaves * 64, RB < 4 || (RB == 4 && kGrad) ? 
         if (live && bin == lead.x && rank >= rank0 && rank < rank0 + 16) rows[rank - rank0] = r;
         __syncthreads();
     } else {
-        t = P.tiles[item / P.slabs];
+        t = P.tiles[tile];
     }
     const int a = t.x, count = t.z;
     // Rows past `count` repeat the last one: its values, stored again.
@@ -418,7 +425,7 @@ __global__ void __launch_bounds__(kAdWaves * 64, RB < 4 || (RB == 4 && kGrad) ? 
         // Rows without an adapter, one a wavefront, eight loads in flight (one: 32
         // rows of 4096 columns take 19 us, as long as a tile with an adapter).
         constexpr int kLoads = 8;
-        const int pieces = P.N / 8, c0 = (int)((int64_t)pieces * slab / P.slabs), c1 = (int)((int64_t)pieces * (slab + 1) / P.slabs);
+        const int pieces = P.N / 8, c0 = (int)((int64_t)pieces * slab / slabs), c1 = (int)((int64_t)pieces * (slab + 1) / slabs);
         for (int m = wave; m < count; m += kAdWaves) {
             const int64_t r = row_of(m);
             uint16_t* to = P.out + r * P.ld_out;
@@ -577,7 +584,7 @@ __global__ void __launch_bounds__(kAdWaves * 64, RB < 4 || (RB == 4 && kGrad) ? 
         for (int k = 0; k < kBLoads; k++) bf[k] = load16(B + (int64_t)n0 * P.R + min(64 * k + lane, units - 1) * 8);
         issue();
     };
-    const int steps2 = (P.N + kCols - 1) / kCols, share = slab * kAdWaves + wave, shares = P.slabs * kAdWaves;
+    const int steps2 = (P.N + kCols - 1) / kCols, share = slab * kAdWaves + wave, shares = slabs * kAdWaves;
     int n0 = (int)((int64_t)steps2 * share / shares) * kCols;
     const int n_end = min((int)((int64_t)steps2 * (share + 1) / shares) * kCols, P.N);
 
@@ -899,7 +906,7 @@ namespace {
 
 template <int RB, bool kBase>
 hipError_t adapter_start(const AdapterParams& P, int64_t tiles, hipStream_t s) {
-    const dim3 grid((unsigned)((tiles * P.slabs + 7) / 8 * 8)), block(kAdWaves * 64);
+    const dim3 grid((unsigned)((tiles + 7) / 8 * 8)), block(kAdWaves * 64);
     if (P.w_pack)
         hipLaunchKernelGGL((adapter_kernel<RB, kAdTile / 16, true, kBase, false>), grid, block, 0, s, P);
     else if (P.ids)
@@ -922,9 +929,15 @@ bool adapter_small(int64_t M) { return M <= kAdWaves * 64; }
 
 hipError_t launch_adapter(AdapterParams P, int64_t tiles, hipStream_t stream) {
     const int cols = 64 * kAdWaves;  // of a step
-    if (P.ids) tiles = P.tile_bound = (int32_t)std::min<int64_t>(P.M, P.n + 1 + P.M / 16);
-    // Few tiles: their columns are shared out, and each share repeats the first product.
-    P.slabs = (int32_t)std::max<int64_t>(1, std::min<int64_t>((P.N + cols - 1) / cols, 256 / tiles));
+    const int64_t most = (P.N + cols - 1) / cols;  // shares of a tile's columns
+    if (P.ids) {
+        P.tile_bound = (int32_t)std::min<int64_t>(P.M, P.n + 1 + P.M / 16);
+        P.slabs = (int32_t)std::max<int64_t>(1, std::min<int64_t>(most, kCus / P.tile_bound));
+        tiles = (int64_t)P.tile_bound * P.slabs;
+    } else {  // what the tiles, at most `tiles`, and the shares of the rest of them come to
+        P.slabs = (int32_t)most;
+        tiles = std::min<int64_t>(tiles * most, tiles + kCus);
+    }
     // Where the rows' tensors (of the gradient x too) fill the 256 MB of the
     // last-level cache, base, which is read once, stays out of it: 128 experts'
     // 335 MB forward 76 -> 60 us, their gradient 80 + 63 -> 74 + 55.  Below, it may be
