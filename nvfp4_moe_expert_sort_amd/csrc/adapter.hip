@@ -50,46 +50,25 @@ __device__ __forceinline__ u32x4 column8(const u32x4 (&z)[8], int c) {
     return f;
 }
 
-// Sums over the earlier entries of N arrays [n], in place; every thread of the
-// workgroup calls it.
-template <int N>
-struct Arrays {
-    int32_t* of[N];
-};
-template <int N>
-__device__ __forceinline__ void block_scan(Arrays<N> a, int n, int32_t (*lds)[3]) {
-    const int per = (n + kPlanThreads - 1) / kPlanThreads, lo = min((int)threadIdx.x * per, n), hi = min(lo + per, n);
-    int32_t sum[N], incl[N];
+// Sums over the earlier entries of an array [n], in place, by one wavefront.
+// (All 16 of the workgroup would take a share of the SIMDs each to do as little:
+// 1.0 us a scan of 9 entries.)
+__device__ __forceinline__ void wave_scan(int32_t* of, int n) {
+    const int lane = threadIdx.x & 63, per = (n + 63) / 64, lo = min(lane * per, n), hi = min(lo + per, n);
+    int32_t sum = 0;
+    for (int i = lo; i < hi; i++) sum += of[i];
+    int32_t run = sum;
 #pragma unroll
-    for (int k = 0; k < N; k++) {
-        sum[k] = 0;
-        for (int i = lo; i < hi; i++) sum[k] += a.of[k][i];
-        incl[k] = sum[k];
+    for (int o = 1; o < 64; o <<= 1) {
+        const int32_t v = __shfl_up(run, o, kWave);
+        if (lane >= o) run += v;
     }
-#pragma unroll
-    for (int o = 1; o < 64; o <<= 1)
-#pragma unroll
-        for (int k = 0; k < N; k++) {
-            const int32_t v = __shfl_up(incl[k], o, kWave);
-            if ((int)(threadIdx.x & 63) >= o) incl[k] += v;
-        }
-    __syncthreads();
-    if ((threadIdx.x & 63) == 63)
-#pragma unroll
-        for (int k = 0; k < N; k++) lds[threadIdx.x >> 6][k] = incl[k];
-    __syncthreads();
-#pragma unroll
-    for (int k = 0; k < N; k++) {
-        int32_t run = incl[k] - sum[k];
-#pragma unroll
-        for (int w = 0; w < kPlanThreads / 64; w++) run += w < (int)(threadIdx.x >> 6) ? lds[w][k] : 0;
-        for (int i = lo; i < hi; i++) {
-            const int32_t v = a.of[k][i];
-            a.of[k][i] = run;
-            run += v;
-        }
+    run -= sum;
+    for (int i = lo; i < hi; i++) {
+        const int32_t v = of[i];
+        of[i] = run;
+        run += v;
     }
-    __syncthreads();
 }
 
 // The bin whose range of a table holds entry i: start[0..n) does not decrease.
@@ -104,26 +83,23 @@ __device__ __forceinline__ int find_bin(const int32_t* start, int n, int32_t i) 
 
 __device__ __forceinline__ int bin_of(const AdapterPlan& P, int32_t id) { return id >= 0 && id < P.n ? id : P.n; }
 
-// Counts the bins of the lanes' four consecutive rows in LDS, of which the
-// first `live` exist.  Neighbouring rows mostly share an adapter, and additions
-// of many lanes to one address take one turn each.
+// Counts of the bins, in copies of which a lane uses one: neighbouring rows
+// mostly share an adapter, and additions of many lanes to one address take one
+// turn each.  (One copy, and lanes that find the others of their adapter by
+// ballots: 1.1 us for 4096 rows, and so 0.4.)
+constexpr int kCopies = 8, kCopyPitch = kBins + 8;
+// The lane's four consecutive rows, of which the first `live` exist.
 __device__ __forceinline__ void count4(int32_t* hist, const AdapterPlan& P, int4 id, int64_t live) {
     if (live <= 0) return;
-    const int b0 = bin_of(P, id.x), b1 = bin_of(P, id.y), b2 = bin_of(P, id.z), b3 = bin_of(P, id.w);
-    const bool same = live >= 4 && b0 == b1 && b0 == b2 && b0 == b3;
-    // Lanes whose four rows share an adapter: one addition for all lanes of it.
-    bool left = same;
-    while (const uint64_t m = __ballot(left)) {
-        const int first = __builtin_ctzll(m), bin = __builtin_amdgcn_readlane(b0, first);
-        const uint64_t run = __ballot(left && b0 == bin);
-        if ((int)(threadIdx.x & 63) == first) atomicAdd(&hist[bin], 4 * __popcll(run));
-        left = left && b0 != bin;
+    hist += (threadIdx.x & (kCopies - 1)) * kCopyPitch;
+    if (live >= 4 && id.x == id.y && id.x == id.z && id.x == id.w) {
+        atomicAdd(&hist[bin_of(P, id.x)], 4);
+        return;
     }
-    if (same) return;
-    atomicAdd(&hist[b0], 1);
-    if (live > 1) atomicAdd(&hist[b1], 1);
-    if (live > 2) atomicAdd(&hist[b2], 1);
-    if (live > 3) atomicAdd(&hist[b3], 1);
+    atomicAdd(&hist[bin_of(P, id.x)], 1);
+    if (live > 1) atomicAdd(&hist[bin_of(P, id.y)], 1);
+    if (live > 2) atomicAdd(&hist[bin_of(P, id.z)], 1);
+    if (live > 3) atomicAdd(&hist[bin_of(P, id.w)], 1);
 }
 
 // B^T and A^T, which take the places of A and B in the gradient's products, of
@@ -186,7 +162,8 @@ __device__ __forceinline__ void pack_adapters(const AdapterPack& P, int64_t item
 // plan to say which of them have rows.
 __global__ void __launch_bounds__(kPlanThreads) adapter_plan_kernel(AdapterPlan P, AdapterPack pack) {
     constexpr int kWaves = kPlanThreads / 64, kAhead = 8;
-    __shared__ int32_t total[kBins + 1], start[kBins + 1], before[kBins], scan[kWaves][3];
+    __shared__ int32_t total[kBins], start[kBins], before[kBins];
+    __shared__ int32_t hist[2][kCopies * kCopyPitch];  // of the rows ahead of this workgroup's, and of the others
     __shared__ uint16_t counts[kWaves][kBins];
     __shared__ int32_t tile0[kBins], chunk0[kBins], slot0[kBins];  // (a tile is a step of the gradients)
     const int bins = P.n + 1, wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
@@ -196,8 +173,9 @@ __global__ void __launch_bounds__(kPlanThreads) adapter_plan_kernel(AdapterPlan 
     }
     const bool tables = (int)blockIdx.x == P.blocks - 1;
     const int64_t first = tables ? 0 : (int64_t)blockIdx.x * P.rows;  // a multiple of 256: a wavefront's rows lie on one side
-    for (int i = threadIdx.x; i <= bins; i += kPlanThreads) total[i] = 0;
-    for (int i = threadIdx.x; i < bins; i += kPlanThreads) before[i] = 0;
+    for (int i = threadIdx.x; i < bins; i += kPlanThreads)
+#pragma unroll
+        for (int c = 0; c < 2 * kCopies; c++) hist[c / kCopies][c % kCopies * kCopyPitch + i] = 0;
     __syncthreads();
     // Four rows a thread.  kAhead such pieces of 4096 rows are loaded before any
     // is counted, and the last piece (which may be a part) before all.
@@ -220,16 +198,20 @@ __global__ void __launch_bounds__(kPlanThreads) adapter_plan_kernel(AdapterPlan 
         issue();
 #pragma unroll
         for (int k = 0; k < kAhead; k++)
-            if (p0 + k < last) count4(4 * ((p0 + k) * kPlanThreads + threadIdx.x) < first ? before : total, P, id[k], 4);
+            if (p0 + k < last) count4(hist[4 * ((p0 + k) * kPlanThreads + threadIdx.x) >= first], P, id[k], 4);
     }
-    count4(r_last < first ? before : total, P, id_last, P.M - r_last);
+    count4(hist[r_last >= first], P, id_last, P.M - r_last);
     __syncthreads();
-    for (int i = threadIdx.x; i <= bins; i += kPlanThreads) {
-        if (i < bins) total[i] += before[i];
-        start[i] = total[i];
+    for (int i = threadIdx.x; i < bins; i += kPlanThreads) {
+        int32_t n[2] = {0, 0};
+#pragma unroll
+        for (int c = 0; c < 2 * kCopies; c++) n[c / kCopies] += hist[c / kCopies][c % kCopies * kCopyPitch + i];
+        before[i] = n[0];
+        total[i] = start[i] = n[0] + n[1];
     }
     __syncthreads();
-    block_scan<1>({start}, bins + 1, scan);
+    if (wave == 0) wave_scan(start, bins);
+    __syncthreads();
     if (!tables) {
         // 1024 rows at a time, one a thread.  Lanes of one bin find each other
         // by a ballot for each bit of it; a row's place is the bin's next one,
@@ -279,10 +261,11 @@ __global__ void __launch_bounds__(kPlanThreads) adapter_plan_kernel(AdapterPlan 
     __syncthreads();
     const int32_t last_tiles = tile0[bins - 1];  // (the rows without an adapter have no chunks)
     __syncthreads();
-    if (P.chunk)
-        block_scan<3>({tile0, chunk0, slot0}, bins, scan);
-    else
-        block_scan<1>({tile0}, bins, scan);
+    if (wave == 0)
+        wave_scan(tile0, bins);
+    else if (P.chunk && wave < 3)
+        wave_scan(wave == 1 ? chunk0 : slot0, bins);
+    __syncthreads();
     const int32_t n_tiles = tile0[bins - 1] + last_tiles, n_chunks = P.chunk ? chunk0[bins - 1] : 0;
     if (threadIdx.x == 0) {
         P.n_tables[0] = n_tiles;
@@ -896,10 +879,11 @@ hipError_t launch_adapter_plan(AdapterPlan P, const AdapterPack* pack, hipStream
 }
 
 // Rows of a forward tile.  Up to rank 16 always 16 rows, of which a CU holds two
-// tiles.  Above, 16 rows take a tile less time as long as every CU has one at
-// most (4096 rows of 4096 columns: rank 64 29 against 33 us, rank 128 40 against
-// 46), and 32 read the adapters half as often (65536 rows: rank 32 365 against
-// 344 us, rank 64 500 against 377, rank 128 705 against 484).
+// tiles.  Above, 16 rows are ahead by some where each CU has one tile at most
+// (600 rows of 4096 columns: rank 64 17.8 against 19.6 us, rank 128 24.6 against
+// 27.2; 4000 rows 28.8 against 29.4 and 39.4 against 38.2), and 32 read the adapters
+// half as often (16384 rows: rank 32 89 against 75 us, rank 64 129 against 95,
+// rank 128 173 against 120).
 int adapter_tile(int32_t R, int64_t M, int64_t n) { return R <= 16 || M / 16 + n + 1 <= 256 ? 16 : 32; }
 
 namespace {
