@@ -160,6 +160,8 @@ __device__ __forceinline__ void pack_adapters(const AdapterPack& P, int64_t item
 // of ids in flight at once), which saves a launch that only counts.
 // Workgroups behind those transpose the adapters, if that need not wait for the
 // plan to say which of them have rows.
+// 5.6 us for 8192 rows, 9.1 for 32768 of 128 adapters: the launch, the chain from
+// the ids to the last table, and what 16 wavefronts a CU take to issue it.
 __global__ void __launch_bounds__(kPlanThreads) adapter_plan_kernel(AdapterPlan P, AdapterPack pack) {
     constexpr int kWaves = kPlanThreads / 64, kAhead = 8;
     __shared__ int32_t total[kBins], start[kBins], before[kBins];
@@ -311,8 +313,16 @@ __global__ void __launch_bounds__(kPlanThreads) adapter_plan_kernel(AdapterPlan 
 // The gradient's A and B, which are copies anyway, come from rank 33 on as the
 // products' operands (adapter_pack_kernel) and need not be turned over: 69
 // against 92 us at 8192 rows, rank 64 and 4096 columns; at rank 16, where the
-// second product's would be twice as long, 88 against 79 us for 128 experts.  (A
-// forward pass that packs first gains less than the packing takes.)
+// second product's would be twice as long, 88 against 79 us for 128 experts (both
+// before the last tiles were shared out).  (A forward pass that packs first gains
+// less than the packing takes.)
+//
+// Bound by memory: 8192 rows, rank 16, 4096 columns, 201 MB 34 us where a part is
+// in the last-level cache, 48 from memory (4.2 TB/s); 128 experts' 335 MB 59 us
+// (5.7 TB/s); rank 64 gradients, 201 MB and 6 of operands, 45 us in 256 tiles.
+// At high ranks by the adapters too, which every tile reads through L2 (rank 128:
+// 2 MB for 0.8 of rows).  Few tiles are a chain: two products of 8 steps a
+// wavefront, 1 to 1.5 us each (rank 64, 130 tiles: 25 us).
 template <int RB, int MB, bool kGrad, bool kBase, bool kSmall>
 __global__ void __launch_bounds__(kAdWaves * 64, RB < 4 || (RB == 4 && kGrad) ? 4 : 2) adapter_kernel(AdapterParams P) {
     constexpr bool kPacked = kGrad && RB >= 4;
@@ -734,7 +744,11 @@ __global__ void __launch_bounds__(256) adapter_pack_kernel(AdapterPack P) {
 // RB: ranks in blocks of 16 (blockIdx.z takes further ones).  The NW wavefronts
 // take steps in turn and join their sums in LDS.  (Wavefronts that take 128
 // columns each and all steps have nothing to join, but uneven experts then leave
-// CUs idle: 71 against 63 us for 128 of them.)
+// CUs idle: 8 us more of 63 for 128 of them.)
+// 8192 rows, rank 64, 4096 columns: 47 us for 128 MB of rows and 39 GFLOP in
+// pieces, the matrix pipe busy for a quarter; 128 experts, 235 MB, 55 us (4.3
+// TB/s).  Bound by the latency of the rows' loads, which the registers of the
+// sums leave few of in flight, and uneven chunks.
 template <int RB, int NW>
 __global__ void __launch_bounds__(NW * 64, RB < 2 ? 4 : 2) adapter_wgrad_kernel(AdapterGrad P) {
     constexpr int kAhead = RB < 2 ? RB : 2;  // rank blocks whose w is in registers
@@ -924,8 +938,8 @@ hipError_t launch_adapter(AdapterParams P, int64_t tiles, hipStream_t stream) {
     }
     // Where the rows' tensors (of the gradient x too) fill the 256 MB of the
     // last-level cache, base, which is read once, stays out of it: 128 experts'
-    // 335 MB forward 76 -> 60 us, their gradient 80 + 63 -> 74 + 55.  Below, it may be
-    // there already: 201 MB 37 us, and 46 past the cache.
+    // 335 MB forward 73 -> 58 us, their gradient 73 + 63 -> 69 + 55.  Below, it may be
+    // there already: 201 MB 33 us, and 40 past the cache.
     P.stream = 2 * P.M * ((P.w_pack ? 2 : 1) * (int64_t)P.K + 2 * P.N) >= ((int64_t)1 << 28);
     switch (adapter_rank_blocks(P.R)) {
         case 1: return adapter_run<1>(P, tiles, stream);
@@ -937,11 +951,16 @@ hipError_t launch_adapter(AdapterParams P, int64_t tiles, hipStream_t stream) {
 
 // Rows of a chunk of the weights' gradients, how a workgroup takes them
 // (adapter_wgrad_kernel), and whether an adapter may have several.
-AdapterSplit adapter_split(int64_t M, int32_t R, int64_t K, int64_t N) {
+AdapterSplit adapter_split(int64_t M, int32_t R, int64_t K, int64_t N, int64_t n) {
     const int64_t slabs = (K + 127) / 128 + (N + 127) / 128;
     AdapterSplit s{};
-    if (R <= 16 && M <= 1024) {  // one chunk, and its steps one or two a wavefront: no sums to join
-        s.waves16 = true;
+    s.waves = 4;
+    if (R <= 16 && M <= 1024) {
+        // One chunk an adapter, without sums to join.  By 16 wavefronts, a step or two
+        // each, while every CU has a workgroup at most: 1021 rows of one adapter, 2048 x
+        // 4096, 7.1 us a launch and by 4 wavefronts 9.2; of 8 adapters 7.1 and 4.7, of 64
+        // 32 and 12.
+        if (n * slabs <= (int64_t)kCus) s.waves = 16;
         s.chunk = 1024;
         s.most = (int32_t)(M / 1024);
     } else {  // the columns' slabs times the chunks are the workgroups that the CUs hold at a time
@@ -955,7 +974,7 @@ AdapterSplit adapter_split(int64_t M, int32_t R, int64_t K, int64_t N) {
 
 hipError_t launch_adapter_wgrad(const AdapterGrad& P, const AdapterSplit& split, int64_t chunks, hipStream_t stream) {
     const dim3 grid((P.K + 127) / 128 + (P.N + 127) / 128, (unsigned)chunks, P.R > 64 ? 2 : 1);
-    if (split.waves16)
+    if (split.waves == 16)
         hipLaunchKernelGGL((adapter_wgrad_kernel<1, 16>), grid, dim3(1024), 0, stream, P);
     else if (P.R <= 16)
         hipLaunchKernelGGL((adapter_wgrad_kernel<1, 4>), grid, dim3(256), 0, stream, P);

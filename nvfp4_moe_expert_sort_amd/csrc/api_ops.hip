@@ -255,7 +255,7 @@ AdapterWork adapter_work(const nvfp4moe_adapters* ad, int64_t M, bool backward) 
     w.first = w.info + up(n * 8, kAlign);
     w.second = w.first + up(n * adapter_units(N, ad->rank) * 16, kAlign);
     w.total = w.second + up(n * adapter_units(K, ad->rank) * 16, kAlign);
-    w.split = adapter_split(M, ad->rank, K, N);
+    w.split = adapter_split(M, ad->rank, K, N, n);
     w.n_chunks = w.split.most + n;
     w.chunks = w.total;
     w.steps = w.chunks + up(w.n_chunks * 16, kAlign);
@@ -264,7 +264,7 @@ AdapterWork adapter_work(const nvfp4moe_adapters* ad, int64_t M, bool backward) 
     w.slots = 2 * w.w_pack - w.v_pack;
     // chunks of adapters that have more than one: at most floor(rows / chunk) + 1
     // each, which is at most twice the first term
-    w.total = w.slots + (w.split.waves16 ? 0 : up(2 * w.split.most * R * (K + N) * 4, kAlign));
+    w.total = w.slots + (w.split.join ? up(2 * w.split.most * R * (K + N) * 4, kAlign) : 0);
     return w;
 }
 int adapter_rows(const uint16_t* p, int64_t ld, int64_t cols) {

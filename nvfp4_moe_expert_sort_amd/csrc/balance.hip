@@ -125,10 +125,14 @@ __device__ __forceinline__ void load_row(const L* row, const BalanceParams& P, i
 // sequence (a lane its own experts over its tokens, then the wavefront's token
 // slots by exchanges, then the wavefronts in LDS), like the counts: a workgroup
 // whose rows belong to several, which the kernel's end waits for, repeats only
-// the sums (once the whole pass, 16384 rows in 13 sequences: LOSS_OLD against LOSS_NEW us).
+// the sums (16384 rows of 256 experts in 13 sequences 13.5 us; with the whole pass
+// repeated 18).
 // Chunk b's part of sequence s goes to slot b + s: a walk along the rows raises
 // b or s at every step, so no two parts share one.  A call of one chunk has its
 // sequences whole here and needs no join.
+// 16384 rows of 256 experts: 11 us for 17 MB (3.3 us at the rate of a large
+// copy).  3 of it is the launch, 2 the exponentials; the rest is one chain from
+// the loads to the sums in LDS, a pass a workgroup.
 template <int LT, int NV, typename L>
 __global__ void __launch_bounds__(kChunkThreads) balance_chunk_kernel(BalanceParams P) {
     constexpr int kTok = kChunkThreads / LT, kWaves = kChunkThreads / 64;
@@ -330,6 +334,9 @@ __global__ void __launch_bounds__(kJoinThreads) balance_join_kernel(BalanceParam
 // where D, G and the difference are FP64: for a token whose top expert has
 // nearly all the probability, n_e - sum n p is small against its terms, and
 // here only the relative errors of the w remain (some 2^-23 each).
+// 32749 rows of 128 experts in BF16: 11.5 us for 17 MB, of which the exponentials
+// and FP64 sums issue for some 5; then the chain from a sequence's offsets to its
+// counts.
 template <int LT, int NV, typename L>
 __global__ void __launch_bounds__(kBalThreads) balance_backward_kernel(BalanceParams P) {
     constexpr int kTok = kBalThreads / LT;

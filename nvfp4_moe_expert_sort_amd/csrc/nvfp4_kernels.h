@@ -241,9 +241,10 @@ struct AdapterGrad {
 struct AdapterSplit {
     int32_t chunk;
     int32_t most;  // at least M / chunk, and not falling as M grows
-    bool waves16, join;
+    int32_t waves;  // of a workgroup
+    bool join;      // an adapter may have several chunks
 };
-AdapterSplit adapter_split(int64_t M, int32_t R, int64_t K, int64_t N);
+AdapterSplit adapter_split(int64_t M, int32_t R, int64_t K, int64_t N, int64_t n);
 hipError_t launch_adapter_wgrad(const AdapterGrad& P, const AdapterSplit& split, int64_t chunks_bound, hipStream_t stream);
 
 // MXFP4 quantizers (mxfp4_quant.hip) and products (mxfp4_gemm.hip).
