@@ -745,7 +745,7 @@ __global__ void __launch_bounds__(256) adapter_pack_kernel(AdapterPack P) {
 // take steps in turn and join their sums in LDS.  (Wavefronts that take 128
 // columns each and all steps have nothing to join, but uneven experts then leave
 // CUs idle: 8 us more of 63 for 128 of them.)
-// 8192 rows, rank 64, 4096 columns: 47 us for 128 MB of rows and 39 GFLOP in
+// 8192 rows, rank 64, 4096 columns: 47 us for 128 MB of rows and 26 GFLOP in
 // pieces, the matrix pipe busy for a quarter; 128 experts, 235 MB, 55 us (4.3
 // TB/s).  Bound by the latency of the rows' loads, which the registers of the
 // sums leave few of in flight, and uneven chunks.
