@@ -449,3 +449,26 @@ def test_two_calls_at_once(gpu):
         for k, o in outs:
             for a, b in zip(o if isinstance(o, tuple) else (o,), want[k] if isinstance(want[k], tuple) else (want[k],)):
                 assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("rank,n,order", [(8, 1, "runs"), (16, 3, "mixed"), (32, 5, "runs"), (64, 3, "mixed"), (64, 200, "mixed"), (128, 2, "runs")])
+def test_rows_do_not_depend_on_large_batches(gpu, rank, n, order):
+    """Rows of batches that take tiles of either height, whole or shared out by columns, to the bit what they are alone;
+    ids that start at any address."""
+    import torch
+    m, dev = gpu
+    M, K, N = 9001, 328, 1544
+    g = torch.Generator(device=dev).manual_seed(rank + n)
+    x, base, A, B = _randn(g, M, K), _randn(g, M, N), _randn(g, n, rank, K, std=0.05), _randn(g, n, N, rank, std=0.1)
+    ids = torch.empty(M + 1, dtype=torch.int32, device=dev)[1:]
+    ids.copy_(torch.randint(-1, n, (M,), generator=g, device=dev))
+    if order == "runs":
+        ids.copy_(ids.sort()[0])
+    whole, v = torch.empty_like(base), torch.empty(M, rank, device=dev)
+    m.adapter_linear(x, ids, A, B, base, v=v, out=whole)
+    for rows in (torch.arange(0, 3), torch.arange(M - 300, M), torch.arange(0, 4200), torch.arange(0, M, 2), torch.arange(1000, 1600),
+                 torch.randperm(M, generator=torch.Generator().manual_seed(1))[:8200]):
+        i = rows.to(dev)
+        vp = torch.empty(len(rows), rank, device=dev)
+        part = m.adapter_linear(x[i], ids[i], A, B, base[i], v=vp)
+        assert torch.equal(part, whole[i]) and torch.equal(vp, v[i])
