@@ -349,8 +349,11 @@ __global__ void __launch_bounds__(kAdWaves * 64, RB < 4 || (RB == 4 && kGrad) ? 
     // and 4096 columns 65 us, shared out 50, and 256 tiles 45.  Consecutive tiles,
     // which mostly share an adapter, on one XCD.
     const uint32_t n_all = kSmall ? P.tile_bound : *P.n_tiles, n_whole = kSmall ? 0 : n_all / kCus * kCus;
-    const uint32_t slabs = blockIdx.x < n_whole ? 1 : kSmall ? P.slabs : max(1u, min((uint32_t)P.slabs, kCus / max(n_all - n_whole, 1u)));
-    const uint32_t first = blockIdx.x < n_whole ? 0 : n_whole, items = blockIdx.x < n_whole ? n_whole : (n_all - n_whole) * slabs;
+    const bool is_whole = blockIdx.x < n_whole;
+    const uint32_t first = is_whole ? 0 : n_whole, tiles = is_whole ? n_whole : n_all - n_whole;
+    uint32_t slabs = is_whole ? 1 : P.slabs;
+    if (!kSmall && !is_whole) slabs = max(1u, min(slabs, kCus / max(tiles, 1u)));
+    const uint32_t items = tiles * slabs;
     const uint32_t per = (items + 7) / 8, block = blockIdx.x - first, item = (block & 7) * per + (block >> 3);
     if ((block >> 3) >= per || item >= items) return;
     const int32_t tile = first + item / slabs, slab = item % slabs;
@@ -425,7 +428,10 @@ __global__ void __launch_bounds__(kAdWaves * 64, RB < 4 || (RB == 4 && kGrad) ? 
             for (int c = c0 + lane; c < c1; c += 64 * kLoads) {
                 u32x4 z[kLoads];
 #pragma unroll
-                for (int j = 0; j < kLoads; j++) z[j] = kBase ? load16(P.base + r * P.ld_base + 8 * min(c + 64 * j, c1 - 1)) : u32x4{0, 0, 0, 0};
+                for (int j = 0; j < kLoads; j++) {
+                    z[j] = u32x4{0, 0, 0, 0};
+                    if (kBase) z[j] = load16(P.base + r * P.ld_base + 8 * min(c + 64 * j, c1 - 1));
+                }
                 issue();
 #pragma unroll
                 for (int j = 0; j < kLoads; j++)

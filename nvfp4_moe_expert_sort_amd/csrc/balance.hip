@@ -176,12 +176,14 @@ __global__ void __launch_bounds__(kChunkThreads) balance_chunk_kernel(BalancePar
             float sum2[2 * kLeft], sum4[kLeft];
 #pragma unroll
             for (int i = 0; i < 2 * kLeft; i++) {
-                const auto v = __builtin_amdgcn_permlane32_swap(__float_as_uint(acc[i]), __float_as_uint(acc[i + 2 * kLeft]), false, false);
+                const auto v = __builtin_amdgcn_permlane32_swap(__float_as_uint(acc[i]), __float_as_uint(acc[i + 2 * kLeft]),
+                                                                false, false);
                 sum2[i] = __uint_as_float(v[0]) + __uint_as_float(v[1]);
             }
 #pragma unroll
             for (int i = 0; i < kLeft; i++) {
-                const auto v = __builtin_amdgcn_permlane16_swap(__float_as_uint(sum2[i]), __float_as_uint(sum2[i + kLeft]), false, false);
+                const auto v = __builtin_amdgcn_permlane16_swap(__float_as_uint(sum2[i]), __float_as_uint(sum2[i + kLeft]),
+                                                                false, false);
                 sum4[i] = __uint_as_float(v[0]) + __uint_as_float(v[1]);
             }
             const int first_acc = (threadIdx.x & 63) / 16 * kLeft;
@@ -191,7 +193,8 @@ __global__ void __launch_bounds__(kChunkThreads) balance_chunk_kernel(BalancePar
         } else {
 #pragma unroll
             for (int i = 0; i < NV / 4; i++)
-                *reinterpret_cast<float4*>(&part[wave][(i * LT + lane) * 4]) = float4{acc[4 * i], acc[4 * i + 1], acc[4 * i + 2], acc[4 * i + 3]};
+                *reinterpret_cast<float4*>(&part[wave][(i * LT + lane) * 4]) =
+                    float4{acc[4 * i], acc[4 * i + 1], acc[4 * i + 2], acc[4 * i + 3]};
         }
 #pragma unroll
         for (int i = 0; i < NV; i++) acc[i] = 0.0f;
@@ -318,7 +321,8 @@ __global__ void __launch_bounds__(kJoinThreads) balance_join_kernel(BalanceParam
     __syncthreads();
     if (!last) return;
     double total = 0.0;
-    for (uint32_t i = threadIdx.x; i < gridDim.x; i += kJoinThreads) total += __hip_atomic_load(&P.part[i], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    for (uint32_t i = threadIdx.x; i < gridDim.x; i += kJoinThreads)
+        total += __hip_atomic_load(&P.part[i], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
     total = wave_sum(total);
     if (col == 0) sums[0][stripe] = total;
     __syncthreads();

@@ -1,5 +1,5 @@
-"""Expert selection, the balance loss, MXFP4 products, low-rank adapters and gradient clipping: the binding of these entry points (``include/nvfp4moe.h``
-documents each) for PyTorch tensors.
+"""Expert selection, the balance loss, MXFP4 products, low-rank adapters and gradient clipping: the binding of these
+entry points (``include/nvfp4moe.h`` documents each) for PyTorch tensors.
 
 At decode sizes a call takes a few microseconds on the GPU, so the binding's own time counts: arguments are checked
 once, pointers and the raw stream go to ctypes as integers, and the device and stream are switched only where they are
@@ -12,8 +12,8 @@ import functools
 
 import torch
 
-from . import (BALANCE_ONE_LAUNCH, BF16, F32, GROUP_MAX, LAYOUT_GEMM, LAYOUT_LOGICAL, MXFP4_SCALE_FLOOR, SCORE_SOFTMAX, Adapters, BalanceConfig,
-               Grad, Mxfp4Tensor, Nvfp4Error, SelectConfig, _check, lib)
+from . import (BALANCE_ONE_LAUNCH, BF16, F32, GROUP_MAX, LAYOUT_GEMM, LAYOUT_LOGICAL, MXFP4_SCALE_FLOOR, SCORE_SOFTMAX,
+               Adapters, BalanceConfig, Grad, Mxfp4Tensor, Nvfp4Error, SelectConfig, _check, lib)
 
 _BF16 = (torch.bfloat16, torch.int16, torch.uint16)  # storage of BF16 bits
 _TYPES = {torch.float32: F32, torch.bfloat16: BF16}
