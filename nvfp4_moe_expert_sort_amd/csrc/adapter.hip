@@ -52,7 +52,7 @@ __device__ __forceinline__ u32x4 column8(const u32x4 (&z)[8], int c) {
 
 // Sums over the earlier entries of an array [n], in place, by one wavefront.
 // (All 16 of the workgroup would take a share of the SIMDs each to do as little:
-// 1.0 us a scan of 9 entries.)
+// 1.0 us a scan of 9 entries, and so 0.6.)
 __device__ __forceinline__ void wave_scan(int32_t* of, int n) {
     const int lane = threadIdx.x & 63, per = (n + 63) / 64, lo = min(lane * per, n), hi = min(lo + per, n);
     int32_t sum = 0;
@@ -86,7 +86,7 @@ __device__ __forceinline__ int bin_of(const AdapterPlan& P, int32_t id) { return
 // Counts of the bins, in copies of which a lane uses one: neighbouring rows
 // mostly share an adapter, and additions of many lanes to one address take one
 // turn each.  (One copy, and lanes that find the others of their adapter by
-// ballots: 1.1 us for 4096 rows, and so 0.4.)
+// ballots: 32768 rows sorted by adapter counted after 6.0 us, and so after 3.5.)
 constexpr int kCopies = 8, kCopyPitch = kBins + 8;
 // The lane's four consecutive rows, of which the first `live` exist.
 __device__ __forceinline__ void count4(int32_t* hist, const AdapterPlan& P, int4 id, int64_t live) {
