@@ -474,8 +474,13 @@ typedef struct {
     float coef;          /* finite */
 } nvfp4moe_balance_config;
 
-/* Up to this many rows the loss takes one launch, and its workspace may be NULL. */
-enum { NVFP4MOE_BALANCE_ONE_LAUNCH = 256 };
+/* Up to this many rows, logits and sequences the loss takes one launch, and its
+ * workspace may be NULL. */
+enum {
+    NVFP4MOE_BALANCE_ONE_LAUNCH = 256,
+    NVFP4MOE_BALANCE_ONE_LAUNCH_LOGITS = 32768,
+    NVFP4MOE_BALANCE_ONE_LAUNCH_SEQUENCES = 4
+};
 
 /* logits [T, E] (rows ld elements apart), ids [T, K] int32 -> loss (device
  * float), counts [S, E] int32, every element written.  The probabilities are

@@ -30,7 +30,7 @@ GROUP_MAX = 0
 GROUP_TOP2 = 1
 MXFP4_SCALE_FLOOR = 0
 MXFP4_SCALE_RU = 1
-BALANCE_ONE_LAUNCH = 256  # rows up to which the balance loss needs no workspace
+BALANCE_ONE_LAUNCH, BALANCE_ONE_LAUNCH_LOGITS, BALANCE_ONE_LAUNCH_SEQUENCES = 256, 32768, 4  # a balance loss without a workspace
 
 # Every function the C header declares (checked against the header by the tests).
 EXPORTS = ["nvfp4_status_str", "nvfp4_quantize", "nvfp4moe_weight_bytes", "nvfp4moe_quantize_weights",

@@ -16,7 +16,9 @@ using namespace nvfp4;
 
 namespace {
 
-static_assert(kBalanceOneLaunch == NVFP4MOE_BALANCE_ONE_LAUNCH, "the header's constant");
+static_assert(kBalanceOneLaunch == NVFP4MOE_BALANCE_ONE_LAUNCH && kBalanceOneLogits == NVFP4MOE_BALANCE_ONE_LAUNCH_LOGITS &&
+                  kBalanceOneSequences == NVFP4MOE_BALANCE_ONE_LAUNCH_SEQUENCES,
+              "the header's constants");
 
 constexpr size_t kAlign = 256;
 size_t up(size_t v, size_t a) { return (v + a - 1) / a * a; }
@@ -89,8 +91,8 @@ struct BalanceWork {
 };
 bool balance_work(int64_t T, int64_t E, int64_t S, BalanceWork* w) {
     if (T < 0 || T >= ((int64_t)1 << 31) || E < 1 || E > kMaxExperts || S < 1 || S > kMaxSequences) return false;
-    // chunks of 64 rows up to 512 of them, then of more: the most that any smaller T has
-    const int64_t slots = std::max(std::min<int64_t>((T + 63) / 64, 512), (T + 255) / 256) + S;
+    // the most chunks that T rows or fewer have (balance_chunk)
+    const int64_t slots = std::max({std::min<int64_t>((T + 15) / 16, 512), (T + 255) / 256, std::min<int64_t>((T + 15) / 16, S / 2 + 1)}) + S;
     w->csum = up(slots * E * 4, kAlign);
     w->part = 2 * w->csum;
     w->done = w->part + up(S * ((E + 63) / 64) * 8, kAlign);
@@ -359,12 +361,12 @@ int nvfp4moe_router_balance_loss(const nvfp4moe_balance_config* cfg, const void*
     if (st != NVFP4_OK) return st;
     BalanceWork w;
     if (!balance_work(T, P.E, P.S, &w)) return NVFP4_E_SHAPE;
-    if (!loss || !counts || (T > kBalanceOneLaunch && !workspace) || (T > 0 && (!logits || !ids))) return NVFP4_E_NULL;
-    if (T > kBalanceOneLaunch && workspace_bytes < w.total) return NVFP4_E_WORKSPACE;
+    P.chunk = balance_chunk(T, P.E, P.S);
+    if (!loss || !counts || (T > P.chunk && !workspace) || (T > 0 && (!logits || !ids))) return NVFP4_E_NULL;
+    if (T > P.chunk && workspace_bytes < w.total) return NVFP4_E_WORKSPACE;
     if (!aligned(ids, 4) || !aligned(loss, 4) || !aligned(counts, 4) || !aligned(workspace, kAlign)) return NVFP4_E_ALIGN;
     uint8_t* ws = (uint8_t*)workspace;
     P.ids = ids;
-    P.chunk = balance_chunk(T);
     P.psum = (float*)ws;
     P.csum = (int32_t*)(ws + w.csum);
     P.part = (double*)(ws + w.part);

@@ -144,7 +144,7 @@ __global__ void __launch_bounds__(kChunkThreads) balance_chunk_kernel(BalancePar
     const int lane = threadIdx.x & (LT - 1), slot = threadIdx.x / LT, wave = threadIdx.x >> 6;
     const int64_t first = (int64_t)blockIdx.x * P.chunk, past = min(P.T, first + P.chunk);
     const bool whole = gridDim.x == 1;
-    double total = 0.0;  // whole: of loss / factor
+    double total = 0.0;  // whole: the thread's part of loss / factor
     int32_t s_next = 0;  // whole: the first sequence whose counts are not written
     if (!whole && blockIdx.x == 0 && threadIdx.x == 0) *P.done = 0;
     float l[NV], acc[NV];
@@ -163,7 +163,7 @@ __global__ void __launch_bounds__(kChunkThreads) balance_chunk_kernel(BalancePar
     for (int e = threadIdx.x; e < P.E; e += kChunkThreads) hist[e] = 0;
     // The sequence that the walk has come to, and its rows.
     int32_t s = max(find_sequence<kChunkThreads>(P, first, found), 0);
-    int64_t lo = seq_start(P, min(s, P.S)), hi = seq_start(P, min(s + 1, P.S));
+    int64_t lo = seq_start(P, min(s, P.S)), hi = seq_start(P, min(s + 1, P.S)), next = seq_start(P, min(s + 2, P.S));
     __syncthreads();
     // Writes the sums and counts of the sequence's rows in this chunk, and clears them.
     auto flush = [&] {
@@ -200,8 +200,8 @@ __global__ void __launch_bounds__(kChunkThreads) balance_chunk_kernel(BalancePar
         for (int i = 0; i < NV; i++) acc[i] = 0.0f;
         __syncthreads();
         const int64_t at = (whole ? s : (int64_t)blockIdx.x + s) * P.E;
-        double share = 0.0;
-        for (int e = threadIdx.x; e < P.E; e += kChunkThreads) {
+        static_assert(kMaxExperts <= kChunkThreads, "an expert a thread");
+        if (const int e = threadIdx.x; e < P.E) {
             float sum = 0.0f;
 #pragma unroll
             for (int k = 0; k < kWaves; k++) sum += part[k][e];
@@ -209,24 +209,17 @@ __global__ void __launch_bounds__(kChunkThreads) balance_chunk_kernel(BalancePar
             hist[e] = 0;
             if (whole) {
                 P.counts[at + e] = n;
-                share += (double)sum * (double)n;
+                total += (double)sum * (double)n / (double)(hi - lo);
             } else {
                 P.psum[at + e] = sum;
                 P.csum[at + e] = n;
             }
         }
         if (whole) {
-            share = wave_sum(share);
-            if ((threadIdx.x & 63) == 0) shares[wave] = share;
             for (int64_t i = (int64_t)s_next * P.E + threadIdx.x; i < (int64_t)s * P.E; i += kChunkThreads) P.counts[i] = 0;
             s_next = s + 1;
         }
         __syncthreads();
-        if (whole) {
-            share = 0.0;
-            for (int k = 0; k < kWaves; k++) share += shares[k];
-            total += share / (double)(hi - lo);
-        }
     };
     for (int64_t t0 = first; t0 < past; t0 += kTok) {
         if (t0 > first) load(t0);
@@ -252,12 +245,20 @@ __global__ void __launch_bounds__(kChunkThreads) balance_chunk_kernel(BalancePar
             if (hi > end || (hi == end && end == past)) break;
             s++;
             lo = hi;
-            hi = seq_start(P, min(s + 1, P.S));
+            hi = next;
+            next = seq_start(P, min(s + 2, P.S));  // (on its way until the sequence after this one)
         }
     }
     if (whole) {  // (sequences without rows have no counts)
         for (int64_t i = (int64_t)s_next * P.E + threadIdx.x; i < (int64_t)P.S * P.E; i += kChunkThreads) P.counts[i] = 0;
-        if (threadIdx.x == 0) *P.loss = balance_scaled(P, total);
+        total = wave_sum(total);
+        if ((threadIdx.x & 63) == 0) shares[wave] = total;
+        __syncthreads();
+        if (threadIdx.x == 0) {
+            total = 0.0;
+            for (int k = 0; k < kWaves; k++) total += shares[k];
+            *P.loss = balance_scaled(P, total);
+        }
     }
 }
 
@@ -454,14 +455,20 @@ hipError_t balance_type(const BalanceParams& P, hipStream_t s) {
 
 }  // namespace
 
-// Rows of a workgroup of the loss: up to 256 in one, whose single launch takes
-// less than a second one would; else 64 and, so that there are at most 512
-// workgroups, up to 256 (a lane then adds 4 tokens, or 16 in rows of more than
-// 256 experts, in FP32 before FP64 takes over).
-int32_t balance_chunk(int64_t T) {
-    if (T <= kBalanceOneLaunch) return kBalanceOneLaunch;
-    int32_t chunk = 64;
-    while (chunk < 256 && (T + chunk - 1) / chunk > 512) chunk *= 2;
+// Rows of a workgroup of the loss.  All of a few rows, whose single launch takes
+// less than a second one would (256 rows of 128 experts: 10.5 against 14.3 us, in 4
+// sequences 12.6 against 14.1, in 8 16.1 against 14.2; of 256 experts 14.2 against
+// 14.9).  Else one pass of its token slots and, so that there are at most 512
+// workgroups (of more than 256 experts 256, one a CU: 16384 rows of 1024 experts 24
+// against 31 us), up to 256 (a lane then adds 4 tokens, or 16 in rows of more than 256
+// experts, in FP32 before FP64 takes over); but fewer where the sequences are so
+// short that a workgroup would add up more than some 4 of them, 0.9 us each (256
+// rows in 64 sequences: 23 us by 64 rows, 14.4 by 16).
+int32_t balance_chunk(int64_t T, int64_t E, int64_t S) {
+    if (T <= kBalanceOneLaunch && T * E <= kBalanceOneLogits && S <= kBalanceOneSequences) return kBalanceOneLaunch;
+    int32_t chunk = E <= 256 ? 64 : 16;
+    while (chunk < 256 && (T + chunk - 1) / chunk > (E <= 256 ? 512 : 256)) chunk *= 2;
+    while (chunk > 16 && S * chunk > 4 * T) chunk /= 2;
     return chunk;
 }
 

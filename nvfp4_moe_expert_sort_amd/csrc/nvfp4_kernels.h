@@ -135,7 +135,8 @@ hipError_t launch_router_select_backward(const SelectParams& P, bool bf16, hipSt
 
 // The balance loss, the experts' counts and the loss's gradient (balance.hip).
 constexpr int32_t kMaxSequences = 65536;
-constexpr int32_t kBalanceOneLaunch = 256;  // rows of one workgroup, which then ends the loss itself
+// What one workgroup takes, which then ends the loss itself.
+constexpr int32_t kBalanceOneLaunch = 256, kBalanceOneLogits = 32768, kBalanceOneSequences = 4;
 struct BalanceParams {
     const void* logits;  // FP32 or BF16 [T, E], rows ld apart
     int64_t ld, T;
@@ -159,7 +160,7 @@ struct BalanceParams {
     int64_t ld_out;
     bool vec_add, vec_out, vec_counts;
 };
-int32_t balance_chunk(int64_t T);
+int32_t balance_chunk(int64_t T, int64_t E, int64_t S);  // rows of a workgroup
 hipError_t launch_balance(const BalanceParams& P, bool bf16, hipStream_t stream);
 
 // Low-rank adapters and their gradients (adapter.hip).

@@ -12,8 +12,8 @@ import functools
 
 import torch
 
-from . import (BALANCE_ONE_LAUNCH, BF16, F32, GROUP_MAX, LAYOUT_GEMM, LAYOUT_LOGICAL, MXFP4_SCALE_FLOOR, SCORE_SOFTMAX,
-               Adapters, BalanceConfig, Grad, Mxfp4Tensor, Nvfp4Error, SelectConfig, _check, lib)
+from . import (BALANCE_ONE_LAUNCH, BALANCE_ONE_LAUNCH_LOGITS, BALANCE_ONE_LAUNCH_SEQUENCES, BF16, F32, GROUP_MAX, LAYOUT_GEMM,
+               LAYOUT_LOGICAL, MXFP4_SCALE_FLOOR, SCORE_SOFTMAX, Adapters, BalanceConfig, Grad, Mxfp4Tensor, Nvfp4Error, SelectConfig, _check, lib)
 
 _BF16 = (torch.bfloat16, torch.int16, torch.uint16)  # storage of BF16 bits
 _TYPES = {torch.float32: F32, torch.bfloat16: BF16}
@@ -187,7 +187,9 @@ def router_balance_loss(logits, ids, coef: float, score: int = SCORE_SOFTMAX, of
     loss = torch.empty((1,), dtype=torch.float32, device=logits.device)
     counts = torch.empty((S, E), dtype=torch.int32, device=logits.device)
     n = _balance_workspace_bytes(T, E, S)
-    ws = torch.empty((n,), dtype=torch.uint8, device=logits.device) if T > BALANCE_ONE_LAUNCH else None  # not used below
+    ws = None  # not used by one launch
+    if T > BALANCE_ONE_LAUNCH or T * E > BALANCE_ONE_LAUNCH_LOGITS or S > BALANCE_ONE_LAUNCH_SEQUENCES:
+        ws = torch.empty((n,), dtype=torch.uint8, device=logits.device)
     st = lib().nvfp4moe_router_balance_loss(_balance_config(E, k, score, kind, coef), logits.data_ptr(), ld, T,
                                             ids.data_ptr(), off, S, loss.data_ptr(), counts.data_ptr(),
                                             None if ws is None else ws.data_ptr(), n, _raw_stream(logits))

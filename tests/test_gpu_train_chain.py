@@ -472,3 +472,24 @@ def test_rows_do_not_depend_on_large_batches(gpu, rank, n, order):
         vp = torch.empty(len(rows), rank, device=dev)
         part = m.adapter_linear(x[i], ids[i], A, B, base[i], v=vp)
         assert torch.equal(part, whole[i]) and torch.equal(vp, v[i])
+
+
+@pytest.mark.parametrize("T,E,S", [(256, 128, 4), (256, 128, 5), (256, 129, 1), (64, 512, 4), (65, 512, 2), (16, 1024, 9), (17, 1024, 9),
+                                   (33, 1000, 40), (700, 600, 700), (5000, 64, 1500), (9000, 300, 3)])
+def test_balance_launches(gpu, T, E, S):
+    """Around the sizes of one launch, and workgroups of fewer rows for short sequences; the workspace dirty."""
+    import torch
+    m, dev = gpu
+    g = torch.Generator(device=dev).manual_seed(T + S)
+    l = torch.randn(T, E, generator=g, device=dev)
+    ids = torch.randint(0, E, (T, 4), generator=g, device=dev).int()
+    cut = torch.randint(0, T + 1, (S - 1,), generator=g, device=dev).sort()[0]
+    off = torch.cat([cut.new_zeros(1), cut, cut.new_full((1,), T)]).int()
+    dirty = torch.full((64 << 20,), 0xFF, dtype=torch.uint8, device=dev)
+    del dirty
+    loss, counts = m.router_balance_loss(l, ids, 0.01, offsets=off)
+    d = m.router_balance_backward(l, counts, 4, 0.01, offsets=off)
+    _balance_near(m, loss, counts, d, l, ids, 0.01, off, None)
+    for _ in range(3):
+        again = m.router_balance_loss(l, ids, 0.01, offsets=off)
+        assert torch.equal(again[0], loss) and torch.equal(again[1], counts)

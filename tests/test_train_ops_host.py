@@ -61,7 +61,7 @@ def test_balance_refuses_bad_arguments(m):
     assert _back(m, c, T=0, logits=None, counts=None, out=None) == 0
     need = m.lib().nvfp4moe_balance_workspace_bytes(257, 128, 2)
     assert need % 256 == 0 and _loss(m, c, T=257, n=need - 1) == WORKSPACE
-    assert m.BALANCE_ONE_LAUNCH == 256
+    assert (m.BALANCE_ONE_LAUNCH, m.BALANCE_ONE_LAUNCH_LOGITS, m.BALANCE_ONE_LAUNCH_SEQUENCES) == (256, 32768, 4)
 
 
 def test_balance_workspace(m):
@@ -180,5 +180,6 @@ def test_a_workspace_is_enough_for_fewer_rows(m):
         size = m.lib().nvfp4moe_adapter_workspace_bytes
         fwd, both = ([size(_ad(m, n=n, rank=rank, K=K, N=N), M, back) for M in rows] for back in (0, 1))
         assert fwd == sorted(fwd) and both == sorted(both) and fwd[0] > 0 and all(a <= b for a, b in zip(fwd, both))
-    sizes = [m.lib().nvfp4moe_balance_workspace_bytes(T, 128, 7) for T in rows]
-    assert sizes == sorted(sizes) and sizes[0] > 0
+    for E, S in ((128, 1), (128, 7), (512, 1), (64, 1000), (1024, 65536)):
+        sizes = [m.lib().nvfp4moe_balance_workspace_bytes(T, E, S) for T in rows]
+        assert sizes == sorted(sizes) and sizes[0] > 0
