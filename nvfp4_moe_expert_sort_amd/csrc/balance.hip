@@ -91,14 +91,27 @@ __device__ __forceinline__ int32_t find_sequence(const BalanceParams& P, int64_t
         for (int32_t i = threadIdx.x & 63; i <= P.S; i += 64) n += seq_start(P, i) <= t ? 1 : 0;
         return wave_sum(n) - 1;
     }
-    for (int32_t i = threadIdx.x; i <= P.S; i += kThreads) n += seq_start(P, i) <= t ? 1 : 0;
-    n = wave_sum(n);
-    __syncthreads();
-    if ((threadIdx.x & 63) == 0) lds[threadIdx.x >> 6] = n;
-    __syncthreads();
-    n = 0;
-    for (int w = 0; w < kThreads / 64; w++) n += lds[w];
-    return n - 1;
+    // Of many, first every step-th one.
+    auto count = [&](int32_t from, int32_t step, int32_t len) {
+        int32_t c = 0;
+        for (int32_t i = threadIdx.x; i < len; i += kThreads) c += seq_start(P, from + i * step) <= t ? 1 : 0;
+        c = wave_sum(c);
+        __syncthreads();
+        if ((threadIdx.x & 63) == 0) lds[threadIdx.x >> 6] = c;
+        __syncthreads();
+        c = 0;
+        for (int w = 0; w < kThreads / 64; w++) c += lds[w];
+        return c;
+    };
+    int32_t from = 0, len = P.S + 1;
+    if (len > kThreads) {
+        const int32_t step = (len + kThreads - 1) / kThreads;
+        n = count(0, step, (len + step - 1) / step);
+        if (n == 0) return -1;
+        from = (n - 1) * step;
+        len = min(step, len - from);
+    }
+    return from + count(from, 1, len) - 1;
 }
 
 // The loss of sum_s 1 / T_s sum_e n_se sum_t p_te.
@@ -262,62 +275,90 @@ __global__ void __launch_bounds__(kChunkThreads) balance_chunk_kernel(BalancePar
     }
 }
 
-// Adds the slots of one sequence and 64 experts in FP64, in one order; the
-// workgroup that is last to finish adds up the workgroups' shares of the loss.
-// Each share is one value, stored and loaded at the scope of the device, which
-// no L2 keeps for itself, and stored for certain before its workgroup is
+// Adds the slots of one sequence and 64 experts in FP64, in one order: a
+// workgroup by 16 stripes of slots or, of so many that a workgroup each would
+// queue at the counter below (16384 of one row: 466 us a call, so 94), a wavefront.
+// The workgroup that is last to finish adds up the workgroups' shares of the
+// loss.  Each share is one value, stored and loaded at the scope of the device,
+// which no L2 keeps for itself, and stored for certain before its workgroup is
 // counted: with nothing else handed over, no cache has to be written back or
 // dropped (two fences: 7.8 us a launch at 13 sequences of 256 experts; so: 5.0).
+constexpr int kStripes = kJoinThreads / 64, kJoinItems = 1024;  // items up to which each has a workgroup
 __global__ void __launch_bounds__(kJoinThreads) balance_join_kernel(BalanceParams P) {
-    constexpr int kStripes = kJoinThreads / 64, kAhead = 4;
+    constexpr int kAhead = 4;
     __shared__ double sums[kStripes][64];
     __shared__ int32_t cnts[kStripes][64];
     __shared__ bool last;
-    const int groups = (P.E + 63) / 64, col = threadIdx.x & 63, stripe = threadIdx.x >> 6;
-    const int32_t s = blockIdx.x / groups;
-    const int e = (blockIdx.x % groups) * 64 + col;
-    const int64_t lo = seq_start(P, s), hi = seq_start(P, s + 1);
-    double sum = 0.0;
+    const int32_t groups = (P.E + 63) / 64, items = P.S * groups;
+    const int col = threadIdx.x & 63, stripe = threadIdx.x >> 6;
+    double sum = 0.0, share = 0.0;
     int32_t n = 0;
-    if (hi > lo && e < P.E) {
+    // Every `step`-th slot of a sequence's.
+    auto add = [&](int64_t lo, int64_t hi, int32_t s, int32_t e, int32_t first, int32_t step) {
+        sum = 0.0;
+        n = 0;
+        if (hi <= lo || e >= P.E) return;
         const int64_t b1 = (hi - 1) / P.chunk;
-        for (int64_t b = lo / P.chunk + stripe; b <= b1; b += kStripes * kAhead) {
+        for (int64_t b = lo / P.chunk + first; b <= b1; b += step * kAhead) {
             float p[kAhead];
             int32_t c[kAhead];
 #pragma unroll
             for (int k = 0; k < kAhead; k++) {
-                const int64_t at = (min(b + k * kStripes, b1) + s) * P.E + e;
+                const int64_t at = (min(b + k * step, b1) + s) * P.E + e;
                 p[k] = P.psum[at];
                 c[k] = P.csum[at];
             }
 #pragma unroll
             for (int k = 0; k < kAhead; k++)
-                if (b + k * kStripes <= b1) {
+                if (b + k * step <= b1) {
                     sum += (double)p[k];
                     n += c[k];
                 }
         }
-    }
-    sums[stripe][col] = sum;
-    cnts[stripe][col] = n;
-    __syncthreads();
-    if (stripe == 0) {
-        sum = 0.0;
-        n = 0;
+    };
+    auto end = [&](int64_t lo, int64_t hi, int32_t s, int32_t e) {
+        if (e >= P.E) return;
+        P.counts[(int64_t)s * P.E + e] = n;
+        if (hi > lo) share += sum * (double)n / (double)(hi - lo);
+    };
+    if (items > kJoinItems) {
+        for (int32_t item = blockIdx.x * kStripes + stripe; item < items; item += gridDim.x * kStripes) {
+            const int32_t s = item / groups, e = item % groups * 64 + col;
+            const int64_t lo = seq_start(P, s), hi = seq_start(P, s + 1);
+            add(lo, hi, s, e, 0, 1);
+            end(lo, hi, s, e);
+        }
+    } else {
+        const int32_t s = blockIdx.x / groups, e = blockIdx.x % groups * 64 + col;
+        const int64_t lo = seq_start(P, s), hi = seq_start(P, s + 1);
+        add(lo, hi, s, e, stripe, kStripes);
+        sums[stripe][col] = sum;
+        cnts[stripe][col] = n;
+        __syncthreads();
+        if (stripe == 0) {
+            sum = 0.0;
+            n = 0;
 #pragma unroll
-        for (int k = 0; k < kStripes; k++) {
-            sum += sums[k][col];
-            n += cnts[k][col];
+            for (int k = 0; k < kStripes; k++) {
+                sum += sums[k][col];
+                n += cnts[k][col];
+            }
+            end(lo, hi, s, e);
         }
-        if (e < P.E) P.counts[(int64_t)s * P.E + e] = n;
-        const double v = wave_sum(hi > lo ? sum * (double)n / (double)(hi - lo) : 0.0);
-        if (col == 0) {
-            __hip_atomic_store(&P.part[blockIdx.x], v, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-            asm volatile("" ::: "memory");
-            __builtin_amdgcn_s_waitcnt(0);  // the store has reached memory
-            asm volatile("" ::: "memory");
-            last = __hip_atomic_fetch_add(P.done, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) == gridDim.x - 1;
-        }
+        __syncthreads();
+    }
+    // The workgroup's share, from its wavefronts' (of few items, the first has it).
+    share = wave_sum(share);
+    if (col == 0) sums[0][stripe] = share;
+    __syncthreads();
+    if (threadIdx.x == 0) {
+        share = 0.0;
+        for (int k = 0; k < kStripes; k++) share += sums[0][k];
+        __hip_atomic_store(&P.part[blockIdx.x], share, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+        asm volatile("" ::: "memory");
+        __builtin_amdgcn_s_waitcnt(0);  // the store has reached memory
+        asm volatile("" ::: "memory");
+        last = __hip_atomic_fetch_add(P.done, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) == gridDim.x - 1;
     }
     __syncthreads();
     if (!last) return;
@@ -431,7 +472,9 @@ hipError_t loss_run(const BalanceParams& P, hipStream_t s) {
     hipLaunchKernelGGL((balance_chunk_kernel<LT, NV, L>), dim3((unsigned)chunks), dim3(kChunkThreads), 0, s, P);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess || chunks == 1) return e;
-    hipLaunchKernelGGL(balance_join_kernel, dim3((unsigned)(P.S * ((P.E + 63) / 64))), dim3(kJoinThreads), 0, s, P);
+    const int items = P.S * ((P.E + 63) / 64);
+    const int groups = items > kJoinItems ? std::min((items + kStripes - 1) / kStripes, 512) : items;
+    hipLaunchKernelGGL(balance_join_kernel, dim3((unsigned)groups), dim3(kJoinThreads), 0, s, P);
     return hipGetLastError();
 }
 template <int LT, int NV, typename L>

@@ -493,3 +493,30 @@ def test_balance_launches(gpu, T, E, S):
     for _ in range(3):
         again = m.router_balance_loss(l, ids, 0.01, offsets=off)
         assert torch.equal(again[0], loss) and torch.equal(again[1], counts)
+
+
+@pytest.mark.parametrize("T,E,S", [(700, 40, 1024), (700, 40, 1025), (3000, 100, 600), (20000, 24, 5000), (300, 8, 65536)])
+def test_balance_of_many_sequences(gpu, T, E, S):
+    """Most of them short, one of a third of the rows: against sums per sequence in FP64."""
+    import torch
+    m, dev = gpu
+    g = torch.Generator(device=dev).manual_seed(T + S)
+    l = torch.randn(T, E, generator=g, device=dev)
+    ids = torch.randint(0, E, (T, 2), generator=g, device=dev).int()
+    cut = torch.randint(0, T + 1, (S - 1,), generator=g, device=dev).sort()[0]
+    cut[(cut > T // 3) & (cut < 2 * T // 3)] = T // 3
+    off = torch.cat([cut.new_zeros(1), cut, cut.new_full((1,), T)])
+    loss, counts = m.router_balance_loss(l, ids, 0.01, offsets=off.int())
+    rows = (off[1:] - off[:-1])
+    seq = torch.repeat_interleave(torch.arange(S, device=dev), rows)
+    n = torch.zeros(S, E, dtype=torch.float64, device=dev).index_put_((seq[:, None].expand(-1, 2), ids.long()), torch.ones((), dtype=torch.float64, device=dev), accumulate=True)
+    assert torch.equal(counts.double(), n)
+    p = torch.softmax(l.double(), 1)
+    f = n * E / (2 * rows[:, None].clamp(min=1))
+    want = 0.01 / T * float((f[seq] * p).sum())
+    assert abs(float(loss) - want) <= 97 * R.U * want
+    d = m.router_balance_backward(l, counts, 2, 0.01, offsets=off.int())
+    ref = 0.01 / T * p * (f[seq] - (f[seq] * p).sum(1, keepdim=True))
+    # w within 12 u, D^2 within 24, the difference's terms within 12 of their size, and the last rounding
+    size = 0.01 / T * p * (f[seq] + (f[seq] * p).sum(1, keepdim=True))
+    assert ((d.double() - ref).abs() <= 64 * R.U * size + 1e-36).all()
