@@ -614,9 +614,9 @@ typedef struct {
  * with base the shared projection's output (nvfp4moe_mxfp4_linear's, say) or
  * NULL for 0.  Rows whose id lies outside [0, n) have no adapter: out_r is
  * base_r to the bit (or 0), v_r is 0.  Sums are FP32, rounded once at the end;
- * v enters the second product as two BF16 values (within 2^-16 of it; an
- * infinite element of B gives NaN where the formula may have an infinity).  A
- * row's bits depend on that row alone: not on the batch, nor on its place in it.
+ * v enters the second product in full (three BF16 values; an infinite element
+ * of B gives NaN where the formula may have an infinity).  A row's bits depend
+ * on that row alone: not on the batch, nor on its place in it.
  * x [M, in_features], base and out [M, out_features] BF16, rows ldx, ld_base
  * and ld_out apart (multiples of 8, pointers 16-byte aligned); out may be base
  * (in place, the same stride, else NVFP4_E_ARG) and may not overlap anything else.  v (FP32

@@ -293,10 +293,12 @@ __global__ void __launch_bounds__(kPlanThreads) adapter_plan_kernel(AdapterPlan 
 //
 // The first product V = A x^T over K is split over the wavefronts and joined in
 // LDS in one fixed order, whatever the tile: a row's bits do not depend on the
-// rows beside it.  V, an FP32 sum, is passed
-// on as two BF16 values (2^-16 of it may be lost, against the 2^-8 of the output's
-// one rounding): 32 of the second product's inputs are then 16 ranks twice,
-// which costs no instruction at rank 16.
+// rows beside it.  V, an FP32 sum, is passed on as three BF16 values, which is all
+// of its 24 bits.  (With two, of the 20480 outputs of 5 rows some 20 lay one BF16
+// step off, and 2 at most so.  The third costs nothing measurable up to rank 32; 8192
+// rows of 4096 columns: rank 64 42.2 -> 43.0 us a call, rank 128 54 -> 58.)  At rank
+// 16 the second product has 32 inputs of 16 ranks of the first two pieces, and 32
+// of the third and zeros.
 //
 // A matrix operand has its rows on neighbouring lanes; read like that, memory
 // gives 16 bytes of 16 lines at a time.  So each wavefront reads its operands
@@ -307,8 +309,8 @@ __global__ void __launch_bounds__(kPlanThreads) adapter_plan_kernel(AdapterPlan 
 // holds neighbouring ones.
 //
 // RB: ranks in blocks of 16; MB: rows in blocks of 16.
-// kGrad: V and the forward's v also go, as three BF16 values, to the operands
-// of the weights' gradients.
+// kGrad: V and the forward's v also go, as such values, to the operands of the
+// weights' gradients.
 // kSmall: at most 512 rows, without a plan: every workgroup groups them itself.
 // The gradient's A and B, which are copies anyway, come from rank 33 on as the
 // products' operands (adapter_pack_kernel) and need not be turned over: 69
@@ -326,7 +328,7 @@ __global__ void __launch_bounds__(kPlanThreads) adapter_plan_kernel(AdapterPlan 
 template <int RB, int MB, bool kGrad, bool kBase, bool kSmall>
 __global__ void __launch_bounds__(kAdWaves * 64, RB < 4 || (RB == 4 && kGrad) ? 4 : 2) adapter_kernel(AdapterParams P) {
     constexpr bool kPacked = kGrad && RB >= 4;
-    constexpr int kR = 16 * RB, kPieces = kGrad ? 3 : 2, kPitch = kPieces * kR + 8;
+    constexpr int kR = 16 * RB, kPieces = 3, kPitch = (RB == 1 ? 4 : kPieces) * kR + 8;
     constexpr int kMost = kPacked ? 4 : 8, kRound = RB * MB < kMost ? RB * MB : kMost;  // blocks of V joined at a time
     constexpr int kA = RB < 2 ? RB : 2;                // rank blocks turned over at a time
     // Steps of the first product whose loads are in registers.
@@ -618,6 +620,8 @@ __global__ void __launch_bounds__(kAdWaves * 64, RB < 4 || (RB == 4 && kGrad) ? 
             for (int p = 0; p < kPieces; p++)
                 *reinterpret_cast<u32x2*>(&vs[16 * m + i][p * kR + r]) =
                     u32x2{part[p][0] | (part[p][1] << 16), part[p][2] | (part[p][3] << 16)};
+            // (the third piece's inputs of the second product are 16 ranks and 16 zeros)
+            if constexpr (RB == 1) *reinterpret_cast<u32x2*>(&vs[16 * m + i][kPieces * kR + r]) = u32x2{0, 0};
         }
     }
     __syncthreads();
@@ -700,7 +704,7 @@ __global__ void __launch_bounds__(kAdWaves * 64, RB < 4 || (RB == 4 && kGrad) ? 
                 w[b] = kPacked ? bf[kPacked ? b * kB + j : 0] : own[p ^ (((p >> 4) ^ (p >> 6)) & 15)];
             }
 #pragma unroll
-            for (int h = RB > 1 ? 1 : 0; h >= 0; h--) {  // the second part of V first
+            for (int h = RB > 1 ? kPieces - 1 : 1; h >= 0; h--) {  // the small parts of V first
                 u32x4 v[MB];
 #pragma unroll
                 for (int m = 0; m < MB; m++) v[m] = *reinterpret_cast<const u32x4*>(&vs[16 * m + i][32 * (j + h * kB) + 8 * q]);
