@@ -33,9 +33,11 @@ __device__ __forceinline__ void issue() { __builtin_amdgcn_sched_barrier(0); }
 __device__ __forceinline__ u32x4 load16(const uint16_t* p) { return *reinterpret_cast<const u32x4*>(p); }
 
 // v as the sum of BF16 values of falling size, each the rounding of what the
-// ones before it leave; an infinite or NaN v is the first of them alone.
+// ones before it leave (of a finite value to a finite one: above 2^128 - 2^119
+// the nearest would be infinity); an infinite or NaN v is the first of them alone.
 __device__ __forceinline__ uint32_t bf16_piece(float& rest) {
-    const uint32_t b = bf16_hw(rest);
+    uint32_t b = bf16_hw(rest);
+    if ((b & 0x7FFF) == 0x7F80 && fabsf(rest) < __builtin_inff()) b--;
     const float r = rest - bf16_to_f32(b);
     rest = fabsf(r) < __builtin_inff() ? r : 0.0f;
     return b;

@@ -48,3 +48,44 @@ def test_all_bits_of_v_reach_the_outputs(gpu, M, rank):
     B = b.t().expand(2, -1, -1).to(torch.bfloat16).to(dev).contiguous()
     dx = m.adapter_backward(x, ids, A, B, v, dy, torch.full((M, K), -1.0, dtype=torch.bfloat16, device=dev))[0]
     assert (dx == 2.0 ** -22).all(), dx.unique()
+
+
+@pytest.mark.parametrize("rank", [8, 32, 64, 128])
+@pytest.mark.parametrize("M", [2, 600])
+@pytest.mark.parametrize("sign", [1, -1])
+def test_the_largest_values_stay_finite(gpu, M, rank, sign):
+    """v and w between the largest BF16 value and the largest FP32 one, which have no BF16 rounding but infinity:
+    outputs and gradients that are finite, whole in FP32, and rounded once."""
+    import torch
+    m, dev = gpu
+    bf, K, N = torch.bfloat16, 72, 136
+    top, more, tiny = sign * float(torch.finfo(bf).max), sign * 0.9375 * 2.0 ** 120, 2.0 ** -100
+    big = torch.tensor(top, dtype=torch.float64) + more
+    assert float(big.float()) == float(big) and torch.isinf(big.to(bf))
+
+    def pair(wide):  # a row of ones, and what makes `big` of it
+        x, z = torch.zeros(wide), torch.zeros(rank, wide)
+        x[:2], z[rank - 1, :2] = 1.0, torch.tensor([top, more])
+        return x.to(bf).to(dev).expand(M, -1).contiguous(), z.to(bf).to(dev)[None].contiguous()
+
+    ids = torch.zeros(M, dtype=torch.int32, device=dev)
+    x, A = pair(K)
+    B = torch.full((1, N, rank), tiny, dtype=bf, device=dev)
+    v = torch.empty(M, rank, device=dev)
+    out = m.adapter_linear(x, ids, A, B, v=v)
+    assert (v[:, rank - 1].double() == float(big)).all() and not v[:, :rank - 1].any()
+    assert torch.equal(out, (big * tiny).float().to(bf).to(dev).expand(M, N))
+    # one row of dy is not zero: dB = dy v^T.  (v's own gradients are small: B is.)
+    dy = torch.zeros(M, N, dtype=bf, device=dev)
+    dy[1] = tiny
+    _, _, dB = m.adapter_backward(x, ids, A, B, v, dy)
+    assert (dB[0, :, rank - 1].double() == float(big) * tiny).all() and not dB[0, :, :rank - 1].any()
+    # w = B^T dy of that size, in one row: dx = A^T w and dA = w x^T
+    dy, Bt = pair(N)
+    dy[0] = 0
+    dy[2:] = 0
+    x = torch.full((M, K), tiny, dtype=bf, device=dev)
+    A = torch.full((1, rank, K), tiny, dtype=bf, device=dev)
+    dx, dA, _ = m.adapter_backward(x, ids, A, Bt.transpose(1, 2).contiguous(), torch.zeros_like(v), dy)
+    assert torch.equal(dx[1], (big * tiny).float().to(bf).to(dev).expand(K)) and not dx[0].any() and not dx[2:].any()
+    assert (dA[0, rank - 1].double() == float(big) * tiny).all() and not dA[0, :rank - 1].any()
