@@ -114,6 +114,17 @@ __device__ __forceinline__ int32_t find_sequence(const BalanceParams& P, int64_t
     return from + count(from, 1, len) - 1;
 }
 
+// The last sequence that starts at row t or before it (S: t lies behind them all),
+// of which sequence s is one.  64 offsets a step, by every wavefront for itself.
+__device__ __forceinline__ int32_t last_start(const BalanceParams& P, int32_t s, int64_t t) {
+    for (int32_t left = P.S - s; left > 0;) {
+        const int32_t step = (left + 63) / 64, at = s + ((threadIdx.x & 63) + 1) * step;
+        s += __popcll(__ballot(at <= P.S && seq_start(P, min(at, P.S)) <= t)) * step;
+        left = min(step - 1, P.S - s);
+    }
+    return s;
+}
+
 // The loss of sum_s 1 / T_s sum_e n_se sum_t p_te.
 __device__ __forceinline__ float balance_scaled(const BalanceParams& P, double total) {
     const double tokens = (double)max(seq_start(P, P.S) - seq_start(P, 0), (int64_t)1);
@@ -259,6 +270,10 @@ __global__ void __launch_bounds__(kChunkThreads) balance_chunk_kernel(BalancePar
             s++;
             lo = hi;
             hi = next;
+            if (hi == lo && s < P.S) {  // without rows: on to the next that has some (40000 such one by one: 15 ms)
+                s = last_start(P, s, lo);
+                hi = seq_start(P, min(s + 1, P.S));
+            }
             next = seq_start(P, min(s + 2, P.S));  // (on its way until the sequence after this one)
         }
     }
@@ -402,7 +417,12 @@ __global__ void __launch_bounds__(kBalThreads) balance_backward_kernel(BalancePa
             for (int j = 0; j < 4; j++) add[4 * i + j] = v[j];
         }
         int32_t s = max(find_sequence<kBalThreads>(P, tile * kTok, found), 0);
-        while (s < P.S && seq_start(P, s + 1) <= tr) s++;
+        // The token's own, by steps that double and then halve: between the tile's rows
+        // there may be thousands of sequences without any (40000 one by one: 8 ms).
+        int32_t step = 1;
+        for (; s + step <= P.S && seq_start(P, s + step) <= tr; step *= 2) s += step;
+        while ((step /= 2) > 0)
+            if (s + step <= P.S && seq_start(P, s + step) <= tr) s += step;
         double rows = 0.0;  // of the sequence; rows of none get no gradient
         if (s < P.S) {
             const int64_t lo = seq_start(P, s), hi = seq_start(P, s + 1);

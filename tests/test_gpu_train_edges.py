@@ -89,3 +89,54 @@ def test_the_largest_values_stay_finite(gpu, M, rank, sign):
     dx, dA, _ = m.adapter_backward(x, ids, A, Bt.transpose(1, 2).contiguous(), torch.zeros_like(v), dy)
     assert torch.equal(dx[1], (big * tiny).float().to(bf).to(dev).expand(K)) and not dx[0].any() and not dx[2:].any()
     assert (dA[0, rank - 1].double() == float(big) * tiny).all() and not dA[0, :rank - 1].any()
+
+
+def _milliseconds(f):
+    """The shortest of five calls."""
+    import torch
+    best = float("inf")
+    for _ in range(5):
+        a, b = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+        a.record()
+        f()
+        b.record()
+        torch.cuda.synchronize()
+        best = min(best, a.elapsed_time(b))
+    return best
+
+
+@pytest.mark.parametrize("T", [12, 100, 1000, 16384])
+@pytest.mark.parametrize("where", ["before", "between", "behind", "within"])
+def test_sequences_without_rows_cost_little(gpu, T, where):
+    """65536 sequences of which a few have rows: what those few alone give, in less than 2 ms.  (Well below 0.2 where
+    nothing steps through them one by one, which takes 8 to 16.)"""
+    import torch
+    m, dev = gpu
+    S, E, k = 65536, 40, 2
+    l, ids = torch.randn(T, E, device=dev), torch.randint(0, E, (T, k), device=dev).int()
+    few = torch.tensor([0, 3, 9, T], dtype=torch.int32, device=dev)
+    off = torch.empty(S + 1, dtype=torch.int32, device=dev)
+    if where == "before":
+        at = [S - 3, S - 2, S - 1]
+        off[:] = 0
+        off[-3:] = few[1:]
+    elif where == "between":
+        at = [0, 30000, 65000]
+        off[:1], off[1:30001], off[30001:65001], off[65001:] = 0, 3, 9, T
+    elif where == "behind":
+        at = [0, 1, 2]
+        off[:] = T
+        off[:3] = few[:3]
+    else:  # the rows before the first offset and behind the last belong to none
+        few = torch.tensor([2, 5, 7, 11], dtype=torch.int32, device=dev)
+        at = [40000, 40001, 65535]
+        off[:40001], off[40001:40002], off[40002:65536], off[65536:] = 2, 5, 7, 11
+    loss, counts = m.router_balance_loss(l, ids, 0.01, offsets=off)
+    want, n = m.router_balance_loss(l, ids, 0.01, offsets=few)
+    # sums over at most 256 tokens in FP32, then FP64, in chunks of other sizes
+    assert abs(float(loss) - float(want)) <= 2 * 97 * 2.0 ** -24 * float(want)
+    assert torch.equal(counts[at], n) and int(counts.sum()) == int(n.sum()) == k * int(few[3] - few[0])
+    d = m.router_balance_backward(l, counts, k, 0.01, offsets=off)
+    assert torch.equal(d, m.router_balance_backward(l, n, k, 0.01, offsets=few))
+    assert _milliseconds(lambda: m.router_balance_loss(l, ids, 0.01, offsets=off)) < 2
+    assert _milliseconds(lambda: m.router_balance_backward(l, counts, k, 0.01, offsets=off)) < 2
