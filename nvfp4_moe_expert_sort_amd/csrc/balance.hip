@@ -464,7 +464,7 @@ __global__ void __launch_bounds__(kBalThreads) balance_backward_kernel(BalancePa
             for (int j = 0; j < 4; j++) {
                 const int k = 4 * i + j;
                 const double d = c * (double)(w[k] * other[k]) * __builtin_fma((double)__float_as_int(n[k]), D, -G);
-                v[j] = (float)(d + (double)add[k]);
+                v[j] = w[k] > 0.0f ? (float)(d + (double)add[k]) : add[k];  // (c may be infinite or NaN, like dloss)
             }
             if constexpr (sizeof(L) == 4) {
                 if (P.vec_out && e0 + 4 <= P.E)

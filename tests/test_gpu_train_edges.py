@@ -140,3 +140,30 @@ def test_sequences_without_rows_cost_little(gpu, T, where):
     assert torch.equal(d, m.router_balance_backward(l, n, k, 0.01, offsets=few))
     assert _milliseconds(lambda: m.router_balance_loss(l, ids, 0.01, offsets=off)) < 2
     assert _milliseconds(lambda: m.router_balance_backward(l, counts, k, 0.01, offsets=off)) < 2
+
+
+@pytest.mark.parametrize("dloss", [float("inf"), float("-inf"), float("nan")])
+def test_a_loss_scale_that_overflowed(gpu, dloss):
+    """A gradient of the loss that is not finite: unusable logits, rows masked whole and rows of no sequence still get
+    `add` alone (or 0), every other row shows that it overflowed."""
+    import torch
+    m, dev = gpu
+    for E, kind in ((16, torch.float32), (130, torch.bfloat16), (600, torch.float32), (1000, torch.bfloat16)):
+        for score in (m.SCORE_SOFTMAX, m.SCORE_SIGMOID):
+            l = torch.randn(40, E, device=dev).to(kind)
+            l[:, ::3] = -float("inf")
+            l[:, 1::7] = float("nan")
+            l[5] = -float("inf")
+            ids = torch.randint(0, E, (40, 2), device=dev).int()
+            ids[:, 0] = 2
+            off = torch.tensor([3, 20, 37], dtype=torch.int32, device=dev)
+            add = torch.randn(40, E, device=dev).to(kind)
+            _, counts = m.router_balance_loss(l, ids, 0.01, score=score, offsets=off)
+            scale = torch.full((1,), dloss, device=dev)
+            dead = ~(l > -float("inf"))
+            dead[:3] = dead[37:] = True
+            for a in (add, None):
+                d = m.router_balance_backward(l, counts, 2, 0.01, score=score, offsets=off, dloss=scale, add=a)
+                assert torch.equal(d[dead], add[dead] if a is not None else torch.zeros_like(add[dead]))
+                live = ~dead.all(1)
+                assert (~torch.isfinite(d[live])).any(1).all()
