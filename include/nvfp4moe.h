@@ -486,7 +486,8 @@ enum {
  * float), counts [S, E] int32, every element written.  The probabilities are
  * summed in FP32 over at most 256 tokens and in FP64 from there, in one order:
  * the same bits in every run.
- * Requirements: 0 <= T < 2^31, 1 <= S <= 65536, ld >= E; logits aligned to
+ * Requirements: 0 <= T < 2^31, 1 <= S <= 65536, ld >= E; a count below 2^31
+ * (so it is unless ids name an expert twice in a row); logits aligned to
  * their element, the others to 4 bytes; workspace 256-byte aligned,
  * nvfp4moe_balance_workspace_bytes(T, E, S) bytes (0 for sizes out of range;
  * enough for fewer rows too), not shared by calls that may run at the same

@@ -166,11 +166,12 @@ __global__ void __launch_bounds__(kChunkThreads) balance_chunk_kernel(BalancePar
     __shared__ int32_t found[kWaves];
     __shared__ double shares[kWaves];
     const int lane = threadIdx.x & (LT - 1), slot = threadIdx.x / LT, wave = threadIdx.x >> 6;
-    const int64_t first = (int64_t)blockIdx.x * P.chunk, past = min(P.T, first + P.chunk);
+    const int64_t block = (int64_t)blockIdx.y * gridDim.x + blockIdx.x;  // (past the last chunk, no rows)
+    const int64_t first = block * P.chunk, past = min(P.T, first + P.chunk);
     const bool whole = gridDim.x == 1;
     double total = 0.0;  // whole: the thread's part of loss / factor
     int32_t s_next = 0;  // whole: the first sequence whose counts are not written
-    if (!whole && blockIdx.x == 0 && threadIdx.x == 0) *P.done = 0;
+    if (!whole && block == 0 && threadIdx.x == 0) *P.done = 0;
     float l[NV], acc[NV];
     int32_t id[kIds], id_tok[kIds];  // the thread's ids of a pass, and which token's each is
     auto load = [&](int64_t t0) {
@@ -223,7 +224,7 @@ __global__ void __launch_bounds__(kChunkThreads) balance_chunk_kernel(BalancePar
 #pragma unroll
         for (int i = 0; i < NV; i++) acc[i] = 0.0f;
         __syncthreads();
-        const int64_t at = (whole ? s : (int64_t)blockIdx.x + s) * P.E;
+        const int64_t at = (whole ? s : block + s) * P.E;
         static_assert(kMaxExperts <= kChunkThreads, "an expert a thread");
         if (const int e = threadIdx.x; e < P.E) {
             float sum = 0.0f;
@@ -489,7 +490,10 @@ namespace {
 template <int LT, int NV, typename L>
 hipError_t loss_run(const BalanceParams& P, hipStream_t s) {
     const int64_t chunks = std::max<int64_t>(1, (P.T + P.chunk - 1) / P.chunk);
-    hipLaunchKernelGGL((balance_chunk_kernel<LT, NV, L>), dim3((unsigned)chunks), dim3(kChunkThreads), 0, s, P);
+    // (a launch has fewer than 2^32 threads along x: 2^22 chunks are too many)
+    const int64_t x = std::min<int64_t>(chunks, 1 << 21);
+    hipLaunchKernelGGL((balance_chunk_kernel<LT, NV, L>), dim3((unsigned)x, (unsigned)((chunks + x - 1) / x)),
+                       dim3(kChunkThreads), 0, s, P);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess || chunks == 1) return e;
     const int items = P.S * ((P.E + 63) / 64);

@@ -167,3 +167,42 @@ def test_a_loss_scale_that_overflowed(gpu, dloss):
                 assert torch.equal(d[dead], add[dead] if a is not None else torch.zeros_like(add[dead]))
                 live = ~dead.all(1)
                 assert (~torch.isfinite(d[live])).any(1).all()
+
+
+def test_balance_of_2_to_the_30_rows(gpu):
+    """More chunks than a launch has workgroups along one axis.  Rows repeat every 2^20."""
+    import torch
+    m, dev = gpu
+    P, times, rest = 1 << 20, 1024, 5
+    T, E = P * times + rest, 2
+    few = torch.randn(P, E, device=dev).to(torch.bfloat16)
+    one = torch.randint(0, E, (P, 1), device=dev).int()
+    l, ids = torch.empty(T, E, dtype=torch.bfloat16, device=dev), torch.empty(T, 1, dtype=torch.int32, device=dev)
+    for t in range(0, T, P):
+        l[t:t + P], ids[t:t + P] = few[:T - t], one[:T - t]
+    p = torch.softmax(few.double(), 1)
+    for cut in (None, P * 1000 + 3):
+        # (times, rest) of each sequence, and where its rows begin in the pattern
+        parts = [(0, T)] if cut is None else [(0, cut), (cut, T)]
+        off = None if cut is None else torch.tensor([0, cut, T], dtype=torch.int32, device=dev)
+        loss, counts = m.router_balance_loss(l, ids, 1.0, offsets=off)
+        d = m.router_balance_backward(l, counts, 1, 1.0, offsets=off)
+        want = 0.0
+
+        def upto(x, n):  # the sum of the first n rows of the repeated x
+            return x.sum(0) * (n // P) + x[:n % P].sum(0)
+
+        hot = torch.nn.functional.one_hot(one[:, 0].long(), E)
+        for s, (a, b) in enumerate(parts):
+            n = upto(hot, b) - upto(hot, a)
+            assert torch.equal(counts[s].long(), n)
+            f = n.double() * E / (b - a)
+            want += float((f * (upto(p, b) - upto(p, a))).sum()) / T
+            for r in (a, b - 37):  # some of the sequence's rows
+                q = p[torch.arange(r, r + 37, device=dev) % P]
+                ref = q * (f - (q @ f[:, None])) / T
+                # every term within 64 u of its size, then the rounding to BF16
+                size = q * (f + (q @ f[:, None])) / T
+                assert ((d[r:r + 37].double() - ref).abs() <= 64 * 2.0 ** -24 * size + 2.0 ** -8 * ref.abs() + 1e-38).all()
+        assert abs(float(loss) - want) <= 97 * 2.0 ** -24 * want
+        del d
