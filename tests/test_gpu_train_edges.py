@@ -206,3 +206,128 @@ def test_balance_of_2_to_the_30_rows(gpu):
                 assert ((d[r:r + 37].double() - ref).abs() <= 64 * 2.0 ** -24 * size + 2.0 ** -8 * ref.abs() + 1e-38).all()
         assert abs(float(loss) - want) <= 97 * 2.0 ** -24 * want
         del d
+
+
+# --- branches that only large calls reach -------------------------------------------------------------
+
+def _ints(g, *shape, top=1):
+    import torch
+    return torch.randint(-top, top + 1, shape, generator=g, device=g.device).to(torch.bfloat16)
+
+
+@pytest.mark.parametrize("M,n,rank", [((1 << 18) + 77, 37, 16), (600001, 1000, 8), (600001, 3, 24)])
+@pytest.mark.parametrize("order", ["mixed", "sorted"])
+def test_adapters_of_more_rows_than_the_plan_has_threads(gpu, M, n, rank, order):
+    """A workgroup of the plan places several times 1024 rows from 2^18 on.  Whole numbers, exact."""
+    import torch
+    from tests import plain_train_ops as R
+    m, dev = gpu
+    g = torch.Generator(device=dev).manual_seed(M + n)
+    K, N = 64, 72
+    x, A, B, dy = _ints(g, M, K), _ints(g, n, rank, K), _ints(g, n, N, rank), _ints(g, M, N)
+    base, dxb = _ints(g, M, N, top=100), _ints(g, M, K, top=9)
+    ids = torch.randint(-1, n + 1, (M,), generator=g, device=dev).int()
+    if order == "sorted":
+        ids = ids.sort()[0]
+    v = torch.empty(M, rank, device=dev)
+    got = m.adapter_linear(x, ids, A, B, base, v=v)
+    want, wv, _ = R.adapter_linear(x, ids, A, B, base, None)
+    assert torch.equal(got, want.float().to(torch.bfloat16)) and torch.equal(v.double(), wv)
+    got = m.adapter_backward(x, ids, A, B, v, dy, dxb)
+    want, _ = R.adapter_backward(x, ids, A, B, v, dy, dxb, None)
+    assert float(want[1].abs().max()) < 2 ** 23 and float(want[2].abs().max()) < 2 ** 23
+    assert torch.equal(got[0], want[0].float().to(torch.bfloat16))
+    assert torch.equal(got[1].double(), want[1]) and torch.equal(got[2].double(), want[2])
+
+
+@pytest.mark.parametrize("K,N", [(64, 4096), (4096, 64), (72, 4104)])
+@pytest.mark.parametrize("rank", [16, 32, 64, 128])
+def test_base_past_the_last_level_cache(gpu, K, N, rank):
+    """More than 2^28 bytes of rows, from which on base is read past the cache: beside the output and in place, forward
+    and dx.  Whole numbers, exact."""
+    import torch
+    from tests import plain_train_ops as R
+    m, dev = gpu
+    M, n = 20011, 5
+    assert 2 * M * (min(K, N) + max(K, N)) * 2 >= 1 << 28
+    g = torch.Generator(device=dev).manual_seed(rank + K)
+    x, A, B, dy = _ints(g, M, K), _ints(g, n, rank, K), _ints(g, n, N, rank), _ints(g, M, N)
+    base, dxb = _ints(g, M, N, top=100), _ints(g, M, K, top=9)
+    ids = torch.randint(-1, n, (M,), generator=g, device=dev).int()
+    v = torch.empty(M, rank, device=dev)
+    want = R.adapter_linear(x, ids, A, B, base, None)[0].float().to(torch.bfloat16)
+    keep = base.clone()
+    assert torch.equal(m.adapter_linear(x, ids, A, B, base, v=v), want) and torch.equal(base, keep)
+    m.adapter_linear(x, ids, A, B, base, out=base)
+    assert torch.equal(base, want)
+    wx, wA, wB = R.adapter_backward(x, ids, A, B, v, dy, dxb, None)[0]
+    assert float(wx.abs().max()) < 2 ** 23 and float(wA.abs().max()) < 2 ** 23 and float(wB.abs().max()) < 2 ** 23
+    keep = dxb.clone()
+    dx, dA, dB = m.adapter_backward(x, ids, A, B, v, dy, dxb)
+    wx = wx.float().to(torch.bfloat16)
+    assert torch.equal(dx, wx) and torch.equal(dA.double(), wA) and torch.equal(dB.double(), wB) and torch.equal(dxb, keep)
+    dx, _, _ = m.adapter_backward(x, ids, A, B, v, dy, dxb, out=(dxb, torch.empty_like(dA), torch.empty_like(dB)))
+    assert dx is dxb and torch.equal(dx, wx)
+
+
+# --- the balance loss's workspace and the neighbours of its outputs -----------------------------------
+
+def _guarded_loss(m, l, ids, off, fill):
+    """(loss, counts) through the C entry point, with a workspace of exactly the size that it asks for and outputs that
+    are slices; everything filled with `fill` before, and what lies around them checked after."""
+    import ctypes
+    import torch
+    T, E = l.shape
+    S = off.numel() - 1
+
+    def slab(size):  # a slice in the middle, 256-byte aligned, and its neighbours
+        buf = torch.full((size + 8192,), fill, dtype=torch.uint8, device=l.device)
+        return buf[4096:4096 + size], (buf[:4096], buf[4096 + size:])
+
+    need = m.lib().nvfp4moe_balance_workspace_bytes(T, E, S)
+    parts = [slab(n) for n in (need, 4, 4 * S * E)]
+    ws, loss, counts = (p[0] for p in parts)
+    cfg = m.BalanceConfig(E, ids.shape[1], m.SCORE_SOFTMAX, m.F32, 0.01)
+    st = m.lib().nvfp4moe_router_balance_loss(ctypes.byref(cfg), l.data_ptr(), l.stride(0), T, ids.data_ptr(), off.data_ptr(), S,
+                                              loss.data_ptr(), counts.data_ptr(), ws.data_ptr(), need,
+                                              torch.cuda.current_stream().cuda_stream)
+    assert st == 0
+    for _, around in parts:
+        assert all((t == fill).all() for t in around)
+    return loss.view(torch.float32).clone(), counts.view(torch.int32).view(S, E).clone()
+
+
+@pytest.mark.parametrize("T,E,S", [(256, 128, 4), (256, 128, 5), (256, 129, 1), (64, 512, 4), (65, 512, 2), (16, 1024, 9), (17, 1024, 9),
+                                   (33, 1000, 40), (700, 600, 700), (5000, 64, 1500), (9000, 300, 3), (700, 40, 1025),
+                                   (20000, 24, 5000), (300, 8, 65536), (131073, 16, 2), (50, 33, 200)])
+def test_balance_workspace_is_kept_to(gpu, T, E, S):
+    """The workspace may hold anything, its size is enough, and the outputs' neighbours stay."""
+    import torch
+    m, dev = gpu
+    g = torch.Generator(device=dev).manual_seed(T + S)
+    l = torch.randn(T, E, generator=g, device=dev)
+    ids = torch.randint(0, E, (T, 4), generator=g, device=dev).int()
+    cut = torch.randint(0, T + 1, (S - 1,), generator=g, device=dev).sort()[0]
+    off = torch.cat([cut.new_zeros(1), cut, cut.new_full((1,), T)]).int()
+    loss, counts = m.router_balance_loss(l, ids, 0.01, offsets=off)
+    assert torch.isfinite(loss).all() and int(counts.sum()) == 4 * T
+    for fill in (0, 0xFF, 0x5A):
+        got = _guarded_loss(m, l, ids, off, fill)
+        assert torch.equal(got[0], loss) and torch.equal(got[1], counts)
+
+
+@pytest.mark.parametrize("T", [50, 700, 5000])
+def test_decreasing_offsets_keep_to_the_workspace(gpu, T):
+    """The results are undefined, what lies beside loss, counts and workspace is not."""
+    import torch
+    m, dev = gpu
+    l, ids = torch.randn(T, 40, device=dev), torch.randint(0, 40, (T, 2), device=dev).int()
+    lists = [[0, 40, 10, T], [T, 0], [30, 20, 10, 0], [0, T, 0, T], [2 ** 31 - 1, -2 ** 31, 5, 3], [5, 5, 3, 3, T, T, 2, 2, T],
+             list(range(T, -1, -1)), [T, 0] * 400, [0] * 300 + [T] * 300 + [0] * 300 + [T]]
+    for off in lists:
+        o = torch.tensor(off, dtype=torch.int32, device=dev)
+        for fill in (0xFF, 0x5A):
+            counts = _guarded_loss(m, l, ids, o, fill)[1]
+            buf = torch.full((T + 2, 40), 7.0, device=dev)
+            m.router_balance_backward(l, counts, 2, 0.01, offsets=o, out=buf[1:T + 1])
+            assert (buf[0] == 7).all() and (buf[-1] == 7).all()
