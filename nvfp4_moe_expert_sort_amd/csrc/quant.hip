@@ -134,10 +134,17 @@ hipError_t launch_quant_rows(const uint16_t* x, int64_t rows, int64_t cols, int6
     // rows of up to 32, 16 or 8 groups.
     const int64_t groups = cols / 32;
     const int rpw = (cols % 32 != 0 || groups > 32) ? 1 : groups > 16 ? 2 : groups > 8 ? 4 : 8;
-    const int64_t blocks = (rows + 4 * rpw - 1) / (4 * rpw);
-    hipLaunchKernelGGL(quant_rows_kernel, dim3((unsigned)blocks), dim3(256), 0, stream, x, rows, cols, ld, codes,
-                       scales, g, gemm ? 1 : 0, round_up ? 1 : 0, rpw);
-    return hipGetLastError();
+    // Rows of a launch: it has fewer than 2^32 threads.  (Whole row tiles of the
+    // GEMM layout, which take as many bytes as the rows' of the logical one.)
+    constexpr int64_t kMost = 1 << 25;
+    for (int64_t r0 = 0; r0 < rows; r0 += kMost) {
+        const int64_t n = rows - r0 < kMost ? rows - r0 : kMost, blocks = (n + 4 * rpw - 1) / (4 * rpw);
+        hipLaunchKernelGGL(quant_rows_kernel, dim3((unsigned)blocks), dim3(256), 0, stream, x + r0 * ld, n, cols, ld,
+                           codes + r0 * cols / 2, scales + r0 * cols / 16, g + r0, gemm ? 1 : 0, round_up ? 1 : 0, rpw);
+        const hipError_t e = hipGetLastError();
+        if (e != hipSuccess) return e;
+    }
+    return hipSuccess;
 }
 
 hipError_t launch_quant_h(const uint16_t* h, int64_t rows_bound, int64_t I, const int32_t* expert_off, int32_t E,
