@@ -220,9 +220,15 @@ hipError_t launch_router(const uint16_t* x, int32_t T, int32_t H, const uint16_t
     if (T <= 0) return hipSuccess;
     hipError_t st = launch_router_scores(x, T, H, w, E, logits, stream);
     if (st != hipSuccess) return st;
-    hipLaunchKernelGGL(router_topk_kernel, dim3((unsigned)((T + kTopkWaves - 1) / kTopkWaves)), dim3(kTopkWaves * 64),
-                       0, stream, T, E, K, renorm ? 1 : 0, logits, ids, probs);
-    return hipGetLastError();
+    constexpr int32_t kMost = 1 << 25;  // tokens of a launch: it has fewer than 2^32 threads
+    for (int64_t t0 = 0; t0 < T; t0 += kMost) {
+        const int32_t n = (int32_t)(T - t0 < kMost ? T - t0 : kMost);
+        hipLaunchKernelGGL(router_topk_kernel, dim3((unsigned)((n + kTopkWaves - 1) / kTopkWaves)), dim3(kTopkWaves * 64),
+                           0, stream, n, E, K, renorm ? 1 : 0, logits + t0 * E, ids + t0 * K, probs + t0 * K);
+        st = hipGetLastError();
+        if (st != hipSuccess) return st;
+    }
+    return hipSuccess;
 }
 
 }  // namespace nvfp4

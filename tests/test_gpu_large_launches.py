@@ -39,3 +39,14 @@ def test_quantizer(gpu, layout):
         each, times, rest = b.numel(), rows // P, rows % P
         assert a.numel() == times * each + rest * (each // P)
         assert (a[:times * each].view(times, each) == b).all() and torch.equal(a[times * each:], b[:rest * (each // P)])
+
+
+def test_router_topk(gpu):
+    """A wavefront a token."""
+    import torch
+    m, dev = gpu
+    P, T, H, E, k = 1 << 20, (1 << 26) + 5, 16, 4, 2
+    few, w = torch.randn(P, H, device=dev).to(torch.bfloat16), torch.randn(E, H, device=dev).to(torch.bfloat16)
+    want, got = m.router_topk(few, w, k), m.router_topk(_repeated(few, T), w, k)
+    for a, b in zip(got, want):
+        assert torch.equal(a, _repeated(b, T))
