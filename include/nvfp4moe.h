@@ -94,7 +94,8 @@ typedef struct {
     int32_t inter;       /* I: expert intermediate size, multiple of 128 */
     int32_t n_experts;   /* E: 1..1024 */
     int32_t top_k;       /* K: 1..n_experts (and <= 32) */
-    int32_t max_tokens;  /* bound on T; sizes the workspace (static capacity) */
+    int32_t max_tokens;  /* bound on T; sizes the workspace (static capacity).  Calls take T < 2^24, the
+                            backward also T * K + 32 E < 2^26 (else NVFP4_E_SHAPE) */
     int32_t scale_round; /* NVFP4_SCALE_RU or NVFP4_SCALE_RNE */
 } nvfp4moe_config;
 

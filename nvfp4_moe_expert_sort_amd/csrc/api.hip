@@ -39,6 +39,11 @@ bool cfg_ok(const nvfp4moe_config* c) {
     return true;
 }
 
+// A workgroup of 256 threads a token (the combine), and a wavefront a sorted row
+// (the SwiGLU's backward), where a launch has fewer than 2^32 threads.
+constexpr int32_t kMostTokens = 1 << 24;
+constexpr int64_t kMostBackwardRows = (int64_t)1 << 26;
+
 struct Layout {
     nvfp4moe_ws_layout pub;
     size_t blk_err, blk_counts, mtiles, mtiles_even, n_mtiles, row_prob, xq_codes, xq_scales, gx;
@@ -263,6 +268,7 @@ int forward_impl(const nvfp4moe_config* cfg, const uint16_t* x, int32_t T, const
     if (capacity != 0 && !capacity_ok(cfg, capacity)) return NVFP4_E_SHAPE;
     if (T < 0) return NVFP4_E_SHAPE;
     if (T > cfg->max_tokens) return NVFP4_E_CAPACITY;
+    if (T >= kMostTokens) return NVFP4_E_SHAPE;
     const int64_t E = cfg->n_experts, K = cfg->top_k, H = cfg->hidden, I = cfg->inter;
     if (!W1q || !W2q) return NVFP4_E_NULL;
     if (!qt_ok(W1q, E, 2 * I, H) || !qt_ok(W2q, E, H, I)) return NVFP4_E_SHAPE;
@@ -529,6 +535,8 @@ int nvfp4moe_moe_expert_backward(const nvfp4moe_config* cfg, const uint16_t* x, 
     if (!cfg_ok(cfg)) return NVFP4_E_SHAPE;
     if (T < 0) return NVFP4_E_SHAPE;
     if (T > cfg->max_tokens) return NVFP4_E_CAPACITY;
+    if (T >= kMostTokens || (int64_t)T * cfg->top_k + (int64_t)cfg->n_experts * kMAlign >= kMostBackwardRows)
+        return NVFP4_E_SHAPE;
     const Layout L = make_layout(cfg);
     if (y1_rows < L.pub.rows_cap) return NVFP4_E_SHAPE;
     if (!fwd_workspace || !workspace) return NVFP4_E_NULL;

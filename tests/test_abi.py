@@ -229,3 +229,27 @@ def test_selftest_argument_checks(m):
                                                   rep, None) == 2
     assert lib.nvfp4moe_selftest_batch_invariance(ctypes.byref(cfg), ctypes.byref(W), ctypes.byref(W), 1, 4, 65,
                                                   0, rep, None) == 5
+
+
+def test_more_tokens_than_a_launch_has_threads_for(m):
+    """The forward's combine takes a workgroup a token, the backward a wavefront a row besides: from 2^32 threads on
+    HIP launches nothing and reports no error, so such calls are refused."""
+    lib = m.lib()
+    fake = ctypes.c_void_p(0x1000)  # never dereferenced: validation fails first
+    W1, W2 = m.QTensor(0x1000, 0x1000, 0x1000, 8, 256, 128, m.LAYOUT_GEMM), m.QTensor(0x1000, 0x1000, 0x1000, 8, 128, 128, m.LAYOUT_GEMM)
+
+    def forward(T):  # (the last check that a call with these pointers passes is that of the workspace's alignment)
+        cfg = m.make_config(128, 128, 8, 1, 1 << 25)
+        return lib.nvfp4moe_moe_expert_forward(ctypes.byref(cfg), fake, T, fake, fake, ctypes.byref(W1), ctypes.byref(W2), fake,
+                                               ctypes.c_void_p(0x1010), m.workspace_bytes(cfg), None)
+
+    def backward(T, K):
+        cfg = m.make_config(128, 128, 8, K, 1 << 25)
+        return lib.nvfp4moe_moe_expert_backward(
+            ctypes.byref(cfg), fake, T, fake, fake, fake, int(m.workspace_layout(cfg).rows_cap), ctypes.c_void_p(0x1010),
+            m.workspace_bytes(cfg), fake, fake, fake, fake, fake, fake,
+            lib.nvfp4moe_backward_workspace_bytes(ctypes.byref(cfg)), None)
+
+    assert forward((1 << 24) - 1) == 3 and forward(1 << 24) == 2
+    assert backward((1 << 24) - 1, 1) == 3 and backward(1 << 24, 1) == 2
+    assert backward((1 << 23) - 32, 8) == 2 and backward((1 << 23) - 33, 8) == 3
