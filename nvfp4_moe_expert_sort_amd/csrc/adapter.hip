@@ -298,7 +298,7 @@ __global__ void __launch_bounds__(kPlanThreads) adapter_plan_kernel(AdapterPlan 
 // rows beside it.  V, an FP32 sum, is passed on as three BF16 values, which is all
 // of its 24 bits.  (With two, of the 20480 outputs of 5 rows some 20 lay one BF16
 // step off, and 2 at most so.  The third costs nothing measurable up to rank 32; 8192
-// rows of 4096 columns: rank 64 42.2 -> 43.0 us a call, rank 128 54 -> 58.)  At rank
+// rows of 4096 columns: rank 64 42.0 -> 43.2 us a call, rank 128 52 -> 58.)  At rank
 // 16 the second product has 32 inputs of 16 ranks of the first two pieces, and 32
 // of the third and zeros.
 //
@@ -315,7 +315,7 @@ __global__ void __launch_bounds__(kPlanThreads) adapter_plan_kernel(AdapterPlan 
 // weights' gradients.
 // kSmall: at most 512 rows, without a plan: every workgroup groups them itself.
 // The gradient's A and B, which are copies anyway, come from rank 33 on as the
-// products' operands (adapter_pack_kernel) and need not be turned over: 69
+// products' operands (pack_adapters) and need not be turned over: 69
 // against 92 us at 8192 rows, rank 64 and 4096 columns; at rank 16, where the
 // second product's would be twice as long, 88 against 79 us for 128 experts (both
 // before the last tiles were shared out).  (A forward pass that packs first gains
@@ -323,10 +323,10 @@ __global__ void __launch_bounds__(kPlanThreads) adapter_plan_kernel(AdapterPlan 
 //
 // Bound by memory: 8192 rows, rank 16, 4096 columns, 201 MB 34 us where a part is
 // in the last-level cache, 48 from memory (4.2 TB/s); 128 experts' 335 MB 59 us
-// (5.7 TB/s); rank 64 gradients, 201 MB and 6 of operands, 45 us in 256 tiles.
+// (5.5 TB/s); rank 64 gradients, 201 MB and 6 of operands, 46 us in 256 tiles.
 // At high ranks by the adapters too, which every tile reads through L2 (rank 128:
 // 2 MB for 0.8 of rows).  Few tiles are a chain: two products of 8 steps a
-// wavefront, 1 to 1.5 us each (rank 64, 130 tiles: 25 us).
+// wavefront, 1 to 1.5 us each (rank 64, 130 tiles: 27 us).
 template <int RB, int MB, bool kGrad, bool kBase, bool kSmall>
 __global__ void __launch_bounds__(kAdWaves * 64, RB < 4 || (RB == 4 && kGrad) ? 4 : 2) adapter_kernel(AdapterParams P) {
     constexpr bool kPacked = kGrad && RB >= 4;
@@ -906,10 +906,10 @@ hipError_t launch_adapter_plan(AdapterPlan P, const AdapterPack* pack, hipStream
 
 // Rows of a forward tile.  Up to rank 16 always 16 rows, of which a CU holds two
 // tiles.  Above, 16 rows are ahead by some where each CU has one tile at most
-// (600 rows of 4096 columns: rank 64 17.8 against 19.6 us, rank 128 24.6 against
-// 27.2; 4000 rows 28.8 against 29.4 and 39.4 against 38.2), and 32 read the adapters
-// half as often (16384 rows: rank 32 89 against 75 us, rank 64 129 against 95,
-// rank 128 173 against 120).
+// (600 rows of 4096 columns: rank 32 14.5 against 15.6 us, rank 64 18.4 against 20.4,
+// rank 128 24.8 against 27.9; near the border, 4000 rows, 25.0 against 24.1, 30.3
+// against 30.7 and 41.4 against 42.0), and 32 read the adapters half as often (16384
+// rows: rank 32 88 against 74 us, rank 64 128 against 97, rank 128 185 against 130).
 int adapter_tile(int32_t R, int64_t M, int64_t n) { return R <= 16 || M / 16 + n + 1 <= 256 ? 16 : 32; }
 
 namespace {
@@ -972,6 +972,12 @@ AdapterSplit adapter_split(int64_t M, int32_t R, int64_t K, int64_t N, int64_t n
         // each, while every CU has a workgroup at most: 1021 rows of one adapter, 2048 x
         // 4096, 7.1 us a launch and by 4 wavefronts 9.2; of 8 adapters 7.1 and 4.7, of 64
         // 32 and 12.
+        // All three launches with one chunk an adapter and with several, 2048 x 4096:
+        // 1000 rows of one adapter 25.6 against 29.3 us, of 8 24.1 and 25.8, of 64 38.3
+        // and 41.2.  (2000 rows in one chunk of 2048 would still gain: 33.4 against 36.2,
+        // 29.1 and 33.0, 40.4 and 43.0.)  From rank 24 on the steps of one chunk are
+        // longer, and 1000 rows of one adapter lose: rank 64 48.5 against 42.4 us (rank 32
+        // 32.3 and 34.5; of 8 adapters 31.0 and 32.3, rank 64 40.4 and 42.0).
         if (n * slabs <= (int64_t)kCus) s.waves = 16;
         s.chunk = 1024;
         s.most = (int32_t)(M / 1024);

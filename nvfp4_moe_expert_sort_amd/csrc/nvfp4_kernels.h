@@ -186,7 +186,7 @@ struct AdapterPlan {  // rows grouped by adapter
 struct AdapterParams {
     const uint16_t* x;
     int64_t ldx;
-    const uint16_t* A;   // [n][R][K] (the gradient's: from adapter_pack_kernel)
+    const uint16_t* A;   // [n][R][K] (the gradient's: transposed copies, AdapterPack)
     const uint16_t* B;   // [n][N][R]
     int64_t units_a, units_b;  // the gradient's: 16-byte units of an adapter
     const float* scale;  // [n] or null
